@@ -58,7 +58,8 @@ def _size(rng, lo, hi, step):
     """A multiple of `step`, spread over the logarithm; half the time a multiple of 128 (the usual widths)."""
     v = _log(rng, lo, hi)
     s = 128 if rng.random() < 0.5 else step
-    return max(s, v // s * s)
+    v = max(s, v // s * s)
+    return v - s if v == 24 * 128 else v
 
 
 def draw(rng):
@@ -76,7 +77,7 @@ def draw(rng):
         E = _log(rng, 1, 256)
         N, K = _size(rng, 128, 7168, 32), _size(rng, 128, 7168, 32)
         if op != "fp4" and rng.random() < 0.5:
-            N, K = N + rng.choice([0, 8, 24]), K + rng.choice([0, 8, 24])
+            N, K = N + rng.choice([0, 8, 40]), K + rng.choice([0, 8, 40])
         R = _log(rng, 1, 38400)
         spread = rng.choice(["even", "zipf", "steps"])
         most = _sizes(dict(E=E, R=R, spread=spread)).max()
