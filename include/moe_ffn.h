@@ -95,6 +95,7 @@ typedef enum {
 typedef enum { MOE_W_MXFP8 = 0, MOE_W_AWQ4 = 1, MOE_W_NVFP4S = 3 } moe_wfmt_t;
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
 typedef enum { MOE_PATH_DECODE = 0, MOE_PATH_GROUPED = 1 } moe_path_t;
+typedef enum { MOE_FP4_NVFP4 = 0, MOE_FP4_MXFP4 = 1 } moe_fp4_t;
 
 /* One projection of all experts; see "Weight formats" above. */
 typedef struct {
@@ -464,6 +465,78 @@ moe_status_t moe_ffn_decode_noalloc(const void *x, int32_t xdt, int32_t M, int32
                                     const int32_t *topk_ids, const float *topk_w, int32_t k,
                                     const moe_weights_t *w13, const moe_weights_t *w2,
                                     void *y, int32_t ydt, int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------ ragged grouped products
+ * No counterpart on the pages: the experts' plain 16-bit products on rows
+ * grouped by expert, forward and both gradients, for layers that are trained
+ * or served unquantized.
+ *   offsets int32 [E + 1] (device): rows offsets[e] .. offsets[e+1] - 1 are
+ *           expert e's, offsets[0] = 0, never decreasing, offsets[E] <= R.  A
+ *           group may have any count, zero included.  Rows from offsets[E] on
+ *           are padding.  (moe_align_block_size with b = 1 orders the routes
+ *           this way; their counts per expert give the offsets.)  Offsets that
+ *           break this are clamped -- no access leaves its buffer -- and
+ *           reported as MOE_ERR_BOUNDS in dev_status[1]; rows that two groups
+ *           claim are then undefined.
+ *   x [R][K], dy [R][N], w [E][N][K] of dt (MOE_BF16 or MOE_FP16);
+ *   moe_grouped_mm:       y[r][n]     = sum_k x[r][k]  w[e][n][k]
+ *   moe_grouped_mm_dgrad: dx[r][k]    = sum_n dy[r][n] w[e][n][k]
+ *   moe_grouped_mm_wgrad: dw[e][n][k] = sum_r dy[r][n] x[r][k]  (+ dw with
+ *                         accumulate = 1; an expert without rows adds zero)
+ *   for the rows r of expert e.  y [R][N], dx [R][K] and dw [E][N][K] are of dt
+ *   or MOE_FP32; sums are FP32, rounded once; padding rows of y and dx are
+ *   set to zero.  A row's result does not depend on the other rows, and the
+ *   same call gives the same bits.  No workspace.
+ * R = 0 is a no-op for y and dx, and writes (or keeps) dw.
+ * Limits: N % 8 == 0, K % 8 == 0, E <= 1024 (MOE_ERR_UNSUPPORTED); tensors
+ * 16-byte aligned (MOE_ERR_INVALID_ARG). */
+moe_status_t moe_grouped_mm(const void *x, const void *w, int32_t dt, const int32_t *offsets, int32_t R, int32_t E,
+                            int32_t N, int32_t K, void *y, int32_t ydt, int32_t *dev_status, void *stream);
+moe_status_t moe_grouped_mm_dgrad(const void *dy, const void *w, int32_t dt, const int32_t *offsets, int32_t R,
+                                  int32_t E, int32_t N, int32_t K, void *dx, int32_t xdt, int32_t *dev_status,
+                                  void *stream);
+moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t dt, const int32_t *offsets, int32_t R,
+                                  int32_t E, int32_t N, int32_t K, void *dw, int32_t wdt, int32_t accumulate,
+                                  int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------- microscaled 4-bit floats
+ * No counterpart on the pages (their NVFP4 weights are paired-sparse): dense
+ * NVFP4 and MXFP4 rows, and the ragged grouped product on them.
+ *   q uint8 [rows][K/2]: E2M1 codes, element 2i in the low nibble of byte i;
+ *   s uint8 [rows][Ks], Ks = K / block rounded up to a multiple of 16 bytes
+ *     (moe_fp4_scale_cols), the rest of a row zero;
+ *   MOE_FP4_NVFP4: blocks of 16, S = UE4M3(binary32(amax * binary32(1 /
+ *     (6 alpha)))) (nearest even, at most 448), code = E2M1(binary32(v *
+ *     binary32(1 / binary32(alpha S)))) (nearest even, at most 6, sign kept;
+ *     magnitude 0 where S = 0); value = alpha * S * code.  alpha fp32
+ *     [groups] (device), one per rows / groups consecutive rows (1 for
+ *     activations, E for weights), each in 2^-100 .. 2^100 (or 0 over rows of
+ *     zeros), usually amax of the rows / 2688;
+ *   MOE_FP4_MXFP4: blocks of 32, X = floor(log2 amax) - 2 clamped to [-127,
+ *     127], byte X + 127, code = E2M1(v 2^-X); value = 2^X * code; alpha NULL.
+ *   A block that holds a NaN or an infinity gets the scale NaN (0x7F / 0xFF)
+ *   and zero codes: it reads back, and multiplies, as NaN.
+ *   v [rows][K] of vdt (MOE_FP32, MOE_BF16 or MOE_FP16; the values of
+ *   moe_fp4_dequantize are rounded to it once).
+ * Limits: K % 32 == 0, rows % groups == 0; tensors 16-byte aligned
+ * (MOE_ERR_INVALID_ARG).
+ *
+ * moe_grouped_mm_fp4: y[r][n] = x_alpha[0] * w_alpha[e] * sum over K of the
+ * scaled codes of row r of x and row n of w[e], on the 4-bit tensor cores;
+ * both operands of the same fmt.  x: xq [R][K/2], xs [R][Ks], x_alpha [1]; w:
+ * wq [E][N][K/2], ws [E][N][Ks], w_alpha [E] (NULL for MXFP4); offsets, rows
+ * and padding as moe_grouped_mm (E = 1: the dense product); y [R][N] MOE_BF16,
+ * MOE_FP16 or MOE_FP32.  Limits: N % 8 == 0, K % 32 == 0, E <= 1024
+ * (MOE_ERR_UNSUPPORTED); tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */
+moe_status_t moe_fp4_scale_cols(int32_t K, int32_t fmt, int32_t *cols);
+moe_status_t moe_fp4_quantize(const void *v, int32_t vdt, int64_t rows, int32_t K, int32_t fmt, const float *alpha,
+                              int64_t groups, uint8_t *q, uint8_t *s, void *stream);
+moe_status_t moe_fp4_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t fmt,
+                                const float *alpha, int64_t groups, void *v, int32_t vdt, void *stream);
+moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, const float *x_alpha, const uint8_t *wq,
+                                const uint8_t *ws, const float *w_alpha, int32_t fmt, const int32_t *offsets,
+                                int32_t R, int32_t E, int32_t N, int32_t K, void *y, int32_t ydt,
+                                int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

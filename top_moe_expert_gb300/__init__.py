@@ -28,6 +28,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
 MOE_W_MXFP8, MOE_W_AWQ4, MOE_W_NVFP4S = 0, 1, 3
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_PATH_DECODE, MOE_PATH_GROUPED = 0, 1
+MOE_FP4_NVFP4, MOE_FP4_MXFP4 = 0, 1
 
 _DT = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 
@@ -78,6 +79,13 @@ _PROTOS = {
     "moe_ffn_grouped_batched": (_I32, [_P, _I32, _I32, _I32, _P, _P, _I32, ctypes.POINTER(moe_weights_t),
                                        ctypes.POINTER(moe_weights_t), _P, _P, _P, _P, _P, _P, _I32, _I32, _P,
                                        _I32, _P, _SZ, _P, _P]),
+    "moe_grouped_mm": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P]),
+    "moe_grouped_mm_dgrad": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P]),
+    "moe_grouped_mm_wgrad": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _I32, _P, _P]),
+    "moe_fp4_scale_cols": (_I32, [_I32, _I32, _P]),
+    "moe_fp4_quantize": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _I64, _P, _P, _P]),
+    "moe_fp4_dequantize": (_I32, [_P, _P, _I64, _I32, _I32, _P, _I64, _P, _I32, _P]),
+    "moe_grouped_mm_fp4": (_I32, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P]),
 }
 
 
@@ -615,4 +623,205 @@ def moe_ffn_grouped(x, topk_ids, topk_w, w13: Weights, w2: Weights, sfa13, sfa2,
                                                  _ptr(sorted_ids), _ptr(expert_ids), _ptr(block_rows), _ptr(npp),
                                                  b, cap_rows, _ptr(y), _DT[y.dtype], _ptr(ws), _nbytes(ws),
                                                  _ptr(dev_status), _stream(stream, dev)), "moe_ffn_grouped_batched")
+    return y
+
+
+# ---------------------------------------------------------------- ragged grouped products
+
+_DT16 = (torch.bfloat16, torch.float16)
+
+
+def _groups(offsets, dev):
+    """Check the group offsets; returns the number of experts."""
+    _need(offsets, "offsets", _IDS, device=dev)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"offsets must be [E + 1], not {tuple(offsets.shape)}")
+    return offsets.numel() - 1
+
+
+def _rows2(t, name, dtypes, dev=None, cols=None):
+    _need(t, name, dtypes, device=dev)
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [R, {'.' if cols is None else cols}], not {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_dtype=None, y=None, dev_status=None,
+                   stream=None):
+    """y [R, N]: rows offsets[e] .. offsets[e+1] - 1 of x [R, K] times w[e]^T,
+    w [E, N, K] of x's type (bf16 or fp16); rows past offsets[E] give zeros.
+    out_dtype: x's type (default) or float32."""
+    R, K = _rows2(x, "x", _DT16)
+    dev = x.device
+    E = _groups(offsets, dev)
+    _need(w, "w", (x.dtype,), device=dev)
+    if w.dim() != 3 or w.shape[0] != E or w.shape[2] != K:
+        raise ValueError(f"w must be [E={E}, N, K={K}], not {tuple(w.shape)}")
+    N = w.shape[1]
+    y = y if y is not None else torch.empty((R, N), dtype=out_dtype or x.dtype, device=dev)
+    _need(y, "y", (x.dtype, torch.float32), (R, N), device=dev)
+    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
+    with _guard(dev):
+        _check(lib().moe_grouped_mm(_ptr(x), _ptr(w), _DT[x.dtype], _ptr(offsets), R, E, N, K, _ptr(y), _DT[y.dtype],
+                                    _ptr(dev_status), _stream(stream, dev)), "moe_grouped_mm")
+    return y
+
+
+def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_dtype=None, dx=None,
+                         dev_status=None, stream=None):
+    """dx [R, K], the gradient of moe_grouped_mm's x: rows of dy [R, N] times
+    their expert's w[e] [N, K]; rows past offsets[E] give zeros."""
+    R, N = _rows2(dy, "dy", _DT16)
+    dev = dy.device
+    E = _groups(offsets, dev)
+    _need(w, "w", (dy.dtype,), device=dev)
+    if w.dim() != 3 or w.shape[0] != E or w.shape[1] != N:
+        raise ValueError(f"w must be [E={E}, N={N}, K], not {tuple(w.shape)}")
+    K = w.shape[2]
+    dx = dx if dx is not None else torch.empty((R, K), dtype=out_dtype or dy.dtype, device=dev)
+    _need(dx, "dx", (dy.dtype, torch.float32), (R, K), device=dev)
+    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
+    with _guard(dev):
+        _check(lib().moe_grouped_mm_dgrad(_ptr(dy), _ptr(w), _DT[dy.dtype], _ptr(offsets), R, E, N, K, _ptr(dx),
+                                          _DT[dx.dtype], _ptr(dev_status), _stream(stream, dev)),
+               "moe_grouped_mm_dgrad")
+    return dx
+
+
+def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out_dtype=torch.float32, dw=None,
+                         accumulate: bool = False, dev_status=None, stream=None):
+    """dw [E, N, K], the gradient of moe_grouped_mm's w: over each expert's
+    rows the sum of dy [R, N] outer x [R, K].  accumulate adds it to the dw
+    given."""
+    R, N = _rows2(dy, "dy", _DT16)
+    dev = dy.device
+    _need(x, "x", (dy.dtype,), device=dev)
+    if x.dim() != 2 or x.shape[0] != R:
+        raise ValueError(f"x must be [R={R}, K], not {tuple(x.shape)}")
+    K = x.shape[1]
+    E = _groups(offsets, dev)
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs the dw to add to")
+    dw = dw if dw is not None else torch.empty((E, N, K), dtype=out_dtype, device=dev)
+    _need(dw, "dw", (dy.dtype, torch.float32), (E, N, K), device=dev)
+    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
+    with _guard(dev):
+        _check(lib().moe_grouped_mm_wgrad(_ptr(dy), _ptr(x), _DT[dy.dtype], _ptr(offsets), R, E, N, K, _ptr(dw),
+                                          _DT[dw.dtype], 1 if accumulate else 0, _ptr(dev_status), _stream(stream, dev)),
+               "moe_grouped_mm_wgrad")
+    return dw
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floats
+
+_FP4_BLOCK = {MOE_FP4_NVFP4: 16, MOE_FP4_MXFP4: 32}
+
+
+def moe_fp4_scale_cols(K: int, fmt: int) -> int:
+    """Scale bytes of a row of K elements (K / block rounded up to 16)."""
+    n = ctypes.c_int32()
+    _check(lib().moe_fp4_scale_cols(K, fmt, ctypes.byref(n)), "moe_fp4_scale_cols")
+    return n.value
+
+
+def _fp4_shape(K: int, fmt: int, what: str) -> int:
+    b = _FP4_BLOCK.get(fmt)
+    if b is None:
+        raise ValueError(f"{what}: unknown format {fmt}")
+    if K < 1 or K % 32:
+        raise ValueError(f"{what}: K = {K} is not a positive multiple of 32")
+    return (K // b + 15) // 16 * 16
+
+
+def _fp4_alpha(alpha, fmt, rows, dev):
+    """Check alpha ([groups] for NVFP4, None for MXFP4); returns groups."""
+    if fmt != MOE_FP4_NVFP4:
+        if alpha is not None:
+            raise ValueError("alpha is only for NVFP4")
+        return 1
+    _need(alpha, "alpha", _F32, min_numel=1, device=dev)
+    if rows % alpha.numel():
+        raise ValueError(f"alpha holds {alpha.numel()} entries, which do not divide the {rows} rows")
+    return alpha.numel()
+
+
+@dataclasses.dataclass(frozen=True)
+class Fp4:
+    """Rows in NVFP4 or MXFP4: q uint8 [..., K/2], s uint8 [..., Ks] and, for
+    NVFP4, alpha float32 (one for activations [R, .], one per expert for
+    weights [E, N, .]), as moe_fp4_quantize returns them.  Checked when the
+    object is made."""
+    fmt: int
+    q: torch.Tensor
+    s: torch.Tensor
+    alpha: torch.Tensor | None = None
+
+    def __post_init__(self):
+        q = _need(self.q, "fp4.q", _U8)
+        if q.dim() not in (2, 3):
+            raise ValueError(f"fp4.q must be [R, K/2] or [E, N, K/2], not {tuple(q.shape)}")
+        Ks = _fp4_shape(q.shape[-1] * 2, self.fmt, "fp4")
+        _need(self.s, "fp4.s", _U8, (*q.shape[:-1], Ks), device=q.device)
+        if self.fmt == MOE_FP4_NVFP4:
+            _need(self.alpha, "fp4.alpha", _F32, (q.shape[0] if q.dim() == 3 else 1,), device=q.device)
+        elif self.alpha is not None:
+            raise ValueError("fp4.alpha is only for NVFP4")
+
+
+def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stream=None):
+    """NVFP4 or MXFP4 codes and scales of v [..., K] (fp32, bf16 or fp16):
+    (q uint8 [..., K/2], s uint8 [..., Ks]).  alpha (NVFP4): float32 [groups],
+    each for an equal run of rows."""
+    _need(v, "v", tuple(_DT))
+    dev, K = v.device, v.shape[-1] if v.dim() else 0
+    Ks = _fp4_shape(K, fmt, "v")
+    rows = v.numel() // K
+    groups = _fp4_alpha(alpha, fmt, rows, dev)
+    q = q if q is not None else torch.empty((*v.shape[:-1], K // 2), dtype=torch.uint8, device=dev)
+    s = s if s is not None else torch.empty((*v.shape[:-1], Ks), dtype=torch.uint8, device=dev)
+    _need(q, "q", _U8, (*v.shape[:-1], K // 2), device=dev)
+    _need(s, "s", _U8, (*v.shape[:-1], Ks), device=dev)
+    with _guard(dev):
+        _check(lib().moe_fp4_quantize(_ptr(v), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, _ptr(q), _ptr(s),
+                                      _stream(stream, dev)), "moe_fp4_quantize")
+    return q, s
+
+
+def moe_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, fmt: int, alpha=None, out_dtype=torch.float32, v=None,
+                       stream=None):
+    """The values v [..., K] that codes and scales stand for."""
+    _need(q, "q", _U8)
+    dev, K = q.device, q.shape[-1] * 2 if q.dim() else 0
+    Ks = _fp4_shape(K, fmt, "q")
+    _need(s, "s", _U8, (*q.shape[:-1], Ks), device=dev)
+    rows = q.numel() // (K // 2)
+    groups = _fp4_alpha(alpha, fmt, rows, dev)
+    v = v if v is not None else torch.empty((*q.shape[:-1], K), dtype=out_dtype, device=dev)
+    _need(v, "v", tuple(_DT), (*q.shape[:-1], K), device=dev)
+    with _guard(dev):
+        _check(lib().moe_fp4_dequantize(_ptr(q), _ptr(s), rows, K, fmt, _ptr(alpha), groups, _ptr(v), _DT[v.dtype],
+                                        _stream(stream, dev)), "moe_fp4_dequantize")
+    return v
+
+
+def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bfloat16, y=None, dev_status=None,
+                       stream=None):
+    """y [R, N]: moe_grouped_mm on 4-bit operands, x [R, K] and w [E, N, K] of
+    the same format (offsets [0, R] with E = 1: the dense product)."""
+    dev = x.q.device
+    E = _groups(offsets, dev)
+    if x.q.dim() != 2 or w.q.dim() != 3 or x.fmt != w.fmt:
+        raise ValueError("x must be [R, K] and w [E, N, K] of one format")
+    if w.q.device != dev:
+        raise ValueError(f"w is on {w.q.device}; the call's tensors are on {dev}")
+    R, N, K = x.q.shape[0], w.q.shape[1], w.q.shape[2] * 2
+    if w.q.shape[0] != E or x.q.shape[1] * 2 != K:
+        raise ValueError(f"w is [{w.q.shape[0]}, {N}, {K}]; offsets are for {E} experts and x has K = {x.q.shape[1] * 2}")
+    y = y if y is not None else torch.empty((R, N), dtype=out_dtype, device=dev)
+    _need(y, "y", tuple(_DT), (R, N), device=dev)
+    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
+    with _guard(dev):
+        _check(lib().moe_grouped_mm_fp4(_ptr(x.q), _ptr(x.s), _ptr(x.alpha), _ptr(w.q), _ptr(w.s), _ptr(w.alpha), x.fmt,
+                                        _ptr(offsets), R, E, N, K, _ptr(y), _DT[y.dtype], _ptr(dev_status),
+                                        _stream(stream, dev)), "moe_grouped_mm_fp4")
     return y
