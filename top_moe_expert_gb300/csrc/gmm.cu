@@ -4,81 +4,420 @@
 //   dx[r][k]    = sum_n dy[r][n] w[e][n][k]     moe_grouped_mm_dgrad
 //   dw[e][n][k] = sum_r dy[r][n] x[r][k]        moe_grouped_mm_wgrad
 // for the rows r of expert e.  Sums are FP32, rounded once.
+//
+// One persistent kernel on the tensor cores (tcgen05 kind::f16), one CTA per
+// SM, two CTAs (a cluster) per 256 x 256 tile.  The left operand is the
+// expert's matrix (w, w^T, or dy^T), 128 of its rows per CTA; the rows of x or
+// dy -- or, for wgrad, the columns of x -- are the right operand's N, half of
+// them held by each CTA.  A group's last tile takes N down to the next 32, so
+// a group of few rows costs few columns of MMA, and a row's result is its own
+// column of the accumulator: what the other columns hold does not reach it.
+// Where an operand's contracted dimension is not its contiguous one (w^T, dy^T
+// and x of wgrad) the tile is loaded as it lies and the MMA reads it
+// MN-major; nothing is transposed in memory.
+//
+// wgrad contracts over the expert's rows, whose count is ragged: the rows of
+// the last step that belong to the next expert are zeroed in shared memory up
+// to the next 16 (both operands, so that a NaN there stays out) and the 16-row
+// MMA steps past them are left out.
+//
+// Roles: warp 0 loads (TMA, 128-byte swizzle, a ring of 6 stages of 64 along
+// the contraction), warp 1 of the pair's leader issues the MMAs into two
+// accumulators of 256 TMEM columns, warps 2..5 drain one while the next tile
+// fills the other, warp 6 zeroes wgrad's row tails.  Every wait is bounded; an
+// expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "attr.h"
 #include "common.cuh"
 #include "fp4.cuh"
+#include "gmm_internal.h"
 #include "ragged.cuh"
+#include "tc_pair.cuh"
 
 namespace moe {
 namespace gmm {
 
-constexpr int kT = 32;                  // tile side
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-// out[r][c] = sum_j a[r][j] * b(e, c, j); b(e, c, j) = w[e][c][j] (TRANS = 0, w
-// [E][C][J]) or w[e][j][c] (TRANS = 1, w [E][J][C]).  One block per (32
-// columns, expert) walks the expert's rows.
-template <typename T, typename YT, int TRANS>
-__global__ void __launch_bounds__(1024)
-rows_kernel(const T *__restrict__ a, const T *__restrict__ w, const int32_t *__restrict__ off, int R, int E, int C, int J,
-            YT *__restrict__ out, int32_t *dev_status)
+constexpr int kStages = 6;
+constexpr int kStageBytes = 32768;             // 128 x 64 of each operand, 16 bits
+constexpr int kThreads = 224;
+constexpr int kTileM = 256, kTileN = 256, kStep = 64;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct Args {
+    const int32_t *off;
+    void *out;
+    int32_t *dev_status;
+    int R, E;
+    int M;                     // rows of the left operand of one expert: N (fwd, wgrad) or K (dgrad)
+    int C;                     // wgrad: columns of dw (K)
+    int J;                     // fwd, dgrad: the contraction
+    int accumulate;
+    int bf16;
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages], tail[kStages], accf[2], acce[2];
+    uint32_t tmem;
+    int abort;
+    ragged::List list;
+};
+
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + static_cast<int>(sizeof(Shared));
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+struct Tile {
+    int e, m0, lo, rows;       // expert, first left row, the expert's rows
+    int n0, n;                 // first column (row of the group, or column of dw) and how many
+    int steps;
+};
+
+template <int OP>
+__device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, int n_mt, int n_nt)
 {
-    __shared__ float sa[kT][kT + 1], sb[kT][kT + 1];
-    const int e = blockIdx.y, c0 = blockIdx.x * kT, tx = threadIdx.x, ty = threadIdx.y;
-    int lo, hi;
-    ragged::group(off, e, R, lo, hi);
-    if (blockIdx.x == 0 && tx == 0 && ty == 0)
-        ragged::report_bad(off, E, R, e, dev_status);
-    const T *we = w + static_cast<int64_t>(e) * C * J;
-    for (int r0 = lo; r0 < hi; r0 += kT) {
-        float acc = 0.f;
-        for (int j0 = 0; j0 < J; j0 += kT) {
-            sa[ty][tx] = r0 + ty < hi && j0 + tx < J ? fp4::to_float(a[static_cast<int64_t>(r0 + ty) * J + j0 + tx]) : 0.f;
-            if (TRANS)
-                sb[ty][tx] = j0 + ty < J && c0 + tx < C ? fp4::to_float(we[static_cast<int64_t>(j0 + ty) * C + c0 + tx]) : 0.f;
-            else
-                sb[tx][ty] = j0 + tx < J && c0 + ty < C ? fp4::to_float(we[static_cast<int64_t>(c0 + ty) * J + j0 + tx]) : 0.f;
-            __syncthreads();
-            for (int j = 0; j < kT; ++j)
-                acc += sa[ty][j] * sb[j][tx];
-            __syncthreads();
+    Tile T;
+    int at;
+    if (OP == kWgrad) {
+        T.e = t / (n_mt * n_nt);
+        at = t - T.e * n_mt * n_nt;
+    } else {
+        T.e = ragged::expert_of(s.list, a.E, t);
+        at = t - s.list.tiles[T.e];
+    }
+    const int nt = at / n_mt;
+    T.m0 = (at - nt * n_mt) * kTileM;
+    T.lo = s.list.lo[T.e];
+    T.rows = s.list.rows[T.e];
+    T.n0 = nt * kTileN;
+    T.n = min(kTileN, (OP == kWgrad ? a.C : T.rows) - T.n0);
+    T.steps = ((OP == kWgrad ? T.rows : a.J) + kStep - 1) / kStep;
+    return T;
+}
+
+__device__ __forceinline__ int n_mma(int n) { return (n + 31) & ~31; }
+
+template <typename OT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (sizeof(OT) == 4) {
+        return 0;
+    } else if constexpr (std::is_same<OT, __half>::value) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// 32 accumulator columns (rows of y or dx) of this lane's output element:
+// neighbouring lanes exchange halves so that each stores two elements of one
+// row, 64 contiguous bytes per row and warp.
+template <typename OT>
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int64_t ld, int m, int M, int n, int lane)
+{
+    if constexpr (sizeof(OT) == 4) {
+        if (m < M) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (c < n)
+                    out[c * ld + m] = __uint_as_float(v[c]);
         }
-        if (r0 + ty < hi && c0 + tx < C)
-            out[static_cast<int64_t>(r0 + ty) * C + c0 + tx] = fp4::from_float<YT>(acc);
-    }
-    // rows outside every group
-    const int first = min(max(off[0], 0), R), last = max(min(off[E], R), 0);
-    if (c0 + tx < C) {
-        for (int r = e * kT + ty; r < first; r += gridDim.y * kT)
-            out[static_cast<int64_t>(r) * C + c0 + tx] = fp4::from_float<YT>(0.f);
-        for (int r = last + e * kT + ty; r < R; r += gridDim.y * kT)
-            out[static_cast<int64_t>(r) * C + c0 + tx] = fp4::from_float<YT>(0.f);
+    } else {
+        const int odd = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const uint32_t own = pack2<OT>(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+            const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+            if (m < M && c + odd < n)
+                *reinterpret_cast<uint32_t *>(out + (c + odd) * ld + (m & ~1)) = w;
+        }
     }
 }
 
-template <typename T, typename YT>
-__global__ void __launch_bounds__(1024)
-wgrad_kernel(const T *__restrict__ dy, const T *__restrict__ x, const int32_t *__restrict__ off, int R, int E, int N, int K,
-             YT *__restrict__ dw, int accumulate, int32_t *dev_status)
+// 32 accumulator columns (columns of dw) of this lane's row of dw; n % 8 == 0.
+template <typename OT>
+__device__ __forceinline__ void store_dw(const uint32_t (&v)[32], OT *out, int n, bool accumulate)
 {
-    __shared__ float sa[kT][kT + 1], sb[kT][kT + 1];
-    const int e = blockIdx.z, n0 = blockIdx.y * kT, k0 = blockIdx.x * kT, tx = threadIdx.x, ty = threadIdx.y;
-    int lo, hi;
-    ragged::group(off, e, R, lo, hi);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tx == 0 && ty == 0)
-        ragged::report_bad(off, E, R, e, dev_status);
-    float acc = 0.f;
-    for (int r0 = lo; r0 < hi; r0 += kT) {
-        sa[ty][tx] = r0 + ty < hi && n0 + tx < N ? fp4::to_float(dy[static_cast<int64_t>(r0 + ty) * N + n0 + tx]) : 0.f;
-        sb[ty][tx] = r0 + ty < hi && k0 + tx < K ? fp4::to_float(x[static_cast<int64_t>(r0 + ty) * K + k0 + tx]) : 0.f;
-        __syncthreads();
-        for (int j = 0; j < kT; ++j)
-            acc += sa[j][ty] * sb[j][tx];
-        __syncthreads();
-    }
-    if (n0 + ty < N && k0 + tx < K) {
-        YT *o = dw + (static_cast<int64_t>(e) * N + n0 + ty) * K + k0 + tx;
-        *o = fp4::from_float<YT>(accumulate ? acc + fp4::to_float(*o) : acc);
+    constexpr int kPer = 16 / sizeof(OT);
+#pragma unroll
+    for (int c = 0; c < 32; c += kPer) {
+        if (c < n) {
+            float f[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                f[i] = __uint_as_float(v[c + i]);
+            uint4 *p = reinterpret_cast<uint4 *>(out + c);
+            if (accumulate) {
+                const uint4 o = *p;
+                const OT *old = reinterpret_cast<const OT *>(&o);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    f[i] += fp4::to_float(old[i]);
+            }
+            uint4 w;
+            if constexpr (sizeof(OT) == 4)
+                w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            else
+                w = make_uint4(pack2<OT>(f[0], f[1]), pack2<OT>(f[2], f[3]), pack2<OT>(f[kPer - 4], f[kPer - 3]),
+                               pack2<OT>(f[kPer - 2], f[kPer - 1]));
+            *p = w;
+        }
     }
 }
+
+template <int OP, typename OT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmB16, const Args a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const uint32_t raw = tc::smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);      // the same offset in both CTAs
+    const uint32_t ring = tc::smem_u32(smem);
+    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes);
+    volatile int *abort = &s.abort;
+    auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(bar(s.full[i]), 2);          // one arrival per CTA's loader (or tail warp)
+            tc::mbar_init(bar(s.empty[i]), 1);
+            tc::mbar_init(bar(s.tail[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(s.accf[i]), 1);
+            tc::mbar_init(bar(s.acce[i]), 8);          // four drain warps of each CTA
+        }
+        s.abort = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tmA);
+        tc::prefetch_tmap(&tmB);
+        tc::prefetch_tmap(&tmB16);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc_pair(tc::smem_u32(&s.tmem), kTmemCols);
+        tc::tmem_relinquish_pair();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int n_mt = (a.M + kTileM - 1) / kTileM, n_nt = (a.C + kTileN - 1) / kTileN;
+    ragged::make_list(s.list, a.off, a.E, a.R, n_mt, kTileN);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    const int total = OP == kWgrad ? a.E * n_mt * n_nt : s.list.tiles[a.E];
+    const int cid = blockIdx.x >> 1, n_cl = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            for (int t = cid; t < total && !*abort; t += n_cl) {
+                const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+                const int m0 = T.m0 + 128 * rank, nh = n_mma(T.n) / 2;
+                const int tail = OP == kWgrad && (T.rows & 15) ? T.steps - 1 : -1;
+                uint32_t bytes = 16384;
+                if (OP == kWgrad)
+                    bytes += nh > 64 ? 16384 : 8192;
+                else
+                    bytes += nh > 64 ? 16384 : nh * 128;
+                for (int j = 0; j < T.steps; ++j, ++issued) {
+                    if (!tc::mbar_wait_cluster(bar(s.empty[st]), ph ^ 1u, abort, kWaitNs))
+                        break;
+                    const uint32_t sa = ring + st * kStageBytes, sb = sa + 16384;
+                    uint32_t fb;
+                    if (j == tail) {
+                        // this CTA's tail warp hears of the data first
+                        fb = bar(s.tail[st]);
+                        tc::mbar_arrive_expect_tx(fb, bytes);
+                    } else {
+                        fb = tc::mapa(bar(s.full[st]), 0);
+                        tc::mbar_arrive_expect_tx_cluster(fb, bytes);
+                    }
+                    if (OP == kFwd) {
+                        tc::tma_load_3d_pair(sa, &tmA, j * kStep, m0, T.e, fb);
+                    } else if (OP == kDgrad) {
+                        tc::tma_load_3d_pair(sa, &tmA, m0, j * kStep, T.e, fb);
+                        tc::tma_load_3d_pair(sa + 8192, &tmA, m0 + 64, j * kStep, T.e, fb);
+                    } else {
+                        tc::tma_load_2d_pair(sa, &tmA, m0, T.lo + j * kStep, fb);
+                        tc::tma_load_2d_pair(sa + 8192, &tmA, m0 + 64, T.lo + j * kStep, fb);
+                    }
+                    if (OP == kWgrad) {
+                        const int c0 = T.n0 + rank * nh;
+                        tc::tma_load_2d_pair(sb, &tmB, c0, T.lo + j * kStep, fb);
+                        if (nh > 64)
+                            tc::tma_load_2d_pair(sb + 8192, &tmB, c0 + 64, T.lo + j * kStep, fb);
+                    } else {
+                        const int r0 = T.lo + T.n0 + rank * nh;
+                        if (nh > 64)
+                            tc::tma_load_2d_pair(sb, &tmB, j * kStep, r0, fb);
+                        else
+                            for (int i = 0; i < nh; i += 16)
+                                tc::tma_load_2d_pair(sb + i * 128, &tmB16, j * kStep, r0 + i, fb);
+                    }
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // every copy has landed before the CTAs may finish (a wait that is
+            // over at once unless a role gave up)
+            if (rank == 0) {
+                volatile int never = 0;
+                for (int i = 1; i <= min(issued, kStages); ++i) {
+                    const int q = st - i < 0 ? st - i + kStages : st - i;
+                    tc::mbar_wait_cluster(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int st = 0, tix = 0;
+            uint32_t ph = 0;
+            for (int t = cid; t < total && !*abort; t += n_cl) {
+                const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+                if (T.steps == 0)
+                    continue;
+                const int buf = tix & 1;
+                if (!tc::mbar_wait_cluster(bar(s.acce[buf]), ((tix >> 1) & 1) ^ 1u, abort, kWaitNs))
+                    break;
+                tc::tc_fence_after();
+                ++tix;
+                const uint32_t acc = tmem + 256 * buf;
+                const uint32_t id = tc::idesc_f16_major(256, n_mma(T.n), a.bf16, OP != kFwd, OP == kWgrad);
+                for (int j = 0; j < T.steps; ++j) {
+                    if (!tc::mbar_wait_cluster(bar(s.full[st]), ph, abort, kWaitNs))
+                        break;
+                    tc::tc_fence_after();
+                    const uint32_t sa = ring + st * kStageBytes, sb = sa + 16384;
+                    const int nk = OP == kWgrad ? min(4, (T.rows - j * kStep + 15) >> 4) : 4;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (OP == kWgrad && kk >= nk)
+                            break;
+                        const uint64_t ad = OP == kFwd ? tc::smem_desc(sa + 32 * kk, 16, 1024, tc::kLayoutSw128)
+                                                       : tc::smem_desc(sa + 2048 * kk, 8192, 1024, tc::kLayoutSw128);
+                        const uint64_t bd = OP != kWgrad ? tc::smem_desc(sb + 32 * kk, 16, 1024, tc::kLayoutSw128)
+                                                         : tc::smem_desc(sb + 2048 * kk, 8192, 1024, tc::kLayoutSw128);
+                        tc::mma_f16_pair(acc, ad, bd, id, (j | kk) != 0 ? 1u : 0u);
+                    }
+                    tc::tc_commit_pair(bar(s.empty[st]));
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                tc::tc_commit_pair(bar(s.accf[buf]));
+            }
+        }
+    } else if (warp == 6) {
+        if (OP == kWgrad) {
+            // zero the last step's rows past the expert's, up to the next 16
+            int st = 0;
+            uint32_t phases = 0;
+            for (int t = cid; t < total; t += n_cl) {
+                const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+                if (T.steps == 0)
+                    continue;
+                const int q = (st + T.steps - 1) % kStages;
+                st = (st + T.steps) % kStages;
+                if (!(T.rows & 15))
+                    continue;
+                if (!tc::mbar_wait(bar(s.tail[q]), (phases >> q) & 1u, abort, kWaitNs))
+                    break;
+                phases ^= 1u << q;
+                const int r0 = T.rows - (T.steps - 1) * kStep, r1 = (r0 + 15) & ~15;
+                for (int i = lane; i < (r1 - r0) * 32; i += 32) {
+                    const int r = r0 + (i >> 5), part = (i >> 3) & 3, col = i & 7;     // 4 chunks of 64 x 128 bytes
+                    *reinterpret_cast<uint4 *>(smem + q * kStageBytes + part * 8192 + r * 128 + col * 16) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive_cluster(tc::mapa(bar(s.full[q]), 0));
+            }
+        }
+    } else {
+        const int q = warp & 3;                         // TMEM lane quadrant
+        int tix = 0;
+        OT *out = static_cast<OT *>(a.out);
+        for (int t = cid; t < total; t += n_cl) {
+            const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+            const int m = T.m0 + 128 * rank + 32 * q + lane;
+            const int buf = tix & 1;
+            if (T.steps) {
+                if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
+                    if (a.dev_status)
+                        atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
+                    break;
+                }
+                tc::tc_fence_after();
+                ++tix;
+            }
+            const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16);
+            for (int c0 = 0; c0 < T.n; c0 += 32) {
+                uint32_t v[32];
+                if (OP != kWgrad || T.steps) {
+                    tc::tmem_ld_32x32b_x32(acc + c0, v);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = 0;
+                }
+                if (OP == kWgrad) {
+                    if (m < a.M && (T.steps || !a.accumulate))
+                        store_dw<OT>(v, out + (static_cast<int64_t>(T.e) * a.M + m) * a.C + T.n0 + c0, T.n - c0, a.accumulate);
+                } else {
+                    store_rows<OT>(v, out + static_cast<int64_t>(T.lo + T.n0 + c0) * a.M, a.M, m, a.M, T.n - c0, lane);
+                }
+            }
+            if (T.steps) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive_cluster(tc::mapa(bar(s.acce[buf]), 0));
+            }
+        }
+        if (OP != kWgrad) {
+            // rows outside every group
+            const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);
+            const int64_t per = static_cast<int64_t>(a.M) * sizeof(OT) / 16;
+            uint4 *o = static_cast<uint4 *>(a.out);
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 64), by = static_cast<int64_t>(gridDim.x) * 128;
+            for (int64_t i = at; i < first * per; i += by)
+                o[i] = make_uint4(0, 0, 0, 0);
+            for (int64_t i = last * per + at; i < a.R * per; i += by)
+                o[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (blockIdx.x == 0)
+            for (int e = threadIdx.x - 64; e < a.E; e += 128)
+                ragged::report_bad(a.off, a.R, e, a.dev_status);
+    }
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();                                  // neither CTA ends while the other still reaches into it
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host
 
 static bool type16(int32_t dt) { return dt == MOE_BF16 || dt == MOE_FP16; }
 static bool out_type(int32_t t, int32_t dt) { return t == MOE_FP32 || t == dt; }
@@ -98,22 +437,43 @@ static moe_status_t check(const void *a, const void *b, const void *out, int32_t
     return MOE_OK;
 }
 
-template <int TRANS>
-static moe_status_t rows(const void *a, const void *w, int32_t dt, int32_t R, int32_t E, int32_t C, int32_t J,
+template <int OP, typename OT>
+static moe_status_t launch(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmB16, const Args &a,
+                           int64_t most_tiles, cudaStream_t s)
+{
+    auto k = gemm_kernel<OP, OT>;
+    static std::atomic<uint64_t> done{0};
+    if (!smem_attr_once(done, reinterpret_cast<const void *>(k), kSmemBytes))
+        return MOE_ERR_CUDA;
+    const int pairs = device_sm_count() / 2;
+    const int grid = 2 * static_cast<int>(most_tiles < pairs ? most_tiles : pairs);
+    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tmA, tmB, tmB16, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int OP>
+static moe_status_t launch_as(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmB16, const Args &a,
+                              int32_t odt, int64_t most_tiles, cudaStream_t s)
+{
+    if (odt == MOE_FP32)
+        return launch<OP, float>(tmA, tmB, tmB16, a, most_tiles, s);
+    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16>(tmA, tmB, tmB16, a, most_tiles, s)
+                           : launch<OP, __half>(tmA, tmB, tmB16, a, most_tiles, s);
+}
+
+// y or dx: C outputs per row from J contracted values; w [E][C][J] (OP kFwd)
+// or [E][J][C] (OP kDgrad).
+template <int OP>
+static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, int32_t E, int32_t C, int32_t J,
                          const int32_t *off, void *y, int32_t ydt, int32_t *dev_status, cudaStream_t s)
 {
-    const dim3 grid((C + kT - 1) / kT, E), block(kT, kT);
-    auto go = [&](auto t, auto u) {
-        using T = decltype(t);
-        using U = decltype(u);
-        rows_kernel<T, U, TRANS><<<grid, block, 0, s>>>(static_cast<const T *>(a), static_cast<const T *>(w), off, R, E, C, J,
-                                                        static_cast<U *>(y), dev_status);
-    };
-    if (dt == MOE_BF16)
-        ydt == MOE_FP32 ? go(__nv_bfloat16{}, float{}) : go(__nv_bfloat16{}, __nv_bfloat16{});
-    else
-        ydt == MOE_FP32 ? go(__half{}, float{}) : go(__half{}, __half{});
-    return launch_status();
+    const CUtensorMapDataType t = dt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tmA, tmB, tmB16;
+    const bool ok = OP == kFwd ? tmap_tile(&tmA, 3, t, 2, w, J, C, E, 64, 128) : tmap_tile(&tmA, 3, t, 2, w, C, J, E, 64, 64);
+    if (!ok || !tmap_tile(&tmB, 2, t, 2, x, J, R, 1, 64, 128) || !tmap_tile(&tmB16, 2, t, 2, x, J, R, 1, 64, 16))
+        return MOE_ERR_CUDA;
+    Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
+    const int64_t n_mt = (C + kTileM - 1) / kTileM;
+    return launch_as<OP>(tmA, tmB, tmB16, a, ydt, n_mt * (static_cast<int64_t>(R) / kTileN + (E < R ? E : R)), s);
 }
 
 }  // namespace gmm
@@ -128,7 +488,7 @@ MOE_API moe_status_t moe_grouped_mm(const void *x, const void *w, int32_t dt, co
     if (R == 0 && E >= 1 && N >= 1 && K >= 1)
         return type16(dt) && out_type(ydt, dt) ? MOE_OK : MOE_ERR_UNSUPPORTED;
     const moe_status_t st = check(x, w, y, dt, ydt, R, E, N, K, offsets);
-    return st != MOE_OK ? st : rows<0>(x, w, dt, R, E, N, K, offsets, y, ydt, dev_status, as_stream(stream));
+    return st != MOE_OK ? st : rows<kFwd>(x, w, dt, R, E, N, K, offsets, y, ydt, dev_status, as_stream(stream));
 }
 
 MOE_API moe_status_t moe_grouped_mm_dgrad(const void *dy, const void *w, int32_t dt, const int32_t *offsets, int32_t R,
@@ -138,7 +498,7 @@ MOE_API moe_status_t moe_grouped_mm_dgrad(const void *dy, const void *w, int32_t
     if (R == 0 && E >= 1 && N >= 1 && K >= 1)
         return type16(dt) && out_type(xdt, dt) ? MOE_OK : MOE_ERR_UNSUPPORTED;
     const moe_status_t st = check(dy, w, dx, dt, xdt, R, E, N, K, offsets);
-    return st != MOE_OK ? st : rows<1>(dy, w, dt, R, E, K, N, offsets, dx, xdt, dev_status, as_stream(stream));
+    return st != MOE_OK ? st : rows<kDgrad>(dy, w, dt, R, E, K, N, offsets, dx, xdt, dev_status, as_stream(stream));
 }
 
 MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t dt, const int32_t *offsets, int32_t R,
@@ -150,17 +510,15 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
     const moe_status_t st = check(dy, x, dw, dt, wdt, R, E, N, K, offsets);
     if (st != MOE_OK)
         return st;
-    const dim3 grid((K + kT - 1) / kT, (N + kT - 1) / kT, E), block(kT, kT);
-    auto go = [&](auto t, auto u) {
-        using T = decltype(t);
-        using U = decltype(u);
-        wgrad_kernel<T, U><<<grid, block, 0, as_stream(stream)>>>(static_cast<const T *>(dy), static_cast<const T *>(x),
-                                                                  offsets, R, E, N, K, static_cast<U *>(dw), accumulate,
-                                                                  dev_status);
-    };
-    if (dt == MOE_BF16)
-        wdt == MOE_FP32 ? go(__nv_bfloat16{}, float{}) : go(__nv_bfloat16{}, __nv_bfloat16{});
-    else
-        wdt == MOE_FP32 ? go(__half{}, float{}) : go(__half{}, __half{});
-    return launch_status();
+    const CUtensorMapDataType t = dt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tmA, tmB;
+    // without rows nothing is loaded; the maps still need an address
+    const void *ra = R ? dy : dw, *rb = R ? x : dw;
+    if (!tmap_tile(&tmA, 2, t, 2, ra, N, R ? R : 1, 1, 64, 64) || !tmap_tile(&tmB, 2, t, 2, rb, K, R ? R : 1, 1, 64, 64))
+        return MOE_ERR_CUDA;
+    Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
+    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + kTileN - 1) / kTileN);
+    if (tiles > INT32_MAX)
+        return MOE_ERR_UNSUPPORTED;
+    return launch_as<kWgrad>(tmA, tmB, tmB, a, wdt, tiles, as_stream(stream));
 }

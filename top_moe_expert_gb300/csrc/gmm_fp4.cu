@@ -31,7 +31,7 @@ rows_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs, cons
     int lo, hi;
     ragged::group(off, e, R, lo, hi);
     if (blockIdx.x == 0 && tx == 0 && ty == 0)
-        ragged::report_bad(off, E, R, e, dev_status);
+        ragged::report_bad(off, R, e, dev_status);
     const float f = FMT == MOE_FP4_NVFP4 ? *xa * wa[e] : 1.f;
     for (int r0 = lo; r0 < hi; r0 += kT) {
         float acc = 0.f;

@@ -1,0 +1,15 @@
+// gmm_internal.h -- pieces shared by the ragged grouped products.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+namespace moe {
+
+// Tensor map of rank 2 ([d1][d0]) or 3 ([d2][d1][d0]), densely packed, box b0 x
+// b1 (x 1) with the 128-byte swizzle (b0 elements are 128 bytes) or none.
+// Reads past d0 or d1 give zeros.
+bool tmap_tile(CUtensorMap *m, int rank, CUtensorMapDataType t, int elem_bytes, const void *base, uint64_t d0, uint64_t d1,
+             uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle = true);
+
+}  // namespace moe

@@ -19,10 +19,67 @@ __device__ __forceinline__ void group(const int32_t *__restrict__ off, int e, in
 }
 
 // Whether offsets are what the contract says; a call reports it once.
-__device__ __forceinline__ void report_bad(const int32_t *__restrict__ off, int E, int R, int e, int32_t *dev_status)
+__device__ __forceinline__ void report_bad(const int32_t *__restrict__ off, int R, int e, int32_t *dev_status)
 {
     if (dev_status && (off[e] < 0 || off[e] > off[e + 1] || off[e + 1] > R || (e == 0 && off[0] != 0)))
         atomicCAS(dev_status + 1, 0, static_cast<int32_t>(MOE_ERR_BOUNDS));
+}
+
+// The persistent kernels' list of tiles, in shared memory: expert e's first
+// row, row count, and the number of tiles before its own (mt tiles across for
+// every nt rows); tiles[E] is the total.  Every CTA makes its own.
+struct List {
+    int lo[kMaxExperts], rows[kMaxExperts], tiles[kMaxExperts + 1];
+    int warp_sum[32];
+};
+
+__device__ __forceinline__ void make_list(List &l, const int32_t *__restrict__ off, int E, int R, int mt, int nt)
+{
+    const int per = (E + blockDim.x - 1) / blockDim.x;
+    const int e0 = min(static_cast<int>(threadIdx.x) * per, E), e1 = min(e0 + per, E);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+        int lo, hi;
+        group(off, e, R, lo, hi);
+        l.lo[e] = lo;
+        l.rows[e] = hi - lo;
+        sum += mt * ((hi - lo + nt - 1) / nt);
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o)
+            run += v;
+    }
+    if (lane == 31)
+        l.warp_sum[warp] = run;
+    __syncthreads();
+    int at = run - sum;
+    for (int w = 0; w < warp; ++w)
+        at += l.warp_sum[w];
+    for (int e = e0; e < e1; ++e) {
+        l.tiles[e] = at;
+        at += mt * ((l.rows[e] + nt - 1) / nt);
+    }
+    if (e1 == E && e0 < E)
+        l.tiles[E] = at;
+    __syncthreads();
+}
+
+// The expert of tile t < tiles[E].
+__device__ __forceinline__ int expert_of(const List &l, int E, int t)
+{
+    int a = 0, b = E;                       // tiles[a] <= t < tiles[b]
+    while (b - a > 1) {
+        const int m = (a + b) >> 1;
+        if (l.tiles[m] <= t)
+            a = m;
+        else
+            b = m;
+    }
+    return a;
 }
 
 }  // namespace ragged
