@@ -42,8 +42,9 @@ namespace gmm {
 
 enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kStages = 6;
+constexpr int kStages = 6;                     // of the ring; wgrad has 5, and 8 staging tiles in the last one's place
 constexpr int kStageBytes = 32768;             // 128 x 64 of each operand, 16 bits
+constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
 constexpr int kThreads = 224;
 constexpr int kTileM = 256, kTileN = 256, kStep = 64;
 constexpr uint32_t kTmemCols = 512;
@@ -62,7 +63,7 @@ struct Args {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], tail[kStages], accf[2], acce[2];
+    uint64_t full[kStages], empty[kStages], tail[kStages], peer[kStages], accf[2], acce[2];
     uint32_t tmem;
     int abort;
     ragged::List list;
@@ -141,33 +142,30 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int
     }
 }
 
-// 32 accumulator columns (columns of dw) of this lane's row of dw; n % 8 == 0.
-template <typename OT>
-__device__ __forceinline__ void store_dw(const uint32_t (&v)[32], OT *out, int n, bool accumulate)
+// This lane's row of a 32 x 128-byte staging tile (128-byte swizzle): eight
+// 16-byte words, word u at u ^ (row % 8).
+__device__ __forceinline__ void stage_row(uint8_t *tile, int lane, const uint32_t (&w)[32])
 {
-    constexpr int kPer = 16 / sizeof(OT);
 #pragma unroll
-    for (int c = 0; c < 32; c += kPer) {
-        if (c < n) {
-            float f[kPer];
+    for (int u = 0; u < 8; ++u)
+        *reinterpret_cast<uint4 *>(tile + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+}
+
+// 32 FP32 sums v of this lane's row of dw plus the old elements, rounded once,
+// into w (n of them exist, n % 8 == 0).
+template <typename OT>
+__device__ __forceinline__ void add_row(const uint32_t (&v)[32], const OT *old, int n, uint32_t *w)
+{
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                f[i] = __uint_as_float(v[c + i]);
-            uint4 *p = reinterpret_cast<uint4 *>(out + c);
-            if (accumulate) {
-                const uint4 o = *p;
-                const OT *old = reinterpret_cast<const OT *>(&o);
+    for (int i = 0; i < 32; i += 8) {
+        if (i < n) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(old + i);
+            const OT *p = reinterpret_cast<const OT *>(&o);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    f[i] += fp4::to_float(old[i]);
-            }
-            uint4 w;
-            if constexpr (sizeof(OT) == 4)
-                w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-            else
-                w = make_uint4(pack2<OT>(f[0], f[1]), pack2<OT>(f[2], f[3]), pack2<OT>(f[kPer - 4], f[kPer - 3]),
-                               pack2<OT>(f[kPer - 2], f[kPer - 1]));
-            *p = w;
+            for (int j = 0; j < 8; j += 2)
+                w[(i + j) / 2] = pack2<OT>(__uint_as_float(v[i + j]) + fp4::to_float(p[j]),
+                                           __uint_as_float(v[i + j + 1]) + fp4::to_float(p[j + 1]));
         }
     }
 }
@@ -175,8 +173,9 @@ __device__ __forceinline__ void store_dw(const uint32_t (&v)[32], OT *out, int n
 template <int OP, typename OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-            const __grid_constant__ CUtensorMap tmB16, const Args a)
+            const __grid_constant__ CUtensorMap tmC, const Args a)
 {
+    // tmC: x or dy in boxes of 16 rows (fwd, dgrad); dw (wgrad)
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -185,13 +184,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const uint32_t ring = tc::smem_u32(smem);
     Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes);
     volatile int *abort = &s.abort;
+    constexpr int kRing = stages_of(OP);
     auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(bar(s.full[i]), 2);          // one arrival per CTA's loader (or tail warp)
+            tc::mbar_init(bar(s.full[i]), 1);          // the leader's loader or tail warp
             tc::mbar_init(bar(s.empty[i]), 1);
             tc::mbar_init(bar(s.tail[i]), 1);
+            tc::mbar_init(bar(s.peer[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(s.accf[i]), 1);
@@ -201,7 +202,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         tc::fence_mbar_init();
         tc::prefetch_tmap(&tmA);
         tc::prefetch_tmap(&tmB);
-        tc::prefetch_tmap(&tmB16);
+        tc::prefetch_tmap(&tmC);
     }
     if (warp == 1) {
         tc::tmem_alloc_pair(tc::smem_u32(&s.tmem), kTmemCols);
@@ -223,6 +224,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (lane == 0) {
             int st = 0, issued = 0;
             uint32_t ph = 0;
+            const uint32_t full_lead = tc::mapa(bar(s.full[0]), 0);
             for (int t = cid; t < total && !*abort; t += n_cl) {
                 const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
                 const int m0 = T.m0 + 128 * rank, nh = n_mma(T.n) / 2;
@@ -233,7 +235,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 else
                     bytes += nh > 64 ? 16384 : nh * 128;
                 for (int j = 0; j < T.steps; ++j, ++issued) {
-                    if (!tc::mbar_wait_cluster(bar(s.empty[st]), ph ^ 1u, abort, kWaitNs))
+                    if (!tc::mbar_wait(bar(s.empty[st]), ph ^ 1u, abort, kWaitNs))
                         break;
                     const uint32_t sa = ring + st * kStageBytes, sb = sa + 16384;
                     uint32_t fb;
@@ -242,8 +244,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         fb = bar(s.tail[st]);
                         tc::mbar_arrive_expect_tx(fb, bytes);
                     } else {
-                        fb = tc::mapa(bar(s.full[st]), 0);
-                        tc::mbar_arrive_expect_tx_cluster(fb, bytes);
+                        // the leader expects both CTAs' bytes; the other CTA
+                        // cannot be a phase ahead, as the leader's MMAs empty
+                        // the stage in both
+                        fb = full_lead + 8 * st;
+                        if (rank == 0)
+                            tc::mbar_arrive_expect_tx(fb, 2 * bytes);
                     }
                     if (OP == kFwd) {
                         tc::tma_load_3d_pair(sa, &tmA, j * kStep, m0, T.e, fb);
@@ -265,9 +271,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             tc::tma_load_2d_pair(sb, &tmB, j * kStep, r0, fb);
                         else
                             for (int i = 0; i < nh; i += 16)
-                                tc::tma_load_2d_pair(sb + i * 128, &tmB16, j * kStep, r0 + i, fb);
+                                tc::tma_load_2d_pair(sb + i * 128, &tmC, j * kStep, r0 + i, fb);
                     }
-                    if (++st == kStages) {
+                    if (++st == kRing) {
                         st = 0;
                         ph ^= 1u;
                     }
@@ -277,9 +283,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // over at once unless a role gave up)
             if (rank == 0) {
                 volatile int never = 0;
-                for (int i = 1; i <= min(issued, kStages); ++i) {
-                    const int q = st - i < 0 ? st - i + kStages : st - i;
-                    tc::mbar_wait_cluster(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
+                for (int i = 1; i <= min(issued, kRing); ++i) {
+                    const int q = st - i < 0 ? st - i + kRing : st - i;
+                    tc::mbar_wait(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
                 }
             }
         }
@@ -299,7 +305,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const uint32_t acc = tmem + 256 * buf;
                 const uint32_t id = tc::idesc_f16_major(256, n_mma(T.n), a.bf16, OP != kFwd, OP == kWgrad);
                 for (int j = 0; j < T.steps; ++j) {
-                    if (!tc::mbar_wait_cluster(bar(s.full[st]), ph, abort, kWaitNs))
+                    if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
                         break;
                     tc::tc_fence_after();
                     const uint32_t sa = ring + st * kStageBytes, sb = sa + 16384;
@@ -315,7 +321,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         tc::mma_f16_pair(acc, ad, bd, id, (j | kk) != 0 ? 1u : 0u);
                     }
                     tc::tc_commit_pair(bar(s.empty[st]));
-                    if (++st == kStages) {
+                    if (++st == kRing) {
                         st = 0;
                         ph ^= 1u;
                     }
@@ -332,13 +338,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
                 if (T.steps == 0)
                     continue;
-                const int q = (st + T.steps - 1) % kStages;
-                st = (st + T.steps) % kStages;
+                const int q = (st + T.steps - 1) % kRing;
+                st = (st + T.steps) % kRing;
                 if (!(T.rows & 15))
                     continue;
-                if (!tc::mbar_wait(bar(s.tail[q]), (phases >> q) & 1u, abort, kWaitNs))
-                    break;
+                const uint32_t ph = (phases >> q) & 1u;
                 phases ^= 1u << q;
+                if (!tc::mbar_wait(bar(s.tail[q]), ph, abort, kWaitNs))
+                    break;
                 const int r0 = T.rows - (T.steps - 1) * kStep, r1 = (r0 + 15) & ~15;
                 for (int i = lane; i < (r1 - r0) * 32; i += 32) {
                     const int r = r0 + (i >> 5), part = (i >> 3) & 3, col = i & 7;     // 4 chunks of 64 x 128 bytes
@@ -346,13 +353,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive_cluster(tc::mapa(bar(s.full[q]), 0));
+                if (rank == 0) {
+                    // both CTAs' tails are zeroed: the stage is full
+                    if (!tc::mbar_wait_cluster(bar(s.peer[q]), ph, abort, kWaitNs))
+                        break;
+                    if (lane == 0)
+                        tc::mbar_arrive(bar(s.full[q]));
+                } else if (lane == 0) {
+                    tc::mbar_arrive_cluster(tc::mapa(bar(s.peer[q]), 0));
+                }
             }
         }
     } else {
         const int q = warp & 3;                         // TMEM lane quadrant
-        int tix = 0;
+        int tix = 0, flip = 0;
         OT *out = static_cast<OT *>(a.out);
         for (int t = cid; t < total; t += n_cl) {
             const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
@@ -368,20 +382,57 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 ++tix;
             }
             const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16);
-            for (int c0 = 0; c0 < T.n; c0 += 32) {
-                uint32_t v[32];
-                if (OP != kWgrad || T.steps) {
+            if (OP == kWgrad) {
+                // 128 bytes of 32 rows of dw at a time go through a staging
+                // tile of this warp's and out by TMA, which cuts them at the
+                // expert's last row and column
+                constexpr int kCols = 128 / sizeof(OT);
+                if (T.steps || !a.accumulate) {
+                    for (int c0 = 0; c0 < T.n; c0 += kCols) {
+                        uint32_t w[32];
+                        if (T.steps == 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                w[i] = 0;
+                        } else if constexpr (sizeof(OT) == 4) {
+                            tc::tmem_ld_32x32b_x32(acc + c0, w);
+                            tc::tmem_ld_wait();
+                        } else {
+                            uint32_t v[32];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                tc::tmem_ld_32x32b_x32(acc + c0 + 32 * h, v);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    w[16 * h + i] = pack2<OT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                                if (a.accumulate && m < a.M)
+                                    add_row<OT>(v, out + (static_cast<int64_t>(T.e) * a.M + m) * a.C + T.n0 + c0 + 32 * h,
+                                                T.n - c0 - 32 * h, w + 16 * h);
+                            }
+                        }
+                        uint8_t *tile = smem + kRing * kStageBytes + (q * 2 + flip) * 4096;
+                        flip ^= 1;
+                        tc::bulk_wait_read<1>();            // the store of two chunks ago has read this tile
+                        __syncwarp();
+                        stage_row(tile, lane, w);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && m < a.M) {
+                            if (sizeof(OT) == 4 && a.accumulate)
+                                tc::tma_add_3d(&tmC, tc::smem_u32(tile), T.n0 + c0, m, T.e);
+                            else
+                                tc::tma_store_3d(&tmC, tc::smem_u32(tile), T.n0 + c0, m, T.e);
+                        }
+                        if (lane == 0)
+                            tc::bulk_commit();
+                    }
+                }
+            } else {
+                for (int c0 = 0; c0 < T.n; c0 += 32) {
+                    uint32_t v[32];
                     tc::tmem_ld_32x32b_x32(acc + c0, v);
                     tc::tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = 0;
-                }
-                if (OP == kWgrad) {
-                    if (m < a.M && (T.steps || !a.accumulate))
-                        store_dw<OT>(v, out + (static_cast<int64_t>(T.e) * a.M + m) * a.C + T.n0 + c0, T.n - c0, a.accumulate);
-                } else {
                     store_rows<OT>(v, out + static_cast<int64_t>(T.lo + T.n0 + c0) * a.M, a.M, m, a.M, T.n - c0, lane);
                 }
             }
@@ -392,6 +443,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tc::mbar_arrive_cluster(tc::mapa(bar(s.acce[buf]), 0));
             }
         }
+        if (OP == kWgrad)
+            tc::bulk_wait<0>();
         if (OP != kWgrad) {
             // rows outside every group
             const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);
@@ -511,14 +564,17 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
     if (st != MOE_OK)
         return st;
     const CUtensorMapDataType t = dt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tmA, tmB;
+    CUtensorMap tmA, tmB, tmC;
     // without rows nothing is loaded; the maps still need an address
     const void *ra = R ? dy : dw, *rb = R ? x : dw;
-    if (!tmap_tile(&tmA, 2, t, 2, ra, N, R ? R : 1, 1, 64, 64) || !tmap_tile(&tmB, 2, t, 2, rb, K, R ? R : 1, 1, 64, 64))
+    const CUtensorMapDataType to = wdt == MOE_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : t;
+    const int size = wdt == MOE_FP32 ? 4 : 2;
+    if (!tmap_tile(&tmA, 2, t, 2, ra, N, R ? R : 1, 1, 64, 64) || !tmap_tile(&tmB, 2, t, 2, rb, K, R ? R : 1, 1, 64, 64) ||
+        !tmap_tile(&tmC, 3, to, size, dw, K, N, E, 128 / size, 32))
         return MOE_ERR_CUDA;
     Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
     const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + kTileN - 1) / kTileN);
     if (tiles > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    return launch_as<kWgrad>(tmA, tmB, tmB, a, wdt, tiles, as_stream(stream));
+    return launch_as<kWgrad>(tmA, tmB, tmC, a, wdt, tiles, as_stream(stream));
 }
