@@ -28,11 +28,10 @@
 // expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "attr.h"
 #include "common.cuh"
 #include "fp4.cuh"
+#include "gmm_common.cuh"
 #include "gmm_internal.h"
 #include "ragged.cuh"
 #include "tc_pair.cuh"
@@ -101,46 +100,6 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, i
 }
 
 __device__ __forceinline__ int n_mma(int n) { return (n + 31) & ~31; }
-
-template <typename OT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    if constexpr (sizeof(OT) == 4) {
-        return 0;
-    } else if constexpr (std::is_same<OT, __half>::value) {
-        const __half2 h = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-
-// 32 accumulator columns (rows of y or dx) of this lane's output element:
-// neighbouring lanes exchange halves so that each stores two elements of one
-// row, 64 contiguous bytes per row and warp.
-template <typename OT>
-__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int64_t ld, int m, int M, int n, int lane)
-{
-    if constexpr (sizeof(OT) == 4) {
-        if (m < M) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-                if (c < n)
-                    out[c * ld + m] = __uint_as_float(v[c]);
-        }
-    } else {
-        const int odd = lane & 1;
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const uint32_t own = pack2<OT>(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-            const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-            if (m < M && c + odd < n)
-                *reinterpret_cast<uint32_t *>(out + (c + odd) * ld + (m & ~1)) = w;
-        }
-    }
-}
 
 // This lane's row of a 32 x 128-byte staging tile (128-byte swizzle): eight
 // 16-byte words, word u at u ^ (row % 8).

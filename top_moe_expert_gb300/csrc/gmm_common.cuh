@@ -1,0 +1,53 @@
+// gmm_common.cuh -- epilogue pieces of the ragged grouped products.
+#pragma once
+
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace moe {
+namespace gmm {
+
+template <typename OT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (sizeof(OT) == 4) {
+        return 0;
+    } else if constexpr (std::is_same<OT, __half>::value) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+// 32 accumulator columns (rows of y or dx) of this lane's output element:
+// neighbouring lanes exchange halves so that each stores two elements of one
+// row, 64 contiguous bytes per row and warp.  f: a factor of every element.
+template <typename OT>
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int64_t ld, int m, int M, int n, int lane,
+                                           float f = 1.f)
+{
+    if constexpr (sizeof(OT) == 4) {
+        if (m < M) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (c < n)
+                    out[c * ld + m] = __uint_as_float(v[c]) * f;
+        }
+    } else {
+        const int odd = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const uint32_t own = pack2<OT>(__uint_as_float(v[c]) * f, __uint_as_float(v[c + 1]) * f);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+            const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+            if (m < M && c + odd < n)
+                *reinterpret_cast<uint32_t *>(out + (c + odd) * ld + (m & ~1)) = w;
+        }
+    }
+}
+
+}  // namespace gmm
+}  // namespace moe

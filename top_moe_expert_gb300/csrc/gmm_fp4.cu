@@ -2,57 +2,363 @@
 // matrices, both NVFP4 or both MXFP4:
 //   y[r][n] = a_x a_w[e] sum over blocks of Sx Sw (sum in the block of cx cw)
 // with E2M1 codes c, a scale S per block along K and, for NVFP4, the two
-// constants.  Sums are FP32, rounded once.
+// constants.  Sums are FP32 on the tensor cores, rounded once.
+//
+// The structure of gmm.cu on tcgen05 kind::mxf4nvf4: one persistent kernel, two
+// CTAs per tile of 256 rows of w (128 each) x 192 rows of x (half each), a
+// stage of 256 along K (128 bytes of codes a row, 4 MMAs of 64).  192 rather
+// than 256 rows leave tensor memory for two accumulators and two stages of
+// scales.
+//
+// Scales lie in memory row by row, 16 bytes (NVFP4: 256 elements, MXFP4: 512)
+// at a time; the MMA wants them in tensor memory with a row's 4 bytes in lane
+// row % 32, column row / 32.  Groups start at any row, so that arrangement
+// cannot be made beforehand for x: the natural 16 bytes of each row come by
+// TMA, a warp turns them into the arrangement in place (a 4 x 4 transpose of
+// words in registers; each lane holds rows l, l + 32, l + 64, l + 96), and
+// tcgen05.cp copies it into every quadrant of tensor memory.  Both CTAs hold
+// the scales of all 192 rows of x and of their own 128 rows of w.
+//
+// Roles: warp 0 loads codes, warp 2 loads scales (a ring of its own, deeper),
+// warps 8..11 arrange them, each every fourth stage, warp 1 of the leader
+// issues copies and MMAs, warps 4..7 drain the accumulators.  Every wait is
+// bounded; an expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
+#include <cuda.h>
+
+#include "attr.h"
 #include "common.cuh"
 #include "fp4.cuh"
+#include "gmm_common.cuh"
+#include "gmm_internal.h"
 #include "ragged.cuh"
+#include "tc_pair.cuh"
 
 namespace moe {
 namespace gmm4 {
 
-constexpr int kT = 32;
+constexpr int kStages = 6, kScaleStages = 7;
+constexpr int kTileM = 256, kTileN = 192, kStep = 256;
+constexpr int kABytes = 128 * 128, kStageBytes = kABytes + kTileN / 2 * 128;
+constexpr int kSfBytes = 2048 + 4096;          // 128 rows of w, up to 256 of x
+constexpr int kThreads = 384, kArrange = 4;
+constexpr uint32_t kTmemCols = 512, kTmemScales = 2 * kTileN;    // accumulators first, then two stages of scales
+constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <int FMT>
-__device__ __forceinline__ float value(const uint8_t *q, const uint8_t *s, int64_t row, int K, int Ks, int k)
+struct Args {
+    const int32_t *off;
+    const float *xa, *wa;
+    void *out;
+    int32_t *dev_status;
+    int R, E, N, K;
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t sfull[kScaleStages], sready[kScaleStages], sempty[kScaleStages];
+    uint64_t accf[2], acce[2];
+    uint32_t tmem;
+    int abort;
+    ragged::List list;
+};
+
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScaleStages * kSfBytes + static_cast<int>(sizeof(Shared));
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+struct Tile {
+    int e, m0, r0, n;          // expert, first row of w, first row of x and how many
+};
+
+__device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, int n_mt)
 {
-    const float2 c = fp4::e2m1_values(q[row * (K / 2) + k / 2]);
-    return (k & 1 ? c.y : c.x) * fp4::scale_value<FMT>(s[row * Ks + k / fp4::block_of(FMT)]);
+    Tile T;
+    T.e = ragged::expert_of(s.list, a.E, t);
+    const int at = t - s.list.tiles[T.e], nt = at / n_mt;
+    T.m0 = (at - nt * n_mt) * kTileM;
+    T.r0 = s.list.lo[T.e] + nt * kTileN;
+    T.n = min(kTileN, s.list.rows[T.e] - nt * kTileN);
+    return T;
 }
 
-template <int FMT, typename YT>
-__global__ void __launch_bounds__(1024)
-rows_kernel(const uint8_t *__restrict__ xq, const uint8_t *__restrict__ xs, const float *__restrict__ xa,
-            const uint8_t *__restrict__ wq, const uint8_t *__restrict__ ws, const float *__restrict__ wa,
-            const int32_t *__restrict__ off, int R, int E, int N, int K, YT *__restrict__ y, int32_t *dev_status)
+__device__ __forceinline__ int n_mma(int n) { return (n + 31) & ~31; }
+
+template <int FMT, typename OT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmSA,
+            const __grid_constant__ CUtensorMap tmSB, const Args a)
 {
-    __shared__ float sa[kT][kT + 1], sb[kT][kT + 1];
-    const int e = blockIdx.y, c0 = blockIdx.x * kT, tx = threadIdx.x, ty = threadIdx.y;
-    const int Ks = fp4::scale_cols(K, FMT);
-    int lo, hi;
-    ragged::group(off, e, R, lo, hi);
-    if (blockIdx.x == 0 && tx == 0 && ty == 0)
-        ragged::report_bad(off, R, e, dev_status);
-    const float f = FMT == MOE_FP4_NVFP4 ? *xa * wa[e] : 1.f;
-    for (int r0 = lo; r0 < hi; r0 += kT) {
-        float acc = 0.f;
-        for (int j0 = 0; j0 < K; j0 += kT) {
-            sa[ty][tx] = r0 + ty < hi ? value<FMT>(xq, xs, r0 + ty, K, Ks, j0 + tx) : 0.f;
-            sb[tx][ty] = c0 + ty < N ? value<FMT>(wq, ws, static_cast<int64_t>(e) * N + c0 + ty, K, Ks, j0 + tx) : 0.f;
-            __syncthreads();
-            for (int j = 0; j < kT; ++j)
-                acc += sa[ty][j] * sb[j][tx];
-            __syncthreads();
+    constexpr bool kMx = FMT == MOE_FP4_MXFP4;
+    constexpr int kWords = kMx ? 2 : 4;                 // words of scales of a row in a stage
+    extern __shared__ uint8_t smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const uint32_t raw = tc::smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t *sf = smem + kStages * kStageBytes;
+    const uint32_t ring = tc::smem_u32(smem), sfring = tc::smem_u32(sf);
+    Shared &s = *reinterpret_cast<Shared *>(sf + kScaleStages * kSfBytes);
+    volatile int *abort = &s.abort;
+    auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(bar(s.full[i]), 1);
+            tc::mbar_init(bar(s.empty[i]), 1);
         }
-        if (r0 + ty < hi && c0 + tx < N)
-            y[static_cast<int64_t>(r0 + ty) * N + c0 + tx] = fp4::from_float<YT>(acc * f);
+        for (int i = 0; i < kScaleStages; ++i) {
+            tc::mbar_init(bar(s.sfull[i]), 1);
+            tc::mbar_init(bar(s.sready[i]), 2);          // one arranging warp of each CTA
+            tc::mbar_init(bar(s.sempty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar(s.accf[i]), 1);
+            tc::mbar_init(bar(s.acce[i]), 8);
+        }
+        s.abort = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tmA);
+        tc::prefetch_tmap(&tmB);
+        tc::prefetch_tmap(&tmB16);
+        tc::prefetch_tmap(&tmSA);
+        tc::prefetch_tmap(&tmSB);
     }
-    const int first = min(max(off[0], 0), R), last = max(min(off[E], R), 0);
-    if (c0 + tx < N) {
-        for (int r = e * kT + ty; r < first; r += gridDim.y * kT)
-            y[static_cast<int64_t>(r) * N + c0 + tx] = fp4::from_float<YT>(0.f);
-        for (int r = last + e * kT + ty; r < R; r += gridDim.y * kT)
-            y[static_cast<int64_t>(r) * N + c0 + tx] = fp4::from_float<YT>(0.f);
+    if (warp == 1) {
+        tc::tmem_alloc_pair(tc::smem_u32(&s.tmem), kTmemCols);
+        tc::tmem_relinquish_pair();
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int n_mt = (a.N + kTileM - 1) / kTileM, steps = (a.K + kStep - 1) / kStep;
+    ragged::make_list(s.list, a.off, a.E, a.R, n_mt, kTileN);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    const int total = s.list.tiles[a.E];
+    const int cid = blockIdx.x >> 1, n_cl = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            const uint32_t full_lead = tc::mapa(bar(s.full[0]), 0);
+            for (int t = cid; t < total && !*abort; t += n_cl) {
+                const Tile T = tile_of(a, s, t, n_mt);
+                const int m0 = T.m0 + 128 * rank, nh = n_mma(T.n) / 2, r0 = T.r0 + rank * nh;
+                const uint32_t bytes = kABytes + (nh > 48 ? kTileN / 2 : nh) * 128;
+                for (int j = 0; j < steps; ++j, ++issued) {
+                    if (!tc::mbar_wait(bar(s.empty[st]), ph ^ 1u, abort, kWaitNs))
+                        break;
+                    const uint32_t sa = ring + st * kStageBytes, sb = sa + kABytes, fb = full_lead + 8 * st;
+                    if (rank == 0)
+                        tc::mbar_arrive_expect_tx(fb, 2 * bytes);
+                    tc::tma_load_3d_pair(sa, &tmA, j * 128, m0, T.e, fb);
+                    if (nh > 48)
+                        tc::tma_load_2d_pair(sb, &tmB, j * 128, r0, fb);
+                    else
+                        for (int i = 0; i < nh; i += 16)
+                            tc::tma_load_2d_pair(sb + i * 128, &tmB16, j * 128, r0 + i, fb);
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (rank == 0) {
+                // every copy has landed before the CTAs may finish
+                volatile int never = 0;
+                for (int i = 1; i <= min(issued, kStages); ++i) {
+                    const int q = st - i < 0 ? st - i + kStages : st - i;
+                    tc::mbar_wait(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
+                }
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            for (int t = cid; t < total && !*abort; t += n_cl) {
+                const Tile T = tile_of(a, s, t, n_mt);
+                const int m0 = T.m0 + 128 * rank, n = n_mma(T.n);
+                for (int j = 0; j < steps; ++j, ++issued) {
+                    if (!tc::mbar_wait(bar(s.sempty[st]), ph ^ 1u, abort, kWaitNs))
+                        break;
+                    const uint32_t sa = sfring + st * kSfBytes, fb = bar(s.sfull[st]);
+                    const int x = kMx ? (j * 8) & ~15 : j * 16;
+                    tc::mbar_arrive_expect_tx(fb, 2048 + n * 16);
+                    tc::tma_load_3d(sa, &tmSA, x, m0, T.e, fb);
+                    for (int i = 0; i < n; i += 32)
+                        tc::tma_load_2d(sa + 2048 + i * 16, &tmSB, x, T.r0 + i, fb);
+                    if (++st == kScaleStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            volatile int never = 0;
+            for (int i = 1; i <= min(issued, kScaleStages); ++i) {
+                const int q = st - i < 0 ? st - i + kScaleStages : st - i;
+                tc::mbar_wait(bar(s.sfull[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int st = 0, sst = 0, tix = 0, g = 0;
+            uint32_t ph = 0, sph = 0;
+            for (int t = cid; t < total && !*abort; t += n_cl, ++tix) {
+                const Tile T = tile_of(a, s, t, n_mt);
+                const int buf = tix & 1, n = n_mma(T.n);
+                if (!tc::mbar_wait_cluster(bar(s.acce[buf]), ((tix >> 1) & 1) ^ 1u, abort, kWaitNs))
+                    break;
+                tc::tc_fence_after();
+                const uint32_t acc = tmem + kTileN * buf;
+                const uint32_t id0 = tc::idesc_fp4(256, n, kMx, 0), id1 = kMx ? tc::idesc_fp4(256, n, kMx, 2) : id0;
+                for (int j = 0; j < steps; ++j, ++g) {
+                    if (!tc::mbar_wait(bar(s.sready[sst]), sph, abort, kWaitNs) ||
+                        !tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
+                        break;
+                    tc::tc_fence_after();
+                    const uint32_t sa = ring + st * kStageBytes, sb = sa + kABytes;
+                    const uint32_t sf0 = sfring + sst * kSfBytes;
+                    const uint32_t ta = tmem + kTmemScales + (g & 1) * 48, tb = ta + 16;
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        tc::tc_cp_32x128b_x4_pair(ta + 4 * w, tc::smem_desc(sf0 + 512 * w, 0, 128, tc::kLayoutNone));
+                        tc::tc_cp_32x128b_x4_pair(tb + 8 * w, tc::smem_desc(sf0 + 2048 + 512 * w, 0, 128, tc::kLayoutNone));
+                        if (n > 128)
+                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, tc::smem_desc(sf0 + 4096 + 512 * w, 0, 128, tc::kLayoutNone));
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t ad = tc::smem_desc(sa + 32 * kk, 16, 1024, tc::kLayoutSw128);
+                        const uint64_t bd = tc::smem_desc(sb + 32 * kk, 16, 1024, tc::kLayoutSw128);
+                        const int w = kMx ? kk >> 1 : kk;
+                        tc::mma_fp4_pair<kMx>(acc, ad, bd, kk & 1 ? id1 : id0, ta + 4 * w, tb + 8 * w, (j | kk) != 0 ? 1u : 0u);
+                    }
+                    tc::tc_commit_pair(bar(s.sempty[sst]));
+                    tc::tc_commit_pair(bar(s.empty[st]));
+                    if (++st == kStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                    if (++sst == kScaleStages) {
+                        sst = 0;
+                        sph ^= 1u;
+                    }
+                }
+                tc::tc_commit_pair(bar(s.accf[buf]));
+            }
+        }
+    } else if (warp >= 8) {
+        // arrange the scales of every kArrange-th stage
+        int g = 0;
+        const uint32_t ready_lead = tc::mapa(bar(s.sready[0]), 0);
+        for (int t = cid; t < total && !*abort; t += n_cl) {
+            const Tile T = tile_of(a, s, t, n_mt);
+            const int blocks = T.n > 128 ? 3 : 2;
+            for (int j = 0; j < steps; ++j, ++g) {
+                if ((g & (kArrange - 1)) != warp - 8)
+                    continue;
+                const int st = g % kScaleStages;
+                if (!tc::mbar_wait(bar(s.sfull[st]), (g / kScaleStages) & 1, abort, kWaitNs))
+                    break;
+                for (int b = 0; b < blocks; ++b) {
+                    uint4 *p = reinterpret_cast<uint4 *>(sf + st * kSfBytes + b * 2048) + lane;
+                    const uint4 r0 = p[0], r1 = p[32], r2 = p[64], r3 = p[96];
+                    __syncwarp();
+                    if (kMx) {
+                        const bool hi = j & 1;
+                        p[0] = hi ? make_uint4(r0.z, r1.z, r2.z, r3.z) : make_uint4(r0.x, r1.x, r2.x, r3.x);
+                        p[32] = hi ? make_uint4(r0.w, r1.w, r2.w, r3.w) : make_uint4(r0.y, r1.y, r2.y, r3.y);
+                    } else {
+                        p[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+                        p[32] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+                        p[64] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+                        p[96] = make_uint4(r0.w, r1.w, r2.w, r3.w);
+                    }
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0)
+                        tc::mbar_arrive(bar(s.sready[st]));
+                    else
+                        tc::mbar_arrive_cluster(ready_lead + 8 * st);
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3;                         // TMEM lane quadrant
+        int tix = 0;
+        OT *out = static_cast<OT *>(a.out);
+        for (int t = cid; t < total; t += n_cl, ++tix) {
+            const Tile T = tile_of(a, s, t, n_mt);
+            const int m = T.m0 + 128 * rank + 32 * q + lane, buf = tix & 1;
+            const float f = kMx ? 1.f : *a.xa * a.wa[T.e];
+            if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
+                if (a.dev_status)
+                    atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
+                break;
+            }
+            tc::tc_fence_after();
+            const uint32_t acc = tmem + kTileN * buf + (static_cast<uint32_t>(32 * q) << 16);
+            for (int c0 = 0; c0 < T.n; c0 += 32) {
+                uint32_t v[32];
+                tc::tmem_ld_32x32b_x32(acc + c0, v);
+                tc::tmem_ld_wait();
+                gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f);
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive_cluster(tc::mapa(bar(s.acce[buf]), 0));
+        }
+        // rows outside every group
+        const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);
+        const int64_t per = static_cast<int64_t>(a.N) * sizeof(OT) / 16;
+        uint4 *o = static_cast<uint4 *>(a.out);
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 128), by = static_cast<int64_t>(gridDim.x) * 128;
+        for (int64_t i = at; i < first * per; i += by)
+            o[i] = make_uint4(0, 0, 0, 0);
+        for (int64_t i = last * per + at; i < a.R * per; i += by)
+            o[i] = make_uint4(0, 0, 0, 0);
+        if (blockIdx.x == 0)
+            for (int e = threadIdx.x - 128; e < a.E; e += 128)
+                ragged::report_bad(a.off, a.R, e, a.dev_status);
+    }
+    __syncwarp();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();                                  // neither CTA ends while the other still reaches into it
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+template <int FMT, typename OT>
+static moe_status_t launch(const CUtensorMap (&tm)[5], const Args &a, cudaStream_t s)
+{
+    auto k = gemm_kernel<FMT, OT>;
+    static std::atomic<uint64_t> done{0};
+    if (!smem_attr_once(done, reinterpret_cast<const void *>(k), kSmemBytes))
+        return MOE_ERR_CUDA;
+    const int64_t most = static_cast<int64_t>((a.N + kTileM - 1) / kTileM) * (a.R / kTileN + (a.E < a.R ? a.E : a.R));
+    const int pairs = device_sm_count() / 2;
+    const int grid = 2 * static_cast<int>(most < pairs ? most : pairs);
+    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tm[0], tm[1], tm[2], tm[3], tm[4], a) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int FMT>
+static moe_status_t launch_as(const CUtensorMap (&tm)[5], const Args &a, int32_t ydt, cudaStream_t s)
+{
+    if (ydt == MOE_FP32)
+        return launch<FMT, float>(tm, a, s);
+    return ydt == MOE_BF16 ? launch<FMT, __nv_bfloat16>(tm, a, s) : launch<FMT, __half>(tm, a, s);
 }
 
 }  // namespace gmm4
@@ -77,18 +383,14 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
         (fmt == MOE_FP4_NVFP4) != (w_alpha != nullptr) || !aligned(xq, 16) || !aligned(xs, 16) || !aligned(wq, 16) ||
         !aligned(ws, 16) || !aligned(y, 16) || !aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
-    const dim3 grid((N + kT - 1) / kT, E), block(kT, kT);
-    auto go = [&](auto t) {
-        using T = decltype(t);
-        auto k = fmt == MOE_FP4_NVFP4 ? rows_kernel<MOE_FP4_NVFP4, T> : rows_kernel<MOE_FP4_MXFP4, T>;
-        k<<<grid, block, 0, as_stream(stream)>>>(xq, xs, x_alpha, wq, ws, w_alpha, offsets, R, E, N, K, static_cast<T *>(y),
-                                                 dev_status);
-    };
-    if (ydt == MOE_FP32)
-        go(float{});
-    else if (ydt == MOE_BF16)
-        go(__nv_bfloat16{});
-    else
-        go(__half{});
-    return launch_status();
+    const int Ks = fp4::scale_cols(K, fmt);
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    CUtensorMap tm[5];
+    if (!tmap_tile(&tm[0], 3, u8, 1, wq, K / 2, N, E, 128, 128) || !tmap_tile(&tm[1], 2, u8, 1, xq, K / 2, R, 1, 128, kTileN / 2) ||
+        !tmap_tile(&tm[2], 2, u8, 1, xq, K / 2, R, 1, 128, 16) || !tmap_tile(&tm[3], 3, u8, 1, ws, Ks, N, E, 16, 128, false) ||
+        !tmap_tile(&tm[4], 2, u8, 1, xs, Ks, R, 1, 16, 32, false))
+        return MOE_ERR_CUDA;
+    const Args a{offsets, x_alpha, w_alpha, y, dev_status, R, E, N, K};
+    return fmt == MOE_FP4_NVFP4 ? launch_as<MOE_FP4_NVFP4>(tm, a, ydt, as_stream(stream))
+                                : launch_as<MOE_FP4_MXFP4>(tm, a, ydt, as_stream(stream));
 }

@@ -114,6 +114,15 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 template <int N>
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory"); }
 
+// The same within this CTA.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols)
 {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -137,6 +146,44 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, ui
                  " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
                  ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
                  : "memory");
+}
+
+// Block-scaled 4-bit MMA, 64 along K: E2M1 operands, per row and column one
+// 32-bit word of scales in tensor memory (4 x UE4M3 of 16 elements, or two
+// E8M0 of 32 elements, picked by the descriptor's scale ids).
+template <bool MX>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    if constexpr (MX)
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+                     " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X"
+                     " [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                     ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+                     " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+                     " [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                     ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+                     : "memory");
+}
+
+// Instruction descriptor of kind::mxf4nvf4: E2M1 x E2M1 (format 1 at bits 7..9
+// and 10..11), both K-major, N >> 3 at bits 17..22, the scale type at bit 23
+// (0 UE4M3, 1 UE8M0), M >> 7 at bits 27..28, the scale ids of B (bits 4..5) and
+// A (bits 29..30), K = 64 (bit 31 clear).
+__device__ __forceinline__ uint32_t idesc_fp4(int M, int N, bool mx, int sf_id)
+{
+    return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (mx ? 1u << 23 : 0u) | (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(sf_id) << 29);
+}
+
+// tc_cp_32x128b_x4 in both CTAs, each from its own shared memory at the
+// descriptor's offset into its own tensor memory.
+__device__ __forceinline__ void tc_cp_32x128b_x4_pair(uint32_t taddr, uint64_t sdesc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Arrive on the barrier at this offset in both CTAs when the tcgen05
