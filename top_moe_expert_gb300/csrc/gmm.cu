@@ -180,7 +180,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int cid = blockIdx.x >> 1, n_cl = gridDim.x >> 1;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (tc::elect_one()) {
             int st = 0, issued = 0;
             uint32_t ph = 0;
             const uint32_t full_lead = tc::mapa(bar(s.full[0]), 0);
@@ -249,7 +249,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && tc::elect_one()) {
+            // descriptors of stage 0; a stage or step further adds to the
+            // address field, so that an MMA costs a few instructions to issue
+            const uint64_t a0 = OP == kFwd ? tc::smem_desc(ring, 16, 1024, tc::kLayoutSw128)
+                                           : tc::smem_desc(ring, 8192, 1024, tc::kLayoutSw128);
+            const uint64_t b0 = OP != kWgrad ? tc::smem_desc(ring + 16384, 16, 1024, tc::kLayoutSw128)
+                                             : tc::smem_desc(ring + 16384, 8192, 1024, tc::kLayoutSw128);
+            constexpr int kAStep = (OP == kFwd ? 32 : 2048) >> 4, kBStep = (OP != kWgrad ? 32 : 2048) >> 4;
             int st = 0, tix = 0;
             uint32_t ph = 0;
             for (int t = cid; t < total && !*abort; t += n_cl) {
@@ -267,18 +274,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
                         break;
                     tc::tc_fence_after();
-                    const uint32_t sa = ring + st * kStageBytes, sb = sa + 16384;
+                    const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
                     const int nk = OP == kWgrad ? min(4, (T.rows - j * kStep + 15) >> 4) : 4;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (OP == kWgrad && kk >= nk)
-                            break;
-                        const uint64_t ad = OP == kFwd ? tc::smem_desc(sa + 32 * kk, 16, 1024, tc::kLayoutSw128)
-                                                       : tc::smem_desc(sa + 2048 * kk, 8192, 1024, tc::kLayoutSw128);
-                        const uint64_t bd = OP != kWgrad ? tc::smem_desc(sb + 32 * kk, 16, 1024, tc::kLayoutSw128)
-                                                         : tc::smem_desc(sb + 2048 * kk, 8192, 1024, tc::kLayoutSw128);
-                        tc::mma_f16_pair(acc, ad, bd, id, (j | kk) != 0 ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (OP != kWgrad || kk < nk)
+                            tc::mma_f16_pair(acc, ad + kk * kAStep, bd + kk * kBStep, id, (j | kk) != 0 ? 1u : 0u);
                     tc::tc_commit_pair(bar(s.empty[st]));
                     if (++st == kRing) {
                         st = 0;

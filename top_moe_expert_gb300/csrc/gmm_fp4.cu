@@ -139,7 +139,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int cid = blockIdx.x >> 1, n_cl = gridDim.x >> 1;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (tc::elect_one()) {
             int st = 0, issued = 0;
             uint32_t ph = 0;
             const uint32_t full_lead = tc::mapa(bar(s.full[0]), 0);
@@ -175,7 +175,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         }
     } else if (warp == 2) {
-        if (lane == 0) {
+        if (tc::elect_one()) {
             int st = 0, issued = 0;
             uint32_t ph = 0;
             for (int t = cid; t < total && !*abort; t += n_cl) {
@@ -203,7 +203,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0 && tc::elect_one()) {
+            // descriptors of stage 0; a stage or step further adds to the
+            // address field (forming them anew costs more than the MMA takes)
+            const uint64_t a0 = tc::smem_desc(ring, 16, 1024, tc::kLayoutSw128);
+            const uint64_t b0 = tc::smem_desc(ring + kABytes, 16, 1024, tc::kLayoutSw128);
+            const uint64_t s0 = tc::smem_desc(sfring, 0, 128, tc::kLayoutNone);
             int st = 0, sst = 0, tix = 0, g = 0;
             uint32_t ph = 0, sph = 0;
             for (int t = cid; t < total && !*abort; t += n_cl, ++tix) {
@@ -219,22 +224,21 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         !tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
                         break;
                     tc::tc_fence_after();
-                    const uint32_t sa = ring + st * kStageBytes, sb = sa + kABytes;
-                    const uint32_t sf0 = sfring + sst * kSfBytes;
+                    const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
+                    const uint64_t sd = s0 + sst * (kSfBytes >> 4);
                     const uint32_t ta = tmem + kTmemScales + (g & 1) * 48, tb = ta + 16;
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
-                        tc::tc_cp_32x128b_x4_pair(ta + 4 * w, tc::smem_desc(sf0 + 512 * w, 0, 128, tc::kLayoutNone));
-                        tc::tc_cp_32x128b_x4_pair(tb + 8 * w, tc::smem_desc(sf0 + 2048 + 512 * w, 0, 128, tc::kLayoutNone));
+                        tc::tc_cp_32x128b_x4_pair(ta + 4 * w, sd + 32 * w);
+                        tc::tc_cp_32x128b_x4_pair(tb + 8 * w, sd + 128 + 32 * w);
                         if (n > 128)
-                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, tc::smem_desc(sf0 + 4096 + 512 * w, 0, 128, tc::kLayoutNone));
+                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, sd + 256 + 32 * w);
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ad = tc::smem_desc(sa + 32 * kk, 16, 1024, tc::kLayoutSw128);
-                        const uint64_t bd = tc::smem_desc(sb + 32 * kk, 16, 1024, tc::kLayoutSw128);
                         const int w = kMx ? kk >> 1 : kk;
-                        tc::mma_fp4_pair<kMx>(acc, ad, bd, kk & 1 ? id1 : id0, ta + 4 * w, tb + 8 * w, (j | kk) != 0 ? 1u : 0u);
+                        tc::mma_fp4_pair<kMx>(acc, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id1 : id0, ta + 4 * w, tb + 8 * w,
+                                              (j | kk) != 0 ? 1u : 0u);
                     }
                     tc::tc_commit_pair(bar(s.sempty[sst]));
                     tc::tc_commit_pair(bar(s.empty[st]));
