@@ -10,19 +10,21 @@
 // than 256 rows leave tensor memory for two accumulators and two stages of
 // scales.
 //
-// Scales lie in memory row by row, 16 bytes (NVFP4: 256 elements, MXFP4: 512)
-// at a time; the MMA wants them in tensor memory with a row's 4 bytes in lane
-// row % 32, column row / 32.  Groups start at any row, so that arrangement
-// cannot be made beforehand for x: the natural 16 bytes of each row come by
-// TMA, a warp turns them into the arrangement in place (a 4 x 4 transpose of
-// words in registers; each lane holds rows l, l + 32, l + 64, l + 96), and
-// tcgen05.cp copies it into every quadrant of tensor memory.  Both CTAs hold
-// the scales of all 192 rows of x and of their own 128 rows of w.
+// Scales lie in memory row by row; the MMA wants them in tensor memory with a
+// row's 4 bytes in lane row % 32, column row / 32.  Groups start at any row, so
+// that arrangement cannot be made beforehand for x: 64 natural bytes of each
+// row (a slot: 1024 elements of NVFP4, 2048 of MXFP4) come by TMA, a warp turns
+// them into the arrangement in place (a 4 x 4 transpose of words in registers;
+// a lane holds rows l, l + 32, l + 64, l + 96), and tcgen05.cp copies a stage's
+// part into every quadrant of tensor memory.  64 bytes rather than a stage's 16
+// because TMA is paid by the row, and because the leader hears of the other
+// CTA's slot by a cluster-scope arrival that takes several hundred cycles.
+// Both CTAs hold the scales of all 192 rows of x and of their own 128 of w.
 //
-// Roles: warp 0 loads codes, warp 2 loads scales (a ring of its own, deeper),
-// warps 8..11 arrange them, each every fourth stage, warp 1 of the leader
-// issues copies and MMAs, warps 4..7 drain the accumulators.  Every wait is
-// bounded; an expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
+// Roles: warp 0 loads codes, warp 2 loads scales, warps 8..10 arrange them (w,
+// the first 128 rows of x, the rest), warp 1 of the leader issues copies and
+// MMAs, warps 4..7 drain the accumulators.  Every wait is bounded; an expired
+// one is reported as MOE_ERR_TIMEOUT in dev_status[1].
 #include <cuda.h>
 
 #include "attr.h"
@@ -36,11 +38,11 @@
 namespace moe {
 namespace gmm4 {
 
-constexpr int kStages = 6, kScaleStages = 7;
+constexpr int kStages = 5, kSlots = 3;
 constexpr int kTileM = 256, kTileN = 192, kStep = 256;
 constexpr int kABytes = 128 * 128, kStageBytes = kABytes + kTileN / 2 * 128;
-constexpr int kSfBytes = 2048 + 4096;          // 128 rows of w, up to 256 of x
-constexpr int kThreads = 384, kArrange = 4;
+constexpr int kBlockBytes = 128 * 64, kSlotBytes = 3 * kBlockBytes;   // scales of 128 rows of w, 2 x 128 of x
+constexpr int kThreads = 352;
 constexpr uint32_t kTmemCols = 512, kTmemScales = 2 * kTileN;    // accumulators first, then two stages of scales
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -54,14 +56,14 @@ struct Args {
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];
-    uint64_t sfull[kScaleStages], sready[kScaleStages], sempty[kScaleStages];
+    uint64_t sfull[kSlots], sready[kSlots], sempty[kSlots];
     uint64_t accf[2], acce[2];
     uint32_t tmem;
     int abort;
     ragged::List list;
 };
 
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScaleStages * kSfBytes + static_cast<int>(sizeof(Shared));
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSlots * kSlotBytes + static_cast<int>(sizeof(Shared));
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct Tile {
@@ -89,6 +91,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 {
     constexpr bool kMx = FMT == MOE_FP4_MXFP4;
     constexpr int kWords = kMx ? 2 : 4;                 // words of scales of a row in a stage
+    constexpr int kSlotSteps = 16 / kWords;             // stages in a slot
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -96,7 +99,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint8_t *sf = smem + kStages * kStageBytes;
     const uint32_t ring = tc::smem_u32(smem), sfring = tc::smem_u32(sf);
-    Shared &s = *reinterpret_cast<Shared *>(sf + kScaleStages * kSfBytes);
+    Shared &s = *reinterpret_cast<Shared *>(sf + kSlots * kSlotBytes);
     volatile int *abort = &s.abort;
     auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
 
@@ -105,9 +108,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             tc::mbar_init(bar(s.full[i]), 1);
             tc::mbar_init(bar(s.empty[i]), 1);
         }
-        for (int i = 0; i < kScaleStages; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             tc::mbar_init(bar(s.sfull[i]), 1);
-            tc::mbar_init(bar(s.sready[i]), 2);          // one arranging warp of each CTA
+            tc::mbar_init(bar(s.sready[i]), 6);          // three arranging warps of each CTA
             tc::mbar_init(bar(s.sempty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -129,6 +132,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int n_mt = (a.N + kTileM - 1) / kTileM, steps = (a.K + kStep - 1) / kStep;
+    const int slots = (steps + kSlotSteps - 1) / kSlotSteps;
     ragged::make_list(s.list, a.off, a.E, a.R, n_mt, kTileN);
     tc::tc_fence_before();
     __syncthreads();
@@ -181,24 +185,23 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (int t = cid; t < total && !*abort; t += n_cl) {
                 const Tile T = tile_of(a, s, t, n_mt);
                 const int m0 = T.m0 + 128 * rank, n = n_mma(T.n);
-                for (int j = 0; j < steps; ++j, ++issued) {
+                for (int j = 0; j < slots; ++j, ++issued) {
                     if (!tc::mbar_wait(bar(s.sempty[st]), ph ^ 1u, abort, kWaitNs))
                         break;
-                    const uint32_t sa = sfring + st * kSfBytes, fb = bar(s.sfull[st]);
-                    const int x = kMx ? (j * 8) & ~15 : j * 16;
-                    tc::mbar_arrive_expect_tx(fb, 2048 + n * 16);
-                    tc::tma_load_3d(sa, &tmSA, x, m0, T.e, fb);
+                    const uint32_t sa = sfring + st * kSlotBytes, fb = bar(s.sfull[st]);
+                    tc::mbar_arrive_expect_tx(fb, kBlockBytes + n * 64);
+                    tc::tma_load_3d(sa, &tmSA, j * 64, m0, T.e, fb);
                     for (int i = 0; i < n; i += 32)
-                        tc::tma_load_2d(sa + 2048 + i * 16, &tmSB, x, T.r0 + i, fb);
-                    if (++st == kScaleStages) {
+                        tc::tma_load_2d(sa + kBlockBytes + i * 64, &tmSB, j * 64, T.r0 + i, fb);
+                    if (++st == kSlots) {
                         st = 0;
                         ph ^= 1u;
                     }
                 }
             }
             volatile int never = 0;
-            for (int i = 1; i <= min(issued, kScaleStages); ++i) {
-                const int q = st - i < 0 ? st - i + kScaleStages : st - i;
+            for (int i = 1; i <= min(issued, kSlots); ++i) {
+                const int q = st - i < 0 ? st - i + kSlots : st - i;
                 tc::mbar_wait(bar(s.sfull[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
             }
         }
@@ -220,19 +223,21 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const uint32_t acc = tmem + kTileN * buf;
                 const uint32_t id0 = tc::idesc_fp4(256, n, kMx, 0), id1 = kMx ? tc::idesc_fp4(256, n, kMx, 2) : id0;
                 for (int j = 0; j < steps; ++j, ++g) {
-                    if (!tc::mbar_wait(bar(s.sready[sst]), sph, abort, kWaitNs) ||
-                        !tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
+                    const int js = j % kSlotSteps;
+                    if (js == 0 && !tc::mbar_wait_cluster(bar(s.sready[sst]), sph, abort, kWaitNs))
+                        break;
+                    if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
                         break;
                     tc::tc_fence_after();
                     const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
-                    const uint64_t sd = s0 + sst * (kSfBytes >> 4);
+                    const uint64_t sd = s0 + (sst * kSlotBytes + js * kWords * 512) / 16;
                     const uint32_t ta = tmem + kTmemScales + (g & 1) * 48, tb = ta + 16;
 #pragma unroll
                     for (int w = 0; w < kWords; ++w) {
                         tc::tc_cp_32x128b_x4_pair(ta + 4 * w, sd + 32 * w);
-                        tc::tc_cp_32x128b_x4_pair(tb + 8 * w, sd + 128 + 32 * w);
+                        tc::tc_cp_32x128b_x4_pair(tb + 8 * w, sd + kBlockBytes / 16 + 32 * w);
                         if (n > 128)
-                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, sd + 256 + 32 * w);
+                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, sd + 2 * kBlockBytes / 16 + 32 * w);
                     }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
@@ -240,55 +245,59 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         tc::mma_fp4_pair<kMx>(acc, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id1 : id0, ta + 4 * w, tb + 8 * w,
                                               (j | kk) != 0 ? 1u : 0u);
                     }
-                    tc::tc_commit_pair(bar(s.sempty[sst]));
                     tc::tc_commit_pair(bar(s.empty[st]));
                     if (++st == kStages) {
                         st = 0;
                         ph ^= 1u;
                     }
-                    if (++sst == kScaleStages) {
-                        sst = 0;
-                        sph ^= 1u;
+                    if (js == kSlotSteps - 1 || j == steps - 1) {
+                        tc::tc_commit_pair(bar(s.sempty[sst]));
+                        if (++sst == kSlots) {
+                            sst = 0;
+                            sph ^= 1u;
+                        }
                     }
                 }
                 tc::tc_commit_pair(bar(s.accf[buf]));
             }
         }
     } else if (warp >= 8) {
-        // arrange the scales of every kArrange-th stage
-        int g = 0;
+        // arrange the scales: each warp its block of 128 rows of every slot
+        const int b = warp - 8;
+        int st = 0;
+        uint32_t ph = 0;
         const uint32_t ready_lead = tc::mapa(bar(s.sready[0]), 0);
         for (int t = cid; t < total && !*abort; t += n_cl) {
             const Tile T = tile_of(a, s, t, n_mt);
-            const int blocks = T.n > 128 ? 3 : 2;
-            for (int j = 0; j < steps; ++j, ++g) {
-                if ((g & (kArrange - 1)) != warp - 8)
-                    continue;
-                const int st = g % kScaleStages;
-                if (!tc::mbar_wait(bar(s.sfull[st]), (g / kScaleStages) & 1, abort, kWaitNs))
+            for (int j = 0; j < slots; ++j) {
+                if (!tc::mbar_wait(bar(s.sfull[st]), ph, abort, kWaitNs))
                     break;
-                for (int b = 0; b < blocks; ++b) {
-                    uint4 *p = reinterpret_cast<uint4 *>(sf + st * kSfBytes + b * 2048) + lane;
-                    const uint4 r0 = p[0], r1 = p[32], r2 = p[64], r3 = p[96];
+                if (b < 2 || T.n > 128) {
+                    uint8_t *p = sf + st * kSlotBytes + b * kBlockBytes;
+                    uint4 v[4][4];                       // [row l + 32 i][16-byte chunk]
+                    const int x = (lane >> 1) & 3;       // the 64-byte swizzle of rows l + 32 i
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            v[i][c] = *reinterpret_cast<const uint4 *>(p + (lane + 32 * i) * 64 + ((c ^ x) << 4));
                     __syncwarp();
-                    if (kMx) {
-                        const bool hi = j & 1;
-                        p[0] = hi ? make_uint4(r0.z, r1.z, r2.z, r3.z) : make_uint4(r0.x, r1.x, r2.x, r3.x);
-                        p[32] = hi ? make_uint4(r0.w, r1.w, r2.w, r3.w) : make_uint4(r0.y, r1.y, r2.y, r3.y);
-                    } else {
-                        p[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
-                        p[32] = make_uint4(r0.y, r1.y, r2.y, r3.y);
-                        p[64] = make_uint4(r0.z, r1.z, r2.z, r3.z);
-                        p[96] = make_uint4(r0.w, r1.w, r2.w, r3.w);
+                    uint4 *o = reinterpret_cast<uint4 *>(p) + lane;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        o[128 * c] = make_uint4(v[0][c].x, v[1][c].x, v[2][c].x, v[3][c].x);
+                        o[128 * c + 32] = make_uint4(v[0][c].y, v[1][c].y, v[2][c].y, v[3][c].y);
+                        o[128 * c + 64] = make_uint4(v[0][c].z, v[1][c].z, v[2][c].z, v[3][c].z);
+                        o[128 * c + 96] = make_uint4(v[0][c].w, v[1][c].w, v[2][c].w, v[3][c].w);
                     }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0)
-                        tc::mbar_arrive(bar(s.sready[st]));
-                    else
-                        tc::mbar_arrive_cluster(ready_lead + 8 * st);
+                if (lane == 0)
+                    tc::mbar_arrive_cluster(ready_lead + 8 * st);
+                if (++st == kSlots) {
+                    st = 0;
+                    ph ^= 1u;
                 }
             }
         }
@@ -391,8 +400,8 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUtensorMap tm[5];
     if (!tmap_tile(&tm[0], 3, u8, 1, wq, K / 2, N, E, 128, 128) || !tmap_tile(&tm[1], 2, u8, 1, xq, K / 2, R, 1, 128, kTileN / 2) ||
-        !tmap_tile(&tm[2], 2, u8, 1, xq, K / 2, R, 1, 128, 16) || !tmap_tile(&tm[3], 3, u8, 1, ws, Ks, N, E, 16, 128, false) ||
-        !tmap_tile(&tm[4], 2, u8, 1, xs, Ks, R, 1, 16, 32, false))
+        !tmap_tile(&tm[2], 2, u8, 1, xq, K / 2, R, 1, 128, 16) || !tmap_tile(&tm[3], 3, u8, 1, ws, Ks, N, E, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !tmap_tile(&tm[4], 2, u8, 1, xs, Ks, R, 1, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
         return MOE_ERR_CUDA;
     const Args a{offsets, x_alpha, w_alpha, y, dev_status, R, E, N, K};
     return fmt == MOE_FP4_NVFP4 ? launch_as<MOE_FP4_NVFP4>(tm, a, ydt, as_stream(stream))

@@ -7,9 +7,10 @@
 namespace moe {
 
 // Tensor map of rank 2 ([d1][d0]) or 3 ([d2][d1][d0]), densely packed, box b0 x
-// b1 (x 1) with the 128-byte swizzle (b0 elements are 128 bytes) or none.
+// b1 (x 1), swizzled over b0 elements (128 or 64 bytes).
 // Reads past d0 or d1 give zeros.
 bool tmap_tile(CUtensorMap *m, int rank, CUtensorMapDataType t, int elem_bytes, const void *base, uint64_t d0, uint64_t d1,
-             uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle = true);
+             uint64_t d2, uint32_t b0, uint32_t b1,
+               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 }  // namespace moe

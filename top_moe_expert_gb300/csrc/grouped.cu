@@ -673,7 +673,7 @@ bool grouped_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, int elem_bytes, con
 }
 
 bool tmap_tile(CUtensorMap *m, int rank, CUtensorMapDataType t, int elem_bytes, const void *base, uint64_t d0, uint64_t d1,
-             uint64_t d2, uint32_t b0, uint32_t b1, bool swizzle)
+             uint64_t d2, uint32_t b0, uint32_t b1, CUtensorMapSwizzle swizzle)
 {
     auto fn = gg::encode_fn();
     if (!fn)
@@ -683,7 +683,7 @@ bool tmap_tile(CUtensorMap *m, int rank, CUtensorMapDataType t, int elem_bytes, 
     cuuint32_t box[3] = {b0, b1, 1};
     cuuint32_t es[3] = {1, 1, 1};
     return fn(m, t, rank, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
