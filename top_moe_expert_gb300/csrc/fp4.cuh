@@ -37,14 +37,6 @@ __device__ __forceinline__ float ue4m3_value(uint32_t b)
     return __half2float(__low2half(e4m3x2_to_half2(static_cast<uint16_t>(b))));
 }
 
-// Two values -> two E2M1 codes, the first in the low nibble.
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
-{
-    uint16_t r;
-    asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n mov.b16 %0, {b, 0};\n}" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // The two values of a byte of codes, low nibble first (exact).
 __device__ __forceinline__ float2 e2m1_values(uint32_t b)
 {
@@ -55,27 +47,27 @@ __device__ __forceinline__ float2 e2m1_values(uint32_t b)
 }
 
 // Scale byte of a block from the bits of its amax; inv is the factor that
-// takes a value onto the E2M1 grid.
-template <int FMT>
-__device__ __forceinline__ uint32_t block_scale(uint32_t amax, float alpha, float &inv)
+// takes a value onto the E2M1 grid.  NVFP4: g = 1 / (6 alpha).
+__device__ __forceinline__ uint32_t block_scale_nv(uint32_t amax, float alpha, float g, float &inv)
 {
-    if constexpr (FMT == MOE_FP4_NVFP4) {
-        inv = 0.f;
-        if (amax >= 0x7F800000u)
-            return 0x7Fu;
-        const uint32_t b = amax ? to_ue4m3(__uint_as_float(amax) * (1.0f / (6.0f * alpha))) : 0u;
-        if (b)
-            inv = 1.0f / (alpha * ue4m3_value(b));
-        return b;
-    } else {
-        inv = 0.f;
-        if (amax >= 0x7F800000u)
-            return 0xFFu;
-        const int ef = static_cast<int>(amax >> 23);
-        const int X = ef == 0 ? -127 : max(ef - 129, -127);       // at most 125
-        inv = __uint_as_float(static_cast<uint32_t>(127 - X) << 23);
-        return static_cast<uint32_t>(X + 127);
-    }
+    inv = 0.f;
+    if (amax >= 0x7F800000u)
+        return 0x7Fu;
+    const uint32_t b = amax ? to_ue4m3(__uint_as_float(amax) * g) : 0u;
+    if (b)
+        inv = 1.0f / (alpha * ue4m3_value(b));
+    return b;
+}
+
+__device__ __forceinline__ uint32_t block_scale_mx(uint32_t amax, float &inv)
+{
+    inv = 0.f;
+    if (amax >= 0x7F800000u)
+        return 0xFFu;
+    const int ef = static_cast<int>(amax >> 23);
+    const int X = ef == 0 ? -127 : max(ef - 129, -127);       // at most 125
+    inv = __uint_as_float(static_cast<uint32_t>(127 - X) << 23);
+    return static_cast<uint32_t>(X + 127);
 }
 
 template <int FMT>

@@ -22,7 +22,7 @@
 // Both CTAs hold the scales of all 192 rows of x and of their own 128 of w.
 //
 // Roles: warp 0 loads codes, warp 2 loads scales, warps 8..10 arrange them (w,
-// the first 128 rows of x, the rest), warp 1 of the leader issues copies and
+// the first 128 rows of x, the rest) and warp 3 tells the leader, warp 1 of the leader issues copies and
 // MMAs, warps 4..7 drain the accumulators.  Every wait is bounded; an expired
 // one is reported as MOE_ERR_TIMEOUT in dev_status[1].
 #include <cuda.h>
@@ -56,7 +56,7 @@ struct Args {
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];
-    uint64_t sfull[kSlots], sready[kSlots], sempty[kSlots];
+    uint64_t sfull[kSlots], sdone[kSlots], sready[kSlots], sempty[kSlots];
     uint64_t accf[2], acce[2];
     uint32_t tmem;
     int abort;
@@ -110,7 +110,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         for (int i = 0; i < kSlots; ++i) {
             tc::mbar_init(bar(s.sfull[i]), 1);
-            tc::mbar_init(bar(s.sready[i]), 6);          // three arranging warps of each CTA
+            tc::mbar_init(bar(s.sdone[i]), 3);           // the three arranging warps
+            tc::mbar_init(bar(s.sready[i]), 2);          // each CTA's relay
             tc::mbar_init(bar(s.sempty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -261,12 +262,34 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 tc::tc_commit_pair(bar(s.accf[buf]));
             }
         }
+    } else if (warp == 3) {
+        // tell the leader of every arranged slot: one thread, because an
+        // arrival in the other CTA is ordered after the writes by a
+        // cluster-scope fence, which costs the more the more warps make it
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            const uint32_t ready_lead = tc::mapa(bar(s.sready[0]), 0);
+            for (int t = cid; t < total && !*abort; t += n_cl) {
+                for (int j = 0; j < slots; ++j) {
+                    if (!tc::mbar_wait(bar(s.sdone[st]), ph, abort, kWaitNs))
+                        break;
+                    if (rank == 0)
+                        tc::mbar_arrive(bar(s.sready[st]));
+                    else
+                        tc::mbar_arrive_cluster(ready_lead + 8 * st);
+                    if (++st == kSlots) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+        }
     } else if (warp >= 8) {
         // arrange the scales: each warp its block of 128 rows of every slot
         const int b = warp - 8;
         int st = 0;
         uint32_t ph = 0;
-        const uint32_t ready_lead = tc::mapa(bar(s.sready[0]), 0);
         for (int t = cid; t < total && !*abort; t += n_cl) {
             const Tile T = tile_of(a, s, t, n_mt);
             for (int j = 0; j < slots; ++j) {
@@ -294,7 +317,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     __syncwarp();
                 }
                 if (lane == 0)
-                    tc::mbar_arrive_cluster(ready_lead + 8 * st);
+                    tc::mbar_arrive(bar(s.sdone[st]));
                 if (++st == kSlots) {
                     st = 0;
                     ph ^= 1u;
