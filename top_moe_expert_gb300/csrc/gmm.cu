@@ -400,7 +400,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    tc::mbar_arrive_cluster(tc::mapa(bar(s.acce[buf]), 0));
+                    tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
             }
         }
         if (OP == kWgrad)

@@ -348,7 +348,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                tc::mbar_arrive_cluster(tc::mapa(bar(s.acce[buf]), 0));
+                tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
         }
         // rows outside every group
         const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);

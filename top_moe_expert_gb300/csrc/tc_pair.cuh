@@ -37,10 +37,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes)
+// The same without ordering this thread's memory operations before it: for
+// hand-overs of tensor memory, whose reads tcgen05.wait::ld has completed.  A
+// releasing arrival would wait for the thread's global stores to be done.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;"
-                 ::"r"(bar), "r"(bytes) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // mbar_wait for a barrier on which the other CTA arrives.
