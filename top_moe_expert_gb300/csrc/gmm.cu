@@ -68,7 +68,8 @@ struct Shared {
     ragged::List list;
 };
 
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + static_cast<int>(sizeof(Shared));
+constexpr int kDrainBytes = 16384;             // four warps' staging tiles (fwd, dgrad)
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kDrainBytes + static_cast<int>(sizeof(Shared));
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct Tile {
@@ -92,7 +93,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, i
     const int nt = at / n_mt;
     T.m0 = (at - nt * n_mt) * kTileM;
     T.lo = s.list.lo[T.e];
-    T.rows = s.list.rows[T.e];
+    T.rows = s.list.rows(T.e);
     T.n0 = nt * kTileN;
     T.n = min(kTileN, (OP == kWgrad ? a.C : T.rows) - T.n0);
     T.steps = ((OP == kWgrad ? T.rows : a.J) + kStep - 1) / kStep;
@@ -132,16 +133,16 @@ __device__ __forceinline__ void add_row(const uint32_t (&v)[32], const OT *old, 
 template <int OP, typename OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-            const __grid_constant__ CUtensorMap tmC, const Args a)
+            const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
-    // tmC: x or dy in boxes of 16 rows (fwd, dgrad); dw (wgrad)
+    // tmB16: B in boxes of 16 rows (fwd, dgrad); tmY: the result
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const uint32_t raw = tc::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);      // the same offset in both CTAs
     const uint32_t ring = tc::smem_u32(smem);
-    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes);
+    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes + kDrainBytes);
     volatile int *abort = &s.abort;
     constexpr int kRing = stages_of(OP);
     auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
@@ -161,7 +162,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         tc::fence_mbar_init();
         tc::prefetch_tmap(&tmA);
         tc::prefetch_tmap(&tmB);
-        tc::prefetch_tmap(&tmC);
+        if (OP != kWgrad)
+            tc::prefetch_tmap(&tmB16);
+        tc::prefetch_tmap(&tmY);
     }
     if (warp == 1) {
         tc::tmem_alloc_pair(tc::smem_u32(&s.tmem), kTmemCols);
@@ -230,7 +233,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             tc::tma_load_2d_pair(sb, &tmB, j * kStep, r0, fb);
                         else
                             for (int i = 0; i < nh; i += 16)
-                                tc::tma_load_2d_pair(sb + i * 128, &tmC, j * kStep, r0 + i, fb);
+                                tc::tma_load_2d_pair(sb + i * 128, &tmB16, j * kStep, r0 + i, fb);
                     }
                     if (++st == kRing) {
                         st = 0;
@@ -380,20 +383,26 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         __syncwarp();
                         if (lane == 0 && m < a.M) {
                             if (sizeof(OT) == 4 && a.accumulate)
-                                tc::tma_add_3d(&tmC, tc::smem_u32(tile), T.n0 + c0, m, T.e);
+                                tc::tma_add_3d(&tmY, tc::smem_u32(tile), T.n0 + c0, m, T.e);
                             else
-                                tc::tma_store_3d(&tmC, tc::smem_u32(tile), T.n0 + c0, m, T.e);
+                                tc::tma_store_3d(&tmY, tc::smem_u32(tile), T.n0 + c0, m, T.e);
                         }
                         if (lane == 0)
                             tc::bulk_commit();
                     }
                 }
             } else {
+                uint8_t *tiles = smem + kStages * kStageBytes + q * 4096;
                 for (int c0 = 0; c0 < T.n; c0 += 32) {
                     uint32_t v[32];
                     tc::tmem_ld_32x32b_x32(acc + c0, v);
                     tc::tmem_ld_wait();
-                    store_rows<OT>(v, out + static_cast<int64_t>(T.lo + T.n0 + c0) * a.M, a.M, m, a.M, T.n - c0, lane);
+                    const int64_t r0 = T.lo + T.n0 + c0;
+                    if (T.n - c0 < 32) {                  // a TMA store would reach into the next group's rows
+                        store_rows<OT>(v, out + r0 * a.M, a.M, m, a.M, T.n - c0, lane);
+                        break;
+                    }
+                    drain_rows<OT>(v, tiles, flip, &tmY, m - lane, static_cast<int>(r0), a.M, lane);
                 }
             }
             if (T.steps) {
@@ -403,8 +412,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
             }
         }
-        if (OP == kWgrad)
-            tc::bulk_wait<0>();
+        tc::bulk_wait<0>();
         if (OP != kWgrad) {
             // rows outside every group
             const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);
@@ -451,8 +459,7 @@ static moe_status_t check(const void *a, const void *b, const void *out, int32_t
 }
 
 template <int OP, typename OT>
-static moe_status_t launch(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmB16, const Args &a,
-                           int64_t most_tiles, cudaStream_t s)
+static moe_status_t launch(const CUtensorMap (&tm)[4], const Args &a, int64_t most_tiles, cudaStream_t s)
 {
     auto k = gemm_kernel<OP, OT>;
     static std::atomic<uint64_t> done{0};
@@ -460,17 +467,22 @@ static moe_status_t launch(const CUtensorMap &tmA, const CUtensorMap &tmB, const
         return MOE_ERR_CUDA;
     const int pairs = device_sm_count() / 2;
     const int grid = 2 * static_cast<int>(most_tiles < pairs ? most_tiles : pairs);
-    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tmA, tmB, tmB16, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
+                                                                                                            : MOE_ERR_CUDA;
 }
 
 template <int OP>
-static moe_status_t launch_as(const CUtensorMap &tmA, const CUtensorMap &tmB, const CUtensorMap &tmB16, const Args &a,
-                              int32_t odt, int64_t most_tiles, cudaStream_t s)
+static moe_status_t launch_as(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int64_t most_tiles, cudaStream_t s)
 {
     if (odt == MOE_FP32)
-        return launch<OP, float>(tmA, tmB, tmB16, a, most_tiles, s);
-    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16>(tmA, tmB, tmB16, a, most_tiles, s)
-                           : launch<OP, __half>(tmA, tmB, tmB16, a, most_tiles, s);
+        return launch<OP, float>(tm, a, most_tiles, s);
+    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16>(tm, a, most_tiles, s) : launch<OP, __half>(tm, a, most_tiles, s);
+}
+
+static CUtensorMapDataType map_type(int32_t dt)
+{
+    return dt == MOE_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                          : dt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
 // y or dx: C outputs per row from J contracted values; w [E][C][J] (OP kFwd)
@@ -479,14 +491,15 @@ template <int OP>
 static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, int32_t E, int32_t C, int32_t J,
                          const int32_t *off, void *y, int32_t ydt, int32_t *dev_status, cudaStream_t s)
 {
-    const CUtensorMapDataType t = dt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tmA, tmB, tmB16;
-    const bool ok = OP == kFwd ? tmap_tile(&tmA, 3, t, 2, w, J, C, E, 64, 128) : tmap_tile(&tmA, 3, t, 2, w, C, J, E, 64, 64);
-    if (!ok || !tmap_tile(&tmB, 2, t, 2, x, J, R, 1, 64, 128) || !tmap_tile(&tmB16, 2, t, 2, x, J, R, 1, 64, 16))
+    const CUtensorMapDataType t = map_type(dt);
+    CUtensorMap tm[4];
+    const bool ok = OP == kFwd ? tmap_tile(&tm[0], 3, t, 2, w, J, C, E, 64, 128) : tmap_tile(&tm[0], 3, t, 2, w, C, J, E, 64, 64);
+    if (!ok || !tmap_tile(&tm[1], 2, t, 2, x, J, R, 1, 64, 128) || !tmap_tile(&tm[2], 2, t, 2, x, J, R, 1, 64, 16) ||
+        !tmap_rows_out(&tm[3], map_type(ydt), ydt == MOE_FP32 ? 4 : 2, y, C, R))
         return MOE_ERR_CUDA;
-    Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
+    const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
     const int64_t n_mt = (C + kTileM - 1) / kTileM;
-    return launch_as<OP>(tmA, tmB, tmB16, a, ydt, n_mt * (static_cast<int64_t>(R) / kTileN + (E < R ? E : R)), s);
+    return launch_as<OP>(tm, a, ydt, n_mt * (static_cast<int64_t>(R) / kTileN + (E < R ? E : R)), s);
 }
 
 }  // namespace gmm
@@ -523,18 +536,18 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
     const moe_status_t st = check(dy, x, dw, dt, wdt, R, E, N, K, offsets);
     if (st != MOE_OK)
         return st;
-    const CUtensorMapDataType t = dt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tmA, tmB, tmC;
-    // without rows nothing is loaded; the maps still need an address
-    const void *ra = R ? dy : dw, *rb = R ? x : dw;
-    const CUtensorMapDataType to = wdt == MOE_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : t;
+    const CUtensorMapDataType t = map_type(dt);
     const int size = wdt == MOE_FP32 ? 4 : 2;
-    if (!tmap_tile(&tmA, 2, t, 2, ra, N, R ? R : 1, 1, 64, 64) || !tmap_tile(&tmB, 2, t, 2, rb, K, R ? R : 1, 1, 64, 64) ||
-        !tmap_tile(&tmC, 3, to, size, dw, K, N, E, 128 / size, 32))
+    CUtensorMap tm[4];
+    // without rows nothing is loaded; the maps still need an address
+    if (!tmap_tile(&tm[0], 2, t, 2, R ? dy : dw, N, R ? R : 1, 1, 64, 64) ||
+        !tmap_tile(&tm[1], 2, t, 2, R ? x : dw, K, R ? R : 1, 1, 64, 64) ||
+        !tmap_tile(&tm[3], 3, map_type(wdt), size, dw, K, N, E, 128 / size, 32))
         return MOE_ERR_CUDA;
-    Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
+    tm[2] = tm[1];
+    const Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
     const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + kTileN - 1) / kTileN);
     if (tiles > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    return launch_as<kWgrad>(tmA, tmB, tmC, a, wdt, tiles, as_stream(stream));
+    return launch_as<kWgrad>(tm, a, wdt, tiles, as_stream(stream));
 }

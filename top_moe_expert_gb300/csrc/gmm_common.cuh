@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "tc_pair.cuh"
 
 namespace moe {
 namespace gmm {
@@ -46,6 +47,43 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int
             if (m < M && c + odd < n)
                 *reinterpret_cast<uint32_t *>(out + (c + odd) * ld + (m & ~1)) = w;
         }
+    }
+}
+
+// The same for 32 whole rows, through a staging tile of this warp's and TMA: 32
+// rows of the warp's 32 elements (64 or 128 bytes, swizzled so that the warp's
+// words of a row or two fall into different banks).  tiles: 4096 bytes; m0:
+// the warp's first element, r0 the first row.
+template <typename OT>
+__device__ __forceinline__ void drain_rows(const uint32_t (&v)[32], uint8_t *tiles, int &flip, const CUtensorMap *map, int m0,
+                                           int r0, int M, int lane, float f = 1.f)
+{
+    if constexpr (sizeof(OT) == 4) {
+        tc::bulk_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            *reinterpret_cast<float *>(tiles + c * 128 + ((lane * 4) ^ ((c & 7) << 4))) = __uint_as_float(v[c]) * f;
+    } else {
+        tiles += flip * 2048;
+        flip ^= 1;
+        tc::bulk_wait_read<1>();
+        __syncwarp();
+        const int odd = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const uint32_t own = pack2<OT>(__uint_as_float(v[c]) * f, __uint_as_float(v[c + 1]) * f);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+            const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+            *reinterpret_cast<uint32_t *>(tiles + (c + odd) * 64 + (((lane & ~1) * 2) ^ (((c >> 1) & 3) << 4))) = w;
+        }
+    }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (m0 < M)
+            tc::tma_store_2d(map, tc::smem_u32(tiles), m0, r0);
+        tc::bulk_commit();
     }
 }
 

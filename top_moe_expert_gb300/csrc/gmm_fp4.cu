@@ -77,7 +77,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, i
     const int at = t - s.list.tiles[T.e], nt = at / n_mt;
     T.m0 = (at - nt * n_mt) * kTileM;
     T.r0 = s.list.lo[T.e] + nt * kTileN;
-    T.n = min(kTileN, s.list.rows[T.e] - nt * kTileN);
+    T.n = min(kTileN, s.list.rows(T.e) - nt * kTileN);
     return T;
 }
 

@@ -13,4 +13,12 @@ bool tmap_tile(CUtensorMap *m, int rank, CUtensorMapDataType t, int elem_bytes, 
              uint64_t d2, uint32_t b0, uint32_t b1,
                CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
+// The map that drain_rows stores through: 32 columns x 32 rows of [rows][cols].
+inline bool tmap_rows_out(CUtensorMap *m, CUtensorMapDataType t, int elem_bytes, const void *base, uint64_t cols,
+                          uint64_t rows)
+{
+    return tmap_tile(m, 2, t, elem_bytes, base, cols, rows, 1, 32, 32,
+                     elem_bytes == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 }  // namespace moe

@@ -9,15 +9,6 @@ namespace ragged {
 
 constexpr int kMaxExperts = 1024;
 
-// Rows [lo, hi) of expert e.  offsets are device data: they are clamped to
-// [0, R] and a group that would run backwards is empty, so no value of them
-// takes an access out of its buffer.
-__device__ __forceinline__ void group(const int32_t *__restrict__ off, int e, int R, int &lo, int &hi)
-{
-    lo = min(max(off[e], 0), R);
-    hi = max(min(off[e + 1], R), lo);
-}
-
 // Whether offsets are what the contract says; a call reports it once.
 __device__ __forceinline__ void report_bad(const int32_t *__restrict__ off, int R, int e, int32_t *dev_status)
 {
@@ -26,11 +17,14 @@ __device__ __forceinline__ void report_bad(const int32_t *__restrict__ off, int 
 }
 
 // The persistent kernels' list of tiles, in shared memory: expert e's first
-// row, row count, and the number of tiles before its own (mt tiles across for
-// every nt rows); tiles[E] is the total.  Every CTA makes its own.
+// row, and the number of tiles before its own (mt tiles across for every nt
+// rows); tiles[E] is the total.  Every CTA makes its own.  Offsets are device
+// data: they are clamped to [0, R] and a group that would run backwards is
+// empty, so no value of them takes an access out of its buffer.
 struct List {
-    int lo[kMaxExperts], rows[kMaxExperts], tiles[kMaxExperts + 1];
+    int lo[kMaxExperts + 1], tiles[kMaxExperts + 1];
     int warp_sum[32];
+    __device__ __forceinline__ int rows(int e) const { return max(lo[e + 1] - lo[e], 0); }
 };
 
 __device__ __forceinline__ void make_list(List &l, const int32_t *__restrict__ off, int E, int R, int mt, int nt)
@@ -40,12 +34,13 @@ __device__ __forceinline__ void make_list(List &l, const int32_t *__restrict__ o
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
-        int lo, hi;
-        group(off, e, R, lo, hi);
-        l.lo[e] = lo;
-        l.rows[e] = hi - lo;
-        sum += mt * ((hi - lo + nt - 1) / nt);
+        l.lo[e] = min(max(off[e], 0), R);
+        if (e == E - 1)
+            l.lo[E] = min(max(off[E], 0), R);
     }
+    __syncthreads();
+    for (int e = e0; e < e1; ++e)
+        sum += mt * ((l.rows(e) + nt - 1) / nt);
     int run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -61,7 +56,7 @@ __device__ __forceinline__ void make_list(List &l, const int32_t *__restrict__ o
         at += l.warp_sum[w];
     for (int e = e0; e < e1; ++e) {
         l.tiles[e] = at;
-        at += mt * ((l.rows[e] + nt - 1) / nt);
+        at += mt * ((l.rows(e) + nt - 1) / nt);
     }
     if (e1 == E && e0 < E)
         l.tiles[E] = at;
