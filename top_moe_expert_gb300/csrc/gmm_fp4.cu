@@ -12,13 +12,13 @@
 //
 // Scales lie in memory row by row; the MMA wants them in tensor memory with a
 // row's 4 bytes in lane row % 32, column row / 32.  Groups start at any row, so
-// that arrangement cannot be made beforehand for x: 64 natural bytes of each
-// row (a slot: 1024 elements of NVFP4, 2048 of MXFP4) come by TMA, a warp turns
+// that arrangement cannot be made beforehand for x: 32 natural bytes of each
+// row (a slot: 512 elements of NVFP4, 1024 of MXFP4) come by TMA, a warp turns
 // them into the arrangement in place (a 4 x 4 transpose of words in registers;
 // a lane holds rows l, l + 32, l + 64, l + 96), and tcgen05.cp copies a stage's
-// part into every quadrant of tensor memory.  64 bytes rather than a stage's 16
-// because TMA is paid by the row, and because the leader hears of the other
-// CTA's slot by a cluster-scope arrival that takes several hundred cycles.
+// part into every quadrant of tensor memory.  TMA is paid by the row: slots of
+// a stage's 16 bytes took 261 us at 8192 x 8192 x 8192 (NVFP4), of 64 bytes
+// with the room for only two of them 183 us, five of 32 bytes 164 us.
 // Both CTAs hold the scales of all 192 rows of x and of their own 128 of w.
 //
 // Roles: warp 0 loads codes, warp 2 loads scales, warps 8..10 arrange them (w,
@@ -38,10 +38,12 @@
 namespace moe {
 namespace gmm4 {
 
-constexpr int kStages = 5, kSlots = 3;
+constexpr int kStages = 5, kSlots = 5;
+constexpr int kSlotRow = 32;                   // bytes of a row's scales in a slot
 constexpr int kTileM = 256, kTileN = 192, kStep = 256;
 constexpr int kABytes = 128 * 128, kStageBytes = kABytes + kTileN / 2 * 128;
-constexpr int kBlockBytes = 128 * 64, kSlotBytes = 3 * kBlockBytes;   // scales of 128 rows of w, 2 x 128 of x
+constexpr int kDrainBytes = 16384;
+constexpr int kBlockBytes = 128 * kSlotRow, kSlotBytes = 3 * kBlockBytes;   // scales of 128 rows of w, 2 x 128 of x
 constexpr int kThreads = 352;
 constexpr uint32_t kTmemCols = 512, kTmemScales = 2 * kTileN;    // accumulators first, then two stages of scales
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -63,7 +65,7 @@ struct Shared {
     ragged::List list;
 };
 
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSlots * kSlotBytes + static_cast<int>(sizeof(Shared));
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kSlots * kSlotBytes + kDrainBytes + static_cast<int>(sizeof(Shared));
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct Tile {
@@ -87,11 +89,11 @@ template <int FMT, typename OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmSA,
-            const __grid_constant__ CUtensorMap tmSB, const Args a)
+            const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
     constexpr bool kMx = FMT == MOE_FP4_MXFP4;
     constexpr int kWords = kMx ? 2 : 4;                 // words of scales of a row in a stage
-    constexpr int kSlotSteps = 16 / kWords;             // stages in a slot
+    constexpr int kSlotSteps = kSlotRow / 4 / kWords;             // stages in a slot
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -99,7 +101,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     uint8_t *sf = smem + kStages * kStageBytes;
     const uint32_t ring = tc::smem_u32(smem), sfring = tc::smem_u32(sf);
-    Shared &s = *reinterpret_cast<Shared *>(sf + kSlots * kSlotBytes);
+    Shared &s = *reinterpret_cast<Shared *>(sf + kSlots * kSlotBytes + kDrainBytes);
     volatile int *abort = &s.abort;
     auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
 
@@ -125,6 +127,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         tc::prefetch_tmap(&tmB16);
         tc::prefetch_tmap(&tmSA);
         tc::prefetch_tmap(&tmSB);
+        tc::prefetch_tmap(&tmY);
     }
     if (warp == 1) {
         tc::tmem_alloc_pair(tc::smem_u32(&s.tmem), kTmemCols);
@@ -190,10 +193,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (!tc::mbar_wait(bar(s.sempty[st]), ph ^ 1u, abort, kWaitNs))
                         break;
                     const uint32_t sa = sfring + st * kSlotBytes, fb = bar(s.sfull[st]);
-                    tc::mbar_arrive_expect_tx(fb, kBlockBytes + n * 64);
-                    tc::tma_load_3d(sa, &tmSA, j * 64, m0, T.e, fb);
+                    tc::mbar_arrive_expect_tx(fb, kBlockBytes + n * kSlotRow);
+                    tc::tma_load_3d(sa, &tmSA, j * kSlotRow, m0, T.e, fb);
                     for (int i = 0; i < n; i += 32)
-                        tc::tma_load_2d(sa + kBlockBytes + i * 64, &tmSB, j * 64, T.r0 + i, fb);
+                        tc::tma_load_2d(sa + kBlockBytes + i * kSlotRow, &tmSB, j * kSlotRow, T.r0 + i, fb);
                     if (++st == kSlots) {
                         st = 0;
                         ph ^= 1u;
@@ -263,9 +266,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
         }
     } else if (warp == 3) {
-        // tell the leader of every arranged slot: one thread, because an
-        // arrival in the other CTA is ordered after the writes by a
-        // cluster-scope fence, which costs the more the more warps make it
+        // tell the leader of every arranged slot, one thread for the three
+        // warps' writes (each is through its own proxy fence by then)
         if (lane == 0) {
             int st = 0;
             uint32_t ph = 0;
@@ -274,10 +276,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 for (int j = 0; j < slots; ++j) {
                     if (!tc::mbar_wait(bar(s.sdone[st]), ph, abort, kWaitNs))
                         break;
-                    if (rank == 0)
-                        tc::mbar_arrive(bar(s.sready[st]));
-                    else
-                        tc::mbar_arrive_cluster(ready_lead + 8 * st);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive_cluster_smem(ready_lead + 8 * st);
                     if (++st == kSlots) {
                         st = 0;
                         ph ^= 1u;
@@ -297,17 +297,18 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     break;
                 if (b < 2 || T.n > 128) {
                     uint8_t *p = sf + st * kSlotBytes + b * kBlockBytes;
-                    uint4 v[4][4];                       // [row l + 32 i][16-byte chunk]
-                    const int x = (lane >> 1) & 3;       // the 64-byte swizzle of rows l + 32 i
+                    constexpr int kChunks = kSlotRow / 16;
+                    uint4 v[4][kChunks];                 // [row l + 32 i][16-byte chunk]
+                    const int x = (lane >> 2) & 1;       // the 32-byte swizzle of rows l + 32 i
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            v[i][c] = *reinterpret_cast<const uint4 *>(p + (lane + 32 * i) * 64 + ((c ^ x) << 4));
+                        for (int c = 0; c < kChunks; ++c)
+                            v[i][c] = *reinterpret_cast<const uint4 *>(p + (lane + 32 * i) * kSlotRow + ((c ^ x) << 4));
                     __syncwarp();
                     uint4 *o = reinterpret_cast<uint4 *>(p) + lane;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kChunks; ++c) {
                         o[128 * c] = make_uint4(v[0][c].x, v[1][c].x, v[2][c].x, v[3][c].x);
                         o[128 * c + 32] = make_uint4(v[0][c].y, v[1][c].y, v[2][c].y, v[3][c].y);
                         o[128 * c + 64] = make_uint4(v[0][c].z, v[1][c].z, v[2][c].z, v[3][c].z);
@@ -326,7 +327,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
     } else if (warp >= 4) {
         const int q = warp & 3;                         // TMEM lane quadrant
-        int tix = 0;
+        int tix = 0, flip = 0;
         OT *out = static_cast<OT *>(a.out);
         for (int t = cid; t < total; t += n_cl, ++tix) {
             const Tile T = tile_of(a, s, t, n_mt);
@@ -339,17 +340,23 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
             tc::tc_fence_after();
             const uint32_t acc = tmem + kTileN * buf + (static_cast<uint32_t>(32 * q) << 16);
+            uint8_t *tiles = sf + kSlots * kSlotBytes + q * 4096;
             for (int c0 = 0; c0 < T.n; c0 += 32) {
                 uint32_t v[32];
                 tc::tmem_ld_32x32b_x32(acc + c0, v);
                 tc::tmem_ld_wait();
-                gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f);
+                if (T.n - c0 < 32) {                     // a TMA store would reach into the next group's rows
+                    gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f);
+                    break;
+                }
+                gmm::drain_rows<OT>(v, tiles, flip, &tmY, m - lane, T.r0 + c0, a.N, lane, f);
             }
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
         }
+        tc::bulk_wait<0>();
         // rows outside every group
         const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);
         const int64_t per = static_cast<int64_t>(a.N) * sizeof(OT) / 16;
@@ -376,7 +383,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 // ---------------------------------------------------------------- host
 
 template <int FMT, typename OT>
-static moe_status_t launch(const CUtensorMap (&tm)[5], const Args &a, cudaStream_t s)
+static moe_status_t launch(const CUtensorMap (&tm)[6], const Args &a, cudaStream_t s)
 {
     auto k = gemm_kernel<FMT, OT>;
     static std::atomic<uint64_t> done{0};
@@ -385,12 +392,12 @@ static moe_status_t launch(const CUtensorMap (&tm)[5], const Args &a, cudaStream
     const int64_t most = static_cast<int64_t>((a.N + kTileM - 1) / kTileM) * (a.R / kTileN + (a.E < a.R ? a.E : a.R));
     const int pairs = device_sm_count() / 2;
     const int grid = 2 * static_cast<int>(most < pairs ? most : pairs);
-    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tm[0], tm[1], tm[2], tm[3], tm[4], a) == cudaSuccess
+    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tm[0], tm[1], tm[2], tm[3], tm[4], tm[5], a) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
 }
 
 template <int FMT>
-static moe_status_t launch_as(const CUtensorMap (&tm)[5], const Args &a, int32_t ydt, cudaStream_t s)
+static moe_status_t launch_as(const CUtensorMap (&tm)[6], const Args &a, int32_t ydt, cudaStream_t s)
 {
     if (ydt == MOE_FP32)
         return launch<FMT, float>(tm, a, s);
@@ -421,10 +428,14 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
         return MOE_ERR_INVALID_ARG;
     const int Ks = fp4::scale_cols(K, fmt);
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    CUtensorMap tm[5];
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_32B;
+    const CUtensorMapDataType ty = ydt == MOE_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : ydt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tm[6];
     if (!tmap_tile(&tm[0], 3, u8, 1, wq, K / 2, N, E, 128, 128) || !tmap_tile(&tm[1], 2, u8, 1, xq, K / 2, R, 1, 128, kTileN / 2) ||
-        !tmap_tile(&tm[2], 2, u8, 1, xq, K / 2, R, 1, 128, 16) || !tmap_tile(&tm[3], 3, u8, 1, ws, Ks, N, E, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !tmap_tile(&tm[4], 2, u8, 1, xs, Ks, R, 1, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        !tmap_tile(&tm[2], 2, u8, 1, xq, K / 2, R, 1, 128, 16) || !tmap_tile(&tm[3], 3, u8, 1, ws, Ks, N, E, kSlotRow, 128, sw) ||
+        !tmap_tile(&tm[4], 2, u8, 1, xs, Ks, R, 1, kSlotRow, 32, sw) ||
+        !tmap_rows_out(&tm[5], ty, ydt == MOE_FP32 ? 4 : 2, y, N, R))
         return MOE_ERR_CUDA;
     const Args a{offsets, x_alpha, w_alpha, y, dev_status, R, E, N, K};
     return fmt == MOE_FP4_NVFP4 ? launch_as<MOE_FP4_NVFP4>(tm, a, ydt, as_stream(stream))
