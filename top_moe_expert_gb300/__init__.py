@@ -101,6 +101,8 @@ def use_library(path: str) -> None:
 def lib() -> ctypes.CDLL:
     """The loaded libmoe_ffn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -121,7 +123,7 @@ def _check(status: int, where: str) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # Every pointer handed to the library is checked first: a host tensor, a
@@ -130,7 +132,7 @@ def _ptr(t):
 # size.  The checks raise ValueError; nothing is launched.
 
 def _is_gpu(t: torch.Tensor) -> bool:
-    return t.device.type == "cuda"
+    return t.is_cuda
 
 
 def _need(t, name: str, dtypes=None, shape=None, min_numel=None, device=None):
@@ -169,19 +171,23 @@ def _nbytes(t) -> int:
 def _guard(device):
     """Make the tensors' GPU current for the call (the library launches on
     the current device)."""
-    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return _NO_GUARD
+    return torch.cuda.device(device)
+
+
+_NO_GUARD = contextlib.nullcontext()
 
 
 def _stream(stream=None, device=None):
     """The stream handle: `stream`, or the current stream of `device`."""
     if stream is None:
-        s = torch.cuda.current_stream(device)
-    else:
-        s = stream
-        sd = getattr(s, "device", None)
-        if device is not None and sd is not None and sd != device:
-            raise ValueError(f"stream is on {sd}; the call's tensors are on {device}")
-    return ctypes.c_void_p(s.cuda_stream)
+        # the handle alone: a Stream object costs more than a small launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device.index)
+    sd = getattr(stream, "device", None)
+    if device is not None and sd is not None and sd != device:
+        raise ValueError(f"stream is on {sd}; the call's tensors are on {device}")
+    return stream.cuda_stream
 
 
 _IDS = (torch.int32,)
