@@ -161,7 +161,9 @@ def _dev(t: torch.Tensor, name: str):
 
 def _opt(t, name: str, **kw):
     """_need for an optional argument (None passes)."""
-    return None if t is None else _need(t, name, **kw)
+    if t is not None:
+        _need(t, name, **kw)
+    return t
 
 
 def _nbytes(t) -> int:
@@ -637,19 +639,32 @@ def moe_ffn_grouped(x, topk_ids, topk_w, w13: Weights, w2: Weights, sfa13, sfa2,
 _DT16 = (torch.bfloat16, torch.float16)
 
 
-def _groups(offsets, dev):
-    """Check the group offsets; returns the number of experts."""
-    _need(offsets, "offsets", _IDS, device=dev)
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError(f"offsets must be [E + 1], not {tuple(offsets.shape)}")
-    return offsets.numel() - 1
-
-
-def _rows2(t, name, dtypes, dev=None, cols=None):
-    _need(t, name, dtypes, device=dev)
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [R, {'.' if cols is None else cols}], not {tuple(t.shape)}")
+def _arg(t, name: str, dtypes, dim, device=None):
+    """_need plus the number of dimensions (None: any but 0), in one pass;
+    returns the shape."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == dim and t.is_contiguous()
+            and (device is None or t.device == device)):
+        _need(t, name, dtypes, device=device)
+        if t.dim() != dim and (dim is not None or t.dim() == 0):
+            raise ValueError(f"{name} must have {dim or 'at least 1'} dimensions, not {tuple(t.shape)}")
     return t.shape
+
+
+def _groups(offsets, dev) -> int:
+    """Check the group offsets; returns the number of experts."""
+    n, = _arg(offsets, "offsets", _IDS, 1, dev)
+    if n < 2:
+        raise ValueError(f"offsets must be [E + 1], not [{n}]")
+    return n - 1
+
+
+def _result(t, name: str, shape, dtype, dtypes, dev):
+    """The output: a new one of `dtype`, or the caller's after its check."""
+    if t is not None:
+        return _need(t, name, dtypes, shape, device=dev)
+    if dtype not in dtypes:
+        raise ValueError(f"{name} cannot be {dtype}; expected {' or '.join(str(d) for d in dtypes)}")
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_dtype=None, y=None, dev_status=None,
@@ -657,18 +672,16 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_
     """y [R, N]: rows offsets[e] .. offsets[e+1] - 1 of x [R, K] times w[e]^T,
     w [E, N, K] of x's type (bf16 or fp16); rows past offsets[E] give zeros.
     out_dtype: x's type (default) or float32."""
-    R, K = _rows2(x, "x", _DT16)
-    dev = x.device
+    R, K = _arg(x, "x", _DT16, 2)
+    dev, dt = x.device, x.dtype
     E = _groups(offsets, dev)
-    _need(w, "w", (x.dtype,), device=dev)
-    if w.dim() != 3 or w.shape[0] != E or w.shape[2] != K:
+    e, N, k = _arg(w, "w", (dt,), 3, dev)
+    if e != E or k != K:
         raise ValueError(f"w must be [E={E}, N, K={K}], not {tuple(w.shape)}")
-    N = w.shape[1]
-    y = y if y is not None else torch.empty((R, N), dtype=out_dtype or x.dtype, device=dev)
-    _need(y, "y", (x.dtype, torch.float32), (R, N), device=dev)
+    y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev)
     _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
     with _guard(dev):
-        _check(lib().moe_grouped_mm(_ptr(x), _ptr(w), _DT[x.dtype], _ptr(offsets), R, E, N, K, _ptr(y), _DT[y.dtype],
+        _check(lib().moe_grouped_mm(_ptr(x), _ptr(w), _DT[dt], _ptr(offsets), R, E, N, K, _ptr(y), _DT[y.dtype],
                                     _ptr(dev_status), _stream(stream, dev)), "moe_grouped_mm")
     return y
 
@@ -677,18 +690,16 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
                          dev_status=None, stream=None):
     """dx [R, K], the gradient of moe_grouped_mm's x: rows of dy [R, N] times
     their expert's w[e] [N, K]; rows past offsets[E] give zeros."""
-    R, N = _rows2(dy, "dy", _DT16)
-    dev = dy.device
+    R, N = _arg(dy, "dy", _DT16, 2)
+    dev, dt = dy.device, dy.dtype
     E = _groups(offsets, dev)
-    _need(w, "w", (dy.dtype,), device=dev)
-    if w.dim() != 3 or w.shape[0] != E or w.shape[1] != N:
+    e, n, K = _arg(w, "w", (dt,), 3, dev)
+    if e != E or n != N:
         raise ValueError(f"w must be [E={E}, N={N}, K], not {tuple(w.shape)}")
-    K = w.shape[2]
-    dx = dx if dx is not None else torch.empty((R, K), dtype=out_dtype or dy.dtype, device=dev)
-    _need(dx, "dx", (dy.dtype, torch.float32), (R, K), device=dev)
+    dx = _result(dx, "dx", (R, K), out_dtype or dt, (dt, torch.float32), dev)
     _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
     with _guard(dev):
-        _check(lib().moe_grouped_mm_dgrad(_ptr(dy), _ptr(w), _DT[dy.dtype], _ptr(offsets), R, E, N, K, _ptr(dx),
+        _check(lib().moe_grouped_mm_dgrad(_ptr(dy), _ptr(w), _DT[dt], _ptr(offsets), R, E, N, K, _ptr(dx),
                                           _DT[dx.dtype], _ptr(dev_status), _stream(stream, dev)),
                "moe_grouped_mm_dgrad")
     return dx
@@ -699,20 +710,18 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     """dw [E, N, K], the gradient of moe_grouped_mm's w: over each expert's
     rows the sum of dy [R, N] outer x [R, K].  accumulate adds it to the dw
     given."""
-    R, N = _rows2(dy, "dy", _DT16)
-    dev = dy.device
-    _need(x, "x", (dy.dtype,), device=dev)
-    if x.dim() != 2 or x.shape[0] != R:
+    R, N = _arg(dy, "dy", _DT16, 2)
+    dev, dt = dy.device, dy.dtype
+    r, K = _arg(x, "x", (dt,), 2, dev)
+    if r != R:
         raise ValueError(f"x must be [R={R}, K], not {tuple(x.shape)}")
-    K = x.shape[1]
     E = _groups(offsets, dev)
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
-    dw = dw if dw is not None else torch.empty((E, N, K), dtype=out_dtype, device=dev)
-    _need(dw, "dw", (dy.dtype, torch.float32), (E, N, K), device=dev)
+    dw = _result(dw, "dw", (E, N, K), out_dtype, (dt, torch.float32), dev)
     _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
     with _guard(dev):
-        _check(lib().moe_grouped_mm_wgrad(_ptr(dy), _ptr(x), _DT[dy.dtype], _ptr(offsets), R, E, N, K, _ptr(dw),
+        _check(lib().moe_grouped_mm_wgrad(_ptr(dy), _ptr(x), _DT[dt], _ptr(offsets), R, E, N, K, _ptr(dw),
                                           _DT[dw.dtype], 1 if accumulate else 0, _ptr(dev_status), _stream(stream, dev)),
                "moe_grouped_mm_wgrad")
     return dw
@@ -745,10 +754,10 @@ def _fp4_alpha(alpha, fmt, rows, dev):
         if alpha is not None:
             raise ValueError("alpha is only for NVFP4")
         return 1
-    _need(alpha, "alpha", _F32, min_numel=1, device=dev)
-    if rows % alpha.numel():
-        raise ValueError(f"alpha holds {alpha.numel()} entries, which do not divide the {rows} rows")
-    return alpha.numel()
+    n, = _arg(alpha, "alpha", _F32, 1, dev)
+    if n < 1 or rows % n:
+        raise ValueError(f"alpha holds {n} entries, which do not divide the {rows} rows")
+    return n
 
 
 @dataclasses.dataclass(frozen=True)
@@ -763,13 +772,17 @@ class Fp4:
     alpha: torch.Tensor | None = None
 
     def __post_init__(self):
-        q = _need(self.q, "fp4.q", _U8)
-        if q.dim() not in (2, 3):
-            raise ValueError(f"fp4.q must be [R, K/2] or [E, N, K/2], not {tuple(q.shape)}")
-        Ks = _fp4_shape(q.shape[-1] * 2, self.fmt, "fp4")
-        _need(self.s, "fp4.s", _U8, (*q.shape[:-1], Ks), device=q.device)
+        dim = 3 if isinstance(self.q, torch.Tensor) and self.q.dim() == 3 else 2
+        *lead, half = _arg(self.q, "fp4.q", _U8, dim)
+        dev = self.q.device
+        Ks = _fp4_shape(half * 2, self.fmt, "fp4")
+        *slead, cols = _arg(self.s, "fp4.s", _U8, dim, dev)
+        if slead != lead or cols != Ks:
+            raise ValueError(f"fp4.s has shape {tuple(self.s.shape)}; expected {(*lead, Ks)}")
         if self.fmt == MOE_FP4_NVFP4:
-            _need(self.alpha, "fp4.alpha", _F32, (q.shape[0] if q.dim() == 3 else 1,), device=q.device)
+            n, = _arg(self.alpha, "fp4.alpha", _F32, 1, dev)
+            if n != (lead[0] if dim == 3 else 1):
+                raise ValueError(f"fp4.alpha holds {n} entries; expected {lead[0] if dim == 3 else 1}")
         elif self.alpha is not None:
             raise ValueError("fp4.alpha is only for NVFP4")
 
@@ -778,15 +791,13 @@ def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stre
     """NVFP4 or MXFP4 codes and scales of v [..., K] (fp32, bf16 or fp16):
     (q uint8 [..., K/2], s uint8 [..., Ks]).  alpha (NVFP4): float32 [groups],
     each for an equal run of rows."""
-    _need(v, "v", tuple(_DT))
-    dev, K = v.device, v.shape[-1] if v.dim() else 0
+    *lead, K = _arg(v, "v", _DT, None)
+    dev = v.device
     Ks = _fp4_shape(K, fmt, "v")
     rows = v.numel() // K
     groups = _fp4_alpha(alpha, fmt, rows, dev)
-    q = q if q is not None else torch.empty((*v.shape[:-1], K // 2), dtype=torch.uint8, device=dev)
-    s = s if s is not None else torch.empty((*v.shape[:-1], Ks), dtype=torch.uint8, device=dev)
-    _need(q, "q", _U8, (*v.shape[:-1], K // 2), device=dev)
-    _need(s, "s", _U8, (*v.shape[:-1], Ks), device=dev)
+    q = _result(q, "q", (*lead, K // 2), torch.uint8, _U8, dev)
+    s = _result(s, "s", (*lead, Ks), torch.uint8, _U8, dev)
     with _guard(dev):
         _check(lib().moe_fp4_quantize(_ptr(v), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, _ptr(q), _ptr(s),
                                       _stream(stream, dev)), "moe_fp4_quantize")
@@ -796,14 +807,13 @@ def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stre
 def moe_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, fmt: int, alpha=None, out_dtype=torch.float32, v=None,
                        stream=None):
     """The values v [..., K] that codes and scales stand for."""
-    _need(q, "q", _U8)
-    dev, K = q.device, q.shape[-1] * 2 if q.dim() else 0
+    *lead, half = _arg(q, "q", _U8, None)
+    dev, K = q.device, half * 2
     Ks = _fp4_shape(K, fmt, "q")
-    _need(s, "s", _U8, (*q.shape[:-1], Ks), device=dev)
-    rows = q.numel() // (K // 2)
+    _need(s, "s", _U8, (*lead, Ks), device=dev)
+    rows = q.numel() // half
     groups = _fp4_alpha(alpha, fmt, rows, dev)
-    v = v if v is not None else torch.empty((*q.shape[:-1], K), dtype=out_dtype, device=dev)
-    _need(v, "v", tuple(_DT), (*q.shape[:-1], K), device=dev)
+    v = _result(v, "v", (*lead, K), out_dtype, _DT, dev)
     with _guard(dev):
         _check(lib().moe_fp4_dequantize(_ptr(q), _ptr(s), rows, K, fmt, _ptr(alpha), groups, _ptr(v), _DT[v.dtype],
                                         _stream(stream, dev)), "moe_fp4_dequantize")
@@ -820,11 +830,11 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
         raise ValueError("x must be [R, K] and w [E, N, K] of one format")
     if w.q.device != dev:
         raise ValueError(f"w is on {w.q.device}; the call's tensors are on {dev}")
-    R, N, K = x.q.shape[0], w.q.shape[1], w.q.shape[2] * 2
-    if w.q.shape[0] != E or x.q.shape[1] * 2 != K:
-        raise ValueError(f"w is [{w.q.shape[0]}, {N}, {K}]; offsets are for {E} experts and x has K = {x.q.shape[1] * 2}")
-    y = y if y is not None else torch.empty((R, N), dtype=out_dtype, device=dev)
-    _need(y, "y", tuple(_DT), (R, N), device=dev)
+    (R, xh), (e, N, half) = x.q.shape, w.q.shape
+    K = half * 2
+    if e != E or xh != half:
+        raise ValueError(f"w is [{e}, {N}, {K}]; offsets are for {E} experts and x has K = {xh * 2}")
+    y = _result(y, "y", (R, N), out_dtype, _DT, dev)
     _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
     with _guard(dev):
         _check(lib().moe_grouped_mm_fp4(_ptr(x.q), _ptr(x.s), _ptr(x.alpha), _ptr(w.q), _ptr(w.s), _ptr(w.alpha), x.fmt,

@@ -20,57 +20,80 @@
 namespace moe {
 namespace fp4 {
 
-// Every thread takes 32 consecutive elements of a row (one block of MXFP4, two
-// of NVFP4) with 16-byte loads, keeps them in registers and writes their 16
-// bytes of codes at once; a warp reads 2 or 4 KB in one go.  Both kernels are
-// streams: the conversions are a few instructions per element (packed cvt),
-// less than the memory time of the 16-bit types.
+// Both kernels are streams.  A lane takes 8 consecutive elements at a time, so
+// that a warp's loads and stores are whole lines whatever the alignment past 16
+// bytes, and has four such units under way; a block's two or four lanes agree
+// on its amax by shuffles.  (32 elements per lane, without shuffles but with
+// half-used sectors, took 408 us for 196608 x 2048 bf16 both ways.)
+constexpr int kUnits = 4;
+
 template <typename VT>
-struct Vec32 {
-    static constexpr int kWords = sizeof(VT) * 32 / 16;
-    uint4 w[kWords];
+struct Unit {
+    uint4 w[sizeof(VT) / 2];
 };
 
-__device__ __forceinline__ void unpack(const Vec32<float> &v, float (&x)[32])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[4 * i] = __uint_as_float(v.w[i].x);
-        x[4 * i + 1] = __uint_as_float(v.w[i].y);
-        x[4 * i + 2] = __uint_as_float(v.w[i].z);
-        x[4 * i + 3] = __uint_as_float(v.w[i].w);
-    }
-}
-
-template <typename VT>
-__device__ __forceinline__ void unpack(const Vec32<VT> &v, float (&x)[32])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {v.w[i].x, v.w[i].y, v.w[i].z, v.w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (std::is_same<VT, __half>::value)
-                f16x2_to_float(w[j], x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-            else
-                bf16x2_to_float(w[j], x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-        }
-    }
-}
-
-// The largest magnitude's bits of B values.
-template <int B>
-__device__ __forceinline__ uint32_t amax_bits(const float *x)
+// A unit's largest magnitude, as the bits of its type (two halves of a word for
+// the 16-bit types, to be folded after the shuffles), and its values.
+__device__ __forceinline__ uint32_t amax_bits(const Unit<float> &u)
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < B; ++i)
-        m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 2; ++i)
+        m = max(m, max(max(u.w[i].x & 0x7FFFFFFFu, u.w[i].y & 0x7FFFFFFFu), max(u.w[i].z & 0x7FFFFFFFu, u.w[i].w & 0x7FFFFFFFu)));
     return m;
 }
 
+template <typename VT>
+__device__ __forceinline__ uint32_t amax_bits(const Unit<VT> &u)
+{
+    constexpr uint32_t k = 0x7FFF7FFFu;
+    return __vmaxu2(__vmaxu2(u.w[0].x & k, u.w[0].y & k), __vmaxu2(u.w[0].z & k, u.w[0].w & k));
+}
+
+template <typename VT>
+__device__ __forceinline__ uint32_t amax_join(uint32_t a, uint32_t b)
+{
+    return sizeof(VT) == 4 ? max(a, b) : __vmaxu2(a, b);
+}
+
+// The FP32 bits of an amax.
+template <typename VT>
+__device__ __forceinline__ uint32_t amax_float(uint32_t a)
+{
+    if constexpr (sizeof(VT) == 4)
+        return a;
+    a = max(a & 0xFFFFu, a >> 16);
+    if constexpr (std::is_same<VT, __half>::value)
+        return __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(a))));
+    return a << 16;
+}
+
+__device__ __forceinline__ void unpack(const Unit<float> &u, float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x[4 * i] = __uint_as_float(u.w[i].x);
+        x[4 * i + 1] = __uint_as_float(u.w[i].y);
+        x[4 * i + 2] = __uint_as_float(u.w[i].z);
+        x[4 * i + 3] = __uint_as_float(u.w[i].w);
+    }
+}
+
+template <typename VT>
+__device__ __forceinline__ void unpack(const Unit<VT> &u, float (&x)[8])
+{
+    const uint32_t w[4] = {u.w[0].x, u.w[0].y, u.w[0].z, u.w[0].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (std::is_same<VT, __half>::value)
+            f16x2_to_float(w[j], x[2 * j], x[2 * j + 1]);
+        else
+            bf16x2_to_float(w[j], x[2 * j], x[2 * j + 1]);
+    }
+}
+
 // 8 values onto the E2M1 grid: one 32-bit word of codes.
-__device__ __forceinline__ uint32_t codes8(const float *x, float inv)
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float inv)
 {
     uint32_t r;
     asm("{\n .reg .b8 a, b, c, d;\n"
@@ -83,98 +106,126 @@ __device__ __forceinline__ uint32_t codes8(const float *x, float inv)
     return r;
 }
 
+// Row and 32-element piece of the row of a lane's units: one division for the
+// first, steps of 8 pieces (32 units) after it.
+struct Place {
+    uint32_t row, piece;
+    __device__ __forceinline__ Place(uint32_t p, uint32_t nq) : row(p / nq), piece(p - row * nq) {}
+    __device__ __forceinline__ void step(uint32_t nq)
+    {
+        piece += 8;
+        while (piece >= nq) {
+            piece -= nq;
+            ++row;
+        }
+    }
+};
+
 template <typename VT, int FMT>
 __global__ void __launch_bounds__(256)
-quantize_kernel(const VT *__restrict__ v, int64_t rows, int nq, int Ks, const float *__restrict__ alpha,
-                int64_t rows_per_alpha, uint4 *__restrict__ q, uint8_t *__restrict__ s)
+quantize_kernel(const VT *__restrict__ v, int64_t units, uint32_t nq, int Ks, const float *__restrict__ alpha,
+                uint32_t rows_per_alpha, uint32_t *__restrict__ q, uint8_t *__restrict__ s)
 {
-    // nq 32-element pieces in a row; the row's scale bytes past its blocks are
-    // zeroed by the threads past them
-    constexpr int kPer = 32 / block_of(FMT);              // scale bytes of a piece
-    const int np = Ks / kPer;
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < rows * np;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = i / np;
-        const int c = static_cast<int>(i - r * np);
-        uint32_t bytes = 0;
-        if (c < nq) {
-            Vec32<VT> in;
-            const uint4 *p = reinterpret_cast<const uint4 *>(v) + (r * nq + c) * Vec32<VT>::kWords;
+    constexpr int kLanes = block_of(FMT) / 8, kPer = 32 / block_of(FMT);
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+    for (int64_t base = (blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)) * (32 * kUnits); base < units;
+         base += warps * (32 * kUnits)) {
+        Unit<VT> in[kUnits];
 #pragma unroll
-            for (int k = 0; k < Vec32<VT>::kWords; ++k)
-                in.w[k] = ld_stream_u4(p + k);
-            float x[32];
-            unpack(in, x);
-            uint32_t w[4];
-            if constexpr (FMT == MOE_FP4_NVFP4) {
-                const float a = __ldg(alpha + r / rows_per_alpha), g = 1.0f / (6.0f * a);
+        for (int j = 0; j < kUnits; ++j) {
+            const int64_t u = base + 32 * j + lane;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float inv;
-                    const uint32_t b = block_scale_nv(amax_bits<16>(x + 16 * h), a, g, inv);
-                    bytes |= b << (8 * h);
-                    w[2 * h] = b == 0x7Fu ? 0u : codes8(x + 16 * h, inv);
-                    w[2 * h + 1] = b == 0x7Fu ? 0u : codes8(x + 16 * h + 8, inv);
-                }
-            } else {
-                float inv;
-                bytes = block_scale_mx(amax_bits<32>(x), inv);
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    w[h] = bytes == 0xFFu ? 0u : codes8(x + 8 * h, inv);
-            }
-            q[r * nq + c] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < static_cast<int>(sizeof(VT) / 2); ++k)
+                in[j].w[k] = u < units ? ld_stream_u4(reinterpret_cast<const uint4 *>(v) + u * (sizeof(VT) / 2) + k)
+                                       : make_uint4(0, 0, 0, 0);
         }
-        if constexpr (kPer == 2)
-            reinterpret_cast<uint16_t *>(s)[i] = static_cast<uint16_t>(bytes);
-        else
-            s[i] = static_cast<uint8_t>(bytes);
+        Place at(static_cast<uint32_t>((base + lane) >> 2), nq);
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j, at.step(nq)) {
+            const int64_t u = base + 32 * j + lane;
+            uint32_t m = amax_bits(in[j]);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+                m = amax_join<VT>(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = amax_float<VT>(m);
+            if (u < units) {
+                float inv;
+                uint32_t byte;
+                if constexpr (FMT == MOE_FP4_NVFP4) {
+                    const float a = __ldg(alpha + at.row / rows_per_alpha);
+                    byte = block_scale_nv(m, a, 1.0f / (6.0f * a), inv);
+                } else {
+                    byte = block_scale_mx(m, inv);
+                }
+                float x[8];
+                unpack(in[j], x);
+                q[u] = m >= 0x7F800000u ? 0u : codes8(x, inv);
+                if ((lane & (kLanes - 1)) == 0) {
+                    uint8_t *row = s + static_cast<int64_t>(at.row) * Ks;
+                    const int b = at.piece * kPer + (kPer == 2 ? (lane >> 1) & 1 : 0);
+                    row[b] = static_cast<uint8_t>(byte);
+                    if (b == static_cast<int>(nq) * kPer - 1)      // the last block zeroes the row's padding
+                        for (int i = b + 1; i < Ks; ++i)
+                            row[i] = 0;
+                }
+            }
+        }
     }
 }
 
 template <typename VT, int FMT>
 __global__ void __launch_bounds__(256)
-dequantize_kernel(const uint4 *__restrict__ q, const uint8_t *__restrict__ s, int64_t rows, int nq, int Ks,
-                  const float *__restrict__ alpha, int64_t rows_per_alpha, VT *__restrict__ v)
+dequantize_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ s, int64_t units, uint32_t nq, int Ks,
+                  const float *__restrict__ alpha, uint32_t rows_per_alpha, VT *__restrict__ v)
 {
     constexpr int kPer = 32 / block_of(FMT);
-    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < rows * nq;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = i / nq;
-        const int c = static_cast<int>(i - r * nq);
-        const uint4 in = ld_stream_u4(q + i);
-        const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-        const float a = FMT == MOE_FP4_NVFP4 ? __ldg(alpha + r / rows_per_alpha) : 1.f;
-        float f[kPer];
-        if constexpr (kPer == 2) {
-            const uint32_t b = reinterpret_cast<const uint16_t *>(s + r * Ks)[c];
-            f[0] = ue4m3_value(b & 0xFFu);
-            f[1] = ue4m3_value(b >> 8);
-        } else {
-            f[0] = scale_value<FMT>(s[r * Ks + c]);
-        }
-        uint4 *o = reinterpret_cast<uint4 *>(v) + i * Vec32<VT>::kWords;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+    for (int64_t base = (blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)) * (32 * kUnits); base < units;
+         base += warps * (32 * kUnits)) {
+        uint32_t c[kUnits];
+        float f[kUnits], al[kUnits];
+        Place at(static_cast<uint32_t>((base + lane) >> 2), nq);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {                       // 8 elements, a word of codes
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 e = e2m1_values((w[h] >> (8 * j)) & 0xFFu);
-                x[2 * j] = e.x * f[h * kPer / 4] * a;
-                x[2 * j + 1] = e.y * f[h * kPer / 4] * a;
+        for (int j = 0; j < kUnits; ++j, at.step(nq)) {
+            const int64_t u = base + 32 * j + lane;
+            if (u < units) {
+                c[j] = __ldcs(q + u);
+                f[j] = scale_value<FMT>(s[static_cast<int64_t>(at.row) * Ks + at.piece * kPer + (kPer == 2 ? (lane >> 1) & 1 : 0)]);
+                al[j] = FMT == MOE_FP4_NVFP4 ? __ldg(alpha + at.row / rows_per_alpha) : 1.f;
             }
-            if constexpr (sizeof(VT) == 4) {
-                o[2 * h] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-                o[2 * h + 1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
-            } else {
-                o[h] = make_uint4(gmm::pack2<VT>(x[0], x[1]), gmm::pack2<VT>(x[2], x[3]), gmm::pack2<VT>(x[4], x[5]),
-                                  gmm::pack2<VT>(x[6], x[7]));
+        }
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int64_t u = base + 32 * j + lane;
+            if (u < units) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = e2m1_values((c[j] >> (8 * i)) & 0xFFu);
+                    x[2 * i] = e.x * f[j] * al[j];
+                    x[2 * i + 1] = e.y * f[j] * al[j];
+                }
+                uint4 *o = reinterpret_cast<uint4 *>(v) + u * (sizeof(VT) / 2);
+                if constexpr (sizeof(VT) == 4) {
+                    __stcs(o, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
+                    __stcs(o + 1, make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7])));
+                } else {
+                    __stcs(o, make_uint4(gmm::pack2<VT>(x[0], x[1]), gmm::pack2<VT>(x[2], x[3]), gmm::pack2<VT>(x[4], x[5]),
+                                         gmm::pack2<VT>(x[6], x[7])));
+                }
             }
         }
     }
 }
 
-constexpr int64_t kMostBlocks = 152 * 64;
+// One warp takes 32 * kUnits units of 8 elements.
+static int grid_of(int64_t units)
+{
+    const int64_t blocks = (units + 32 * kUnits * 8 - 1) / (32 * kUnits * 8);
+    return static_cast<int>(blocks < 152 * 64 ? blocks : 152 * 64);
+}
 
 template <typename F>
 static bool by_type(int32_t dt, F f)
@@ -200,6 +251,8 @@ static moe_status_t check(const void *v, int32_t vdt, int64_t rows, int32_t K, i
         return MOE_ERR_UNSUPPORTED;
     if ((fmt == MOE_FP4_NVFP4) != (alpha != nullptr) && rows)
         return MOE_ERR_INVALID_ARG;
+    if (rows * (K / 32) > UINT32_MAX)
+        return MOE_ERR_UNSUPPORTED;
     if (rows && (!v || !q || !s || !aligned(v, 16) || !aligned(q, 16) || !aligned(s, 16)))
         return MOE_ERR_INVALID_ARG;
     return MOE_OK;
@@ -227,14 +280,13 @@ MOE_API moe_status_t moe_fp4_quantize(const void *v, int32_t vdt, int64_t rows, 
     const moe_status_t st = check(v, vdt, rows, K, fmt, alpha, groups, q, s);
     if (st != MOE_OK || rows == 0)
         return st;
-    const int Ks = scale_cols(K, fmt), np = Ks * block_of(fmt) / 32;
-    const int64_t blocks = (rows * np + 255) / 256;
-    const int grid = static_cast<int>(blocks < kMostBlocks ? blocks : kMostBlocks);
+    const int64_t units = rows * (K / 8);
     by_type(vdt, [&](auto t) {
         using T = decltype(t);
         auto k = fmt == MOE_FP4_NVFP4 ? quantize_kernel<T, MOE_FP4_NVFP4> : quantize_kernel<T, MOE_FP4_MXFP4>;
-        k<<<grid, 256, 0, as_stream(stream)>>>(static_cast<const T *>(v), rows, K / 32, Ks, alpha, rows / groups,
-                                               reinterpret_cast<uint4 *>(q), s);
+        k<<<grid_of(units), 256, 0, as_stream(stream)>>>(static_cast<const T *>(v), units, K / 32, scale_cols(K, fmt), alpha,
+                                                         static_cast<uint32_t>(rows / groups),
+                                                         reinterpret_cast<uint32_t *>(q), s);
     });
     return launch_status();
 }
@@ -245,14 +297,13 @@ MOE_API moe_status_t moe_fp4_dequantize(const uint8_t *q, const uint8_t *s, int6
     const moe_status_t st = check(v, vdt, rows, K, fmt, alpha, groups, q, s);
     if (st != MOE_OK || rows == 0)
         return st;
-    const int Ks = scale_cols(K, fmt);
-    const int64_t blocks = (rows * (K / 32) + 255) / 256;
-    const int grid = static_cast<int>(blocks < kMostBlocks ? blocks : kMostBlocks);
+    const int64_t units = rows * (K / 8);
     by_type(vdt, [&](auto t) {
         using T = decltype(t);
         auto k = fmt == MOE_FP4_NVFP4 ? dequantize_kernel<T, MOE_FP4_NVFP4> : dequantize_kernel<T, MOE_FP4_MXFP4>;
-        k<<<grid, 256, 0, as_stream(stream)>>>(reinterpret_cast<const uint4 *>(q), s, rows, K / 32, Ks, alpha,
-                                               rows / groups, static_cast<T *>(v));
+        k<<<grid_of(units), 256, 0, as_stream(stream)>>>(reinterpret_cast<const uint32_t *>(q), s, units, K / 32,
+                                                         scale_cols(K, fmt), alpha, static_cast<uint32_t>(rows / groups),
+                                                         static_cast<T *>(v));
     });
     return launch_status();
 }
