@@ -22,9 +22,9 @@
 // MMA steps past them are left out.
 //
 // Roles: warp 0 loads (TMA, 128-byte swizzle, a ring of 6 stages of 64 along
-// the contraction), warp 1 of the pair's leader issues the MMAs into two
-// accumulators of 256 TMEM columns, warps 2..5 drain one while the next tile
-// fills the other, warp 6 zeroes wgrad's row tails.  Every wait is bounded; an
+// the contraction, 5 for wgrad), warp 1 of the pair's leader issues the MMAs into two
+// accumulators of 256 TMEM columns, warps 4..7 drain one while the next tile
+// fills the other, warp 2 zeroes wgrad's row tails.  Every wait is bounded; an
 // expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
 #include <cuda.h>
 
@@ -41,10 +41,18 @@ namespace gmm {
 
 enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kStages = 6;                     // of the ring; wgrad has 5, and 8 staging tiles in the last one's place
 constexpr int kStageBytes = 32768;             // 128 x 64 of each operand, 16 bits
+constexpr int kMaxStages = 6;
+
+// Ring stages, and bytes of each draining warp's staging tiles: wgrad writes far
+// more per tile of MMA work and has two tiles of 128-byte rows in place of a
+// stage (4 stages: 8 to 12 % slower where the MMAs bound it; 64-byte rows or
+// one tile: 10 to 25 % slower where dw does).
 constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
-constexpr int kThreads = 224;
+constexpr int staging_of(int op) { return op == kWgrad ? 8192 : 4096; }
+constexpr int kDrain = 4;                      // draining warps, one to a quadrant of tensor memory
+constexpr int kThreads = 32 * (4 + kDrain);
+
 constexpr int kTileM = 256, kTileN = 256, kStep = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -62,15 +70,17 @@ struct Args {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], tail[kStages], peer[kStages], accf[2], acce[2];
+    uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer[kMaxStages], accf[2], acce[2];
     uint32_t tmem;
     int abort;
     ragged::List list;
 };
 
-constexpr int kDrainBytes = 16384;             // four warps' staging tiles (fwd, dgrad)
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kDrainBytes + static_cast<int>(sizeof(Shared));
-static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+constexpr int smem_of(int op)
+{
+    return 1024 + stages_of(op) * kStageBytes + kDrain * staging_of(op) + static_cast<int>(sizeof(Shared));
+}
+static_assert(smem_of(kFwd) <= 232448 && smem_of(kWgrad) <= 232448, "shared memory of one CTA");
 
 struct Tile {
     int e, m0, lo, rows;       // expert, first left row, the expert's rows
@@ -136,15 +146,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
     // tmB16: B in boxes of 16 rows (fwd, dgrad); tmY: the result
+    constexpr int kStages = stages_of(OP);
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const uint32_t raw = tc::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);      // the same offset in both CTAs
     const uint32_t ring = tc::smem_u32(smem);
-    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes + kDrainBytes);
+    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes + kDrain * staging_of(OP));
     volatile int *abort = &s.abort;
-    constexpr int kRing = stages_of(OP);
     auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
 
     if (threadIdx.x == 0) {
@@ -156,7 +166,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(s.accf[i]), 1);
-            tc::mbar_init(bar(s.acce[i]), 8);          // four drain warps of each CTA
+            tc::mbar_init(bar(s.acce[i]), 2 * kDrain); // of both CTAs
         }
         s.abort = 0;
         tc::fence_mbar_init();
@@ -235,7 +245,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             for (int i = 0; i < nh; i += 16)
                                 tc::tma_load_2d_pair(sb + i * 128, &tmB16, j * kStep, r0 + i, fb);
                     }
-                    if (++st == kRing) {
+                    if (++st == kStages) {
                         st = 0;
                         ph ^= 1u;
                     }
@@ -245,8 +255,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             // over at once unless a role gave up)
             if (rank == 0) {
                 volatile int never = 0;
-                for (int i = 1; i <= min(issued, kRing); ++i) {
-                    const int q = st - i < 0 ? st - i + kRing : st - i;
+                for (int i = 1; i <= min(issued, kStages); ++i) {
+                    const int q = st - i < 0 ? st - i + kStages : st - i;
                     tc::mbar_wait(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
                 }
             }
@@ -284,7 +294,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         if (OP != kWgrad || kk < nk)
                             tc::mma_f16_pair(acc, ad + kk * kAStep, bd + kk * kBStep, id, (j | kk) != 0 ? 1u : 0u);
                     tc::tc_commit_pair(bar(s.empty[st]));
-                    if (++st == kRing) {
+                    if (++st == kStages) {
                         st = 0;
                         ph ^= 1u;
                     }
@@ -292,7 +302,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 tc::tc_commit_pair(bar(s.accf[buf]));
             }
         }
-    } else if (warp == 6) {
+    } else if (warp == 2) {
         if (OP == kWgrad) {
             // zero the last step's rows past the expert's, up to the next 16
             int st = 0;
@@ -301,8 +311,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
                 if (T.steps == 0)
                     continue;
-                const int q = (st + T.steps - 1) % kRing;
-                st = (st + T.steps) % kRing;
+                const int q = (st + T.steps - 1) % kStages;
+                st = (st + T.steps) % kStages;
                 if (!(T.rows & 15))
                     continue;
                 const uint32_t ph = (phases >> q) & 1u;
@@ -327,10 +337,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
             }
         }
-    } else {
+    } else if (warp >= 4) {
         const int q = warp & 3;                         // TMEM lane quadrant
         int tix = 0, flip = 0;
         OT *out = static_cast<OT *>(a.out);
+        uint8_t *tiles = smem + kStages * kStageBytes + (warp - 4) * staging_of(OP);
         for (int t = cid; t < total; t += n_cl) {
             const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
             const int m = T.m0 + 128 * rank + 32 * q + lane;
@@ -374,7 +385,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                                 T.n - c0 - 32 * h, w + 16 * h);
                             }
                         }
-                        uint8_t *tile = smem + kRing * kStageBytes + (q * 2 + flip) * 4096;
+                        uint8_t *tile = tiles + flip * 4096;
                         flip ^= 1;
                         tc::bulk_wait_read<1>();            // the store of two chunks ago has read this tile
                         __syncwarp();
@@ -392,7 +403,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                 }
             } else {
-                uint8_t *tiles = smem + kStages * kStageBytes + q * 4096;
                 for (int c0 = 0; c0 < T.n; c0 += 32) {
                     uint32_t v[32];
                     tc::tmem_ld_32x32b_x32(acc + c0, v);
@@ -418,14 +428,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const int first = min(max(a.off[0], 0), a.R), last = min(max(a.off[a.E], 0), a.R);
             const int64_t per = static_cast<int64_t>(a.M) * sizeof(OT) / 16;
             uint4 *o = static_cast<uint4 *>(a.out);
-            const int64_t at = static_cast<int64_t>(blockIdx.x) * 128 + (threadIdx.x - 64), by = static_cast<int64_t>(gridDim.x) * 128;
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * (32 * kDrain) + (threadIdx.x - 128);
+            const int64_t by = static_cast<int64_t>(gridDim.x) * (32 * kDrain);
             for (int64_t i = at; i < first * per; i += by)
                 o[i] = make_uint4(0, 0, 0, 0);
             for (int64_t i = last * per + at; i < a.R * per; i += by)
                 o[i] = make_uint4(0, 0, 0, 0);
         }
         if (blockIdx.x == 0)
-            for (int e = threadIdx.x - 64; e < a.E; e += 128)
+            for (int e = threadIdx.x - 128; e < a.E; e += 32 * kDrain)
                 ragged::report_bad(a.off, a.R, e, a.dev_status);
     }
     __syncwarp();
@@ -463,11 +474,11 @@ static moe_status_t launch(const CUtensorMap (&tm)[4], const Args &a, int64_t mo
 {
     auto k = gemm_kernel<OP, OT>;
     static std::atomic<uint64_t> done{0};
-    if (!smem_attr_once(done, reinterpret_cast<const void *>(k), kSmemBytes))
+    if (!smem_attr_once(done, reinterpret_cast<const void *>(k), smem_of(OP)))
         return MOE_ERR_CUDA;
     const int pairs = device_sm_count() / 2;
     const int grid = 2 * static_cast<int>(most_tiles < pairs ? most_tiles : pairs);
-    return launch_pdl(k, dim3(grid), dim3(kThreads), kSmemBytes, s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
+    return launch_pdl(k, dim3(grid), dim3(kThreads), smem_of(OP), s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
                                                                                                             : MOE_ERR_CUDA;
 }
 
