@@ -1,0 +1,135 @@
+"""The ragged expert layer (top_moe_expert_gb300.ragged): routing to groups, its outputs and gradients against a 64-bit
+layer, the 4-bit layer against a 64-bit layer on the same codes, and a captured training step."""
+import pytest
+import torch
+
+import top_moe_expert_gb300 as moe
+from tests import ragged_ref as ref
+from top_moe_expert_gb300 import ragged
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def _layer64(x, ids, w, w13, w2, h_round=lambda h: h):
+    """The layer in float64, by token and slot; leaves of autograd where they require gradients."""
+    E = w13.shape[0]
+    ys = []
+    for t in range(x.shape[0]):
+        y = torch.zeros(w2.shape[1], dtype=torch.float64)
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if 0 <= e < E:
+                g, u = (w13[e] @ x[t]).chunk(2)
+                y = y + w[t, j] * (w2[e] @ h_round(torch.nn.functional.silu(g) * u))
+        ys.append(y)
+    return torch.stack(ys)
+
+
+def test_group_routes():
+    g = torch.Generator().manual_seed(1)
+    M, k, E = 37, 3, 11
+    ids = torch.randint(-1, E + 1, (M, k), generator=g, dtype=torch.int32)     # -1 and E are invalid
+    gr = ragged.group_routes(ids.cuda(), E)
+    valid = (ids >= 0) & (ids < E)
+    counts = [int((ids[valid] == e).sum()) for e in range(E)]
+    assert gr.offsets.tolist() == ref.offsets_of(counts).tolist() and gr.offsets.dtype == torch.int32
+    flat = ids.flatten().tolist()
+    order = sorted((i for i in range(M * k) if 0 <= flat[i] < E), key=lambda i: (flat[i], i))
+    assert gr.token[:len(order)].tolist() == [i // k for i in order]
+    row = gr.row.flatten().tolist()
+    assert all(row[i] == r for r, i in enumerate(order)) and all(row[i] == M * k for i in range(M * k) if not 0 <= flat[i] < E)
+
+
+def _problem(M, E, k, d, I, seed, invalid):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((M, d), generator=g).to(BF)
+    w13 = (torch.randn((E, 2 * I, d), generator=g) * d ** -0.5).to(BF)
+    w2 = (torch.randn((E, d, I), generator=g) * I ** -0.5).to(BF)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(M)]).to(torch.int32)
+    if invalid:
+        ids[::5, 0], ids[3] = -1, E
+    w = torch.rand((M, k), generator=g)
+    return x, ids, w, w13, w2
+
+
+@pytest.mark.parametrize("M,E,k,d,I,invalid", [(1, 4, 2, 64, 32, False), (23, 6, 3, 136, 72, True), (70, 5, 2, 128, 64, False)])
+def test_layer_and_gradients(M, E, k, d, I, invalid):
+    x, ids, w, w13, w2 = _problem(M, E, k, d, I, M, invalid)
+    leaves = [t.cuda().requires_grad_() for t in (x, w, w13, w2)]
+    y = ragged.expert_layer(leaves[0], ids.cuda(), *leaves[1:])
+    dy = torch.randn((M, d), generator=torch.Generator().manual_seed(9))
+    (y * dy.cuda()).sum().backward()
+    want = [t.double().requires_grad_() for t in (x, w, w13, w2)]
+    y64 = _layer64(want[0], ids, *want[1:])
+    (y64 * dy.double()).sum().backward()
+    # roundings to bf16 on the way: the two products' outputs, h and, backward, their gradients -- each at most 2^-9 of its
+    # value (half a step), a handful of them in any path; 12 of them bound the relative 2-norm of every result
+    for got, exp in ((y, y64), *((a.grad, b.grad) for a, b in zip(leaves, want))):
+        rel = float((got.detach().cpu().double() - exp.detach()).norm() / exp.detach().norm())
+        assert rel <= 12 * 2.0 ** -9, rel
+    if invalid:
+        assert not y[3].any() and not leaves[0].grad[3].any()
+
+
+@pytest.mark.parametrize("fmt", [moe.MOE_FP4_NVFP4, moe.MOE_FP4_MXFP4])
+def test_fp4_layer_on_the_same_codes(fmt):
+    """x and the weights as their codes stand; h is quantized by the layer, compared through the same quantizer."""
+    M, E, k, d, I = 21, 5, 2, 128, 64
+    x, ids, w, w13, w2 = _problem(M, E, k, d, I, 3, True)
+    nv = fmt == moe.MOE_FP4_NVFP4
+    q13, q2 = ragged.quantize_experts(w13.cuda(), fmt), ragged.quantize_experts(w2.cuda(), fmt)
+    ax = ragged.tensor_alpha(x.cuda()) if nv else None
+    ah = torch.full((1,), 0.002, device="cuda") if nv else None
+    y = ragged.expert_layer_fp4(x.cuda(), ids.cuda(), w.cuda(), q13, q2, ax, ah).cpu().double()
+
+    def back(q):
+        v = torch.from_numpy(ref.values(q.q.cpu(), q.s.cpu(), fmt))
+        return v * q.alpha.cpu().double().view(-1, 1, 1) if nv else v
+
+    xq, xs = ref.quantize(x.double().numpy(), fmt, ax.cpu().numpy() if nv else None)
+    xv = torch.from_numpy(ref.values(xq, xs, fmt)) * (float(ax) if nv else 1.0)
+
+    def h_round(h):
+        q, s = ref.quantize(h.float().double().numpy()[None], fmt, ah.cpu().numpy() if nv else None)
+        return torch.from_numpy(ref.values(q, s, fmt))[0] * (float(ah) if nv else 1.0)
+
+    want = _layer64(xv, ids, w.double(), back(q13), back(q2), h_round)
+    # h differs by FP32 rounding, so a few of its values may fall on the other side of a 4-bit border (a step there is up to
+    # a third of the value): allow one value in 50, whose squares add up to (1/3)^2 / 50 of h's
+    rel = float((y - want).norm() / want.norm())
+    assert rel <= (1 / 3) * 50 ** -0.5, rel
+    assert not y[3].any()
+
+
+def test_captured_training_step_matches_eager():
+    """Forward, loss and backward of fresh leaves in a graph: the same bits as eager, and the replay follows new inputs."""
+    M, E, k, d, I = 40, 4, 2, 128, 64
+    x, ids, w, w13, w2 = _problem(M, E, k, d, I, 5, False)
+    ids, w = ids.cuda(), w.cuda()
+
+    def eager(x):
+        leaves = [t.cuda().requires_grad_() for t in (x, w13, w2)]
+        ragged.expert_layer(leaves[0], ids, w, *leaves[1:]).square().sum().backward()
+        return [t.grad.clone() for t in leaves]
+
+    want = eager(x), eager(-x + 1)
+    xs = x.cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):                                  # warm-up on the capture's stream, its graph freed
+        eager(x)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    leaves = [xs.requires_grad_(), w13.cuda().requires_grad_(), w2.cuda().requires_grad_()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ragged.expert_layer(leaves[0], ids, w, *leaves[1:]).square().sum()
+        grads = torch.autograd.grad(out, leaves)
+        del out
+    for new, exp in ((x, want[0]), (-x + 1, want[1])):
+        with torch.no_grad():
+            leaves[0].copy_(new)
+        graph.replay()
+        for a, b in zip(grads, exp):
+            assert torch.equal(a, b)
