@@ -650,6 +650,25 @@ def _arg(t, name: str, dtypes, dim, device=None):
     return t.shape
 
 
+def _launch(dev, name: str, *args) -> None:
+    """The entry point `name` with dev current; raises on a refusal."""
+    fn = getattr(lib(), name)
+    if dev.type == "cuda" and dev.index != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    else:
+        status = fn(*args)
+    if status != MOE_OK:
+        raise MoeError(status, name)
+
+
+def _status(dev_status, dev):
+    """Check dev_status; returns its address (None without one)."""
+    if dev_status is None:
+        return None
+    return _need(dev_status, "dev_status", _IDS, min_numel=2, device=dev).data_ptr()
+
+
 def _groups(offsets, dev) -> int:
     """Check the group offsets; returns the number of experts."""
     n, = _arg(offsets, "offsets", _IDS, 1, dev)
@@ -679,10 +698,8 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_
     if e != E or k != K:
         raise ValueError(f"w must be [E={E}, N, K={K}], not {tuple(w.shape)}")
     y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev)
-    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
-    with _guard(dev):
-        _check(lib().moe_grouped_mm(_ptr(x), _ptr(w), _DT[dt], _ptr(offsets), R, E, N, K, _ptr(y), _DT[y.dtype],
-                                    _ptr(dev_status), _stream(stream, dev)), "moe_grouped_mm")
+    _launch(dev, "moe_grouped_mm", x.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K, y.data_ptr(),
+            _DT[y.dtype], _status(dev_status, dev), _stream(stream, dev))
     return y
 
 
@@ -697,11 +714,8 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     if e != E or n != N:
         raise ValueError(f"w must be [E={E}, N={N}, K], not {tuple(w.shape)}")
     dx = _result(dx, "dx", (R, K), out_dtype or dt, (dt, torch.float32), dev)
-    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
-    with _guard(dev):
-        _check(lib().moe_grouped_mm_dgrad(_ptr(dy), _ptr(w), _DT[dt], _ptr(offsets), R, E, N, K, _ptr(dx),
-                                          _DT[dx.dtype], _ptr(dev_status), _stream(stream, dev)),
-               "moe_grouped_mm_dgrad")
+    _launch(dev, "moe_grouped_mm_dgrad", dy.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
+            dx.data_ptr(), _DT[dx.dtype], _status(dev_status, dev), _stream(stream, dev))
     return dx
 
 
@@ -719,11 +733,8 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
     dw = _result(dw, "dw", (E, N, K), out_dtype, (dt, torch.float32), dev)
-    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
-    with _guard(dev):
-        _check(lib().moe_grouped_mm_wgrad(_ptr(dy), _ptr(x), _DT[dt], _ptr(offsets), R, E, N, K, _ptr(dw),
-                                          _DT[dw.dtype], 1 if accumulate else 0, _ptr(dev_status), _stream(stream, dev)),
-               "moe_grouped_mm_wgrad")
+    _launch(dev, "moe_grouped_mm_wgrad", dy.data_ptr(), x.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
+            dw.data_ptr(), _DT[dw.dtype], 1 if accumulate else 0, _status(dev_status, dev), _stream(stream, dev))
     return dw
 
 
@@ -798,9 +809,8 @@ def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stre
     groups = _fp4_alpha(alpha, fmt, rows, dev)
     q = _result(q, "q", (*lead, K // 2), torch.uint8, _U8, dev)
     s = _result(s, "s", (*lead, Ks), torch.uint8, _U8, dev)
-    with _guard(dev):
-        _check(lib().moe_fp4_quantize(_ptr(v), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, _ptr(q), _ptr(s),
-                                      _stream(stream, dev)), "moe_fp4_quantize")
+    _launch(dev, "moe_fp4_quantize", v.data_ptr(), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, q.data_ptr(),
+            s.data_ptr(), _stream(stream, dev))
     return q, s
 
 
@@ -814,9 +824,8 @@ def moe_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, fmt: int, alpha=None, o
     rows = q.numel() // half
     groups = _fp4_alpha(alpha, fmt, rows, dev)
     v = _result(v, "v", (*lead, K), out_dtype, _DT, dev)
-    with _guard(dev):
-        _check(lib().moe_fp4_dequantize(_ptr(q), _ptr(s), rows, K, fmt, _ptr(alpha), groups, _ptr(v), _DT[v.dtype],
-                                        _stream(stream, dev)), "moe_fp4_dequantize")
+    _launch(dev, "moe_fp4_dequantize", q.data_ptr(), s.data_ptr(), rows, K, fmt, _ptr(alpha), groups, v.data_ptr(),
+            _DT[v.dtype], _stream(stream, dev))
     return v
 
 
@@ -835,9 +844,7 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
     if e != E or xh != half:
         raise ValueError(f"w is [{e}, {N}, {K}]; offsets are for {E} experts and x has K = {xh * 2}")
     y = _result(y, "y", (R, N), out_dtype, _DT, dev)
-    _opt(dev_status, "dev_status", dtypes=_IDS, min_numel=2, device=dev)
-    with _guard(dev):
-        _check(lib().moe_grouped_mm_fp4(_ptr(x.q), _ptr(x.s), _ptr(x.alpha), _ptr(w.q), _ptr(w.s), _ptr(w.alpha), x.fmt,
-                                        _ptr(offsets), R, E, N, K, _ptr(y), _DT[y.dtype], _ptr(dev_status),
-                                        _stream(stream, dev)), "moe_grouped_mm_fp4")
+    _launch(dev, "moe_grouped_mm_fp4", x.q.data_ptr(), x.s.data_ptr(), _ptr(x.alpha), w.q.data_ptr(), w.s.data_ptr(),
+            _ptr(w.alpha), x.fmt, offsets.data_ptr(), R, E, N, K, y.data_ptr(), _DT[y.dtype], _status(dev_status,
+            dev), _stream(stream, dev))
     return y
