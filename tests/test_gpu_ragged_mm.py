@@ -63,6 +63,31 @@ def test_exact_on_small_integers(name, N, K):
     assert st.tolist() == [0, 0]
 
 
+@pytest.mark.parametrize("sizes", [[1], [4], [0, 2, 0, 2], [1, 0, 3], [1, 1, 1, 1], [0, 0], [5], [2, 3]])
+@pytest.mark.parametrize("N,K,pad", [(8, 8, 0), (136, 264, 1), (512, 2048, 0), (1000, 7176, 0)])
+def test_few_rows_exact(sizes, N, K, pad):
+    """The counts around the kernel for at most four rows, padding rows among them."""
+    g = _gen(N + K)
+    R, E = sum(sizes) + pad, len(sizes)
+    for dt in (BF, HF):
+        x, w = _ints((R, K), g, dt, 1), _ints((E, N, K), g, dt, 1)
+        off = ref.offsets_of(sizes).cuda()
+        want = ref.mm(x, w, sizes)[0]
+        for out in (dt, F32):
+            y = torch.full((R, N), float("nan"), dtype=out, device="cuda")
+            st = torch.zeros(2, dtype=torch.int32, device="cuda")
+            _same(moe.moe_grouped_mm(x.cuda(), w.cuda(), off, y=y, dev_status=st), want, "y")
+            assert st.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("bad", [[0, 3, 1, 4], [-2, 1, 2, 4], [0, 1, 9, 4]])
+def test_few_rows_offsets_out_of_contract(bad):
+    x, w = torch.ones((4, 64), dtype=BF, device="cuda"), torch.ones((3, 32, 64), dtype=BF, device="cuda")
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_mm(x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), dev_status=st)
+    assert st.tolist() == [0, 7]
+
+
 @pytest.mark.parametrize("dt", [BF, HF])
 @pytest.mark.parametrize("out", [None, F32])
 @pytest.mark.parametrize("sizes,N,K", [([40, 0, 3, 300], 256, 1024), ([1, 1, 0, 1], 768, 2048), ([513], 136, 264)])

@@ -33,6 +33,7 @@
 #include "fp4.cuh"
 #include "gmm_common.cuh"
 #include "gmm_internal.h"
+#include "gmm_small.h"
 #include "ragged.cuh"
 #include "tc_pair.cuh"
 
@@ -525,6 +526,8 @@ MOE_API moe_status_t moe_grouped_mm(const void *x, const void *w, int32_t dt, co
     if (R == 0 && E >= 1 && N >= 1 && K >= 1)
         return type16(dt) && out_type(ydt, dt) ? MOE_OK : MOE_ERR_UNSUPPORTED;
     const moe_status_t st = check(x, w, y, dt, ydt, R, E, N, K, offsets);
+    if (st == MOE_OK && R <= kSmallRows)
+        return grouped_mm_small(x, w, dt, offsets, R, E, N, K, y, ydt, dev_status, as_stream(stream));
     return st != MOE_OK ? st : rows<kFwd>(x, w, dt, R, E, N, K, offsets, y, ydt, dev_status, as_stream(stream));
 }
 
