@@ -484,9 +484,14 @@ moe_status_t moe_ffn_decode_noalloc(const void *x, int32_t xdt, int32_t M, int32
  *   moe_grouped_mm_wgrad: dw[e][n][k] = sum_r dy[r][n] x[r][k]  (+ dw with
  *                         accumulate = 1; an expert without rows adds zero)
  *   for the rows r of expert e.  y [R][N], dx [R][K] and dw [E][N][K] are of dt
- *   or MOE_FP32; sums are FP32, rounded once; padding rows of y and dx are
- *   set to zero.  A row's result does not depend on the other rows, and the
- *   same call gives the same bits.  No workspace.
+ *   or MOE_FP32; sums are FP32, rounded once (for FP32 results, and for
+ *   16-bit ones past 16384 contracted elements, in parts of 768 elements added
+ *   to nearest, so that long sums do not drift); padding rows of y and dx are
+ *   set to zero.  The same call gives the same bits, and among calls
+ *   of more than four rows (and among those of at most four, which have their
+ *   own kernel) a row's result does not depend on the other rows.  No
+ *   workspace.  (accumulate to MOE_FP32 adds in the L2, where a subnormal sum
+ *   may be flushed to zero.)
  * R = 0 is a no-op for y and dx, and writes (or keeps) dw.
  * Limits: N % 8 == 0, K % 8 == 0, E <= 1024 (MOE_ERR_UNSUPPORTED); tensors
  * 16-byte aligned (MOE_ERR_INVALID_ARG). */

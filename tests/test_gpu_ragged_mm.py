@@ -133,8 +133,45 @@ def test_nan_and_infinity_stay_with_their_rows_and_experts():
     _same(y[clean][:, [1, 2, 3]], ref.mm(x, w, sizes)[0][clean][:, [1, 2, 3]], "y, clean rows and columns")
 
 
+def test_long_sums_do_not_drift():
+    """Sums of many terms of one sign.  A part of at most 768 terms is 48 accumulator updates, each off by at most 2^-23 of
+    the part; the parts are added in FP32 rounded to nearest, each addition off by at most 2^-24 of the sum so far."""
+    g = _gen(17)
+    R, N, K = 40_000, 32, 24
+    x, dy = torch.rand((R, K), generator=g).to(BF), torch.rand((R, N), generator=g).to(BF)
+    off = ref.offsets_of([R]).cuda()
+    got = moe.moe_grouped_mm_wgrad(dy.cuda(), x.cuda(), off).cpu().double()
+    want = ref.wgrad(dy, x, [R])[0]
+    parts = -(-R // 768)
+    assert ((got - want).abs() <= (48 * 2.0 ** -23 + parts * 2.0 ** -24) * want).all()
+    w, xs = torch.rand((1, N, 20_000), generator=g).to(BF), torch.rand((40, 20_000), generator=g).to(BF)
+    got = moe.moe_grouped_mm(xs.cuda(), w.cuda(), ref.offsets_of([40]).cuda(), out_dtype=F32).cpu().double()
+    want = ref.mm(xs, w, [40])[0]
+    assert ((got - want).abs() <= (48 * 2.0 ** -23 + 27 * 2.0 ** -24) * want).all()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_long_contractions_with_16_bit_results(dt):
+    """Past 16384 contracted elements the 16-bit results take the kernels that add parts in registers; exact sums."""
+    g = _gen(18)
+    sizes, N, K = [16_500, 0, 37, 900], 136, 72
+    R = sum(sizes)
+    x, dy = _ints((R, K), g, dt, 1), _ints((R, N), g, dt, 1)
+    off = ref.offsets_of(sizes).cuda()
+    want = ref.wgrad(dy, x, sizes)[0]
+    dw = torch.full((4, N, K), float("nan"), dtype=dt, device="cuda")
+    _same(moe.moe_grouped_mm_wgrad(dy.cuda(), x.cuda(), off, dw=dw), want, "dw")
+    old = _ints((4, N, K), g, dt, 50)
+    _same(moe.moe_grouped_mm_wgrad(dy.cuda(), x.cuda(), off, dw=old.cuda(), accumulate=True), want + old, "dw +=")
+    w, xs = _ints((2, 40, 16_400), g, dt, 1), _ints((75, 16_400), g, dt, 1)
+    o2 = ref.offsets_of([33, 42]).cuda()
+    _same(moe.moe_grouped_mm(xs.cuda(), w.cuda(), o2), ref.mm(xs, w, [33, 42])[0], "y")
+    wt = _ints((2, 16_400, 40), g, dt, 1)
+    _same(moe.moe_grouped_mm_dgrad(xs.cuda(), wt.cuda(), o2), ref.dgrad(xs, wt, [33, 42])[0], "dx")
+
+
 def test_same_bits_again_and_alone():
-    """The same call gives the same bits, and a row's bits do not depend on the rows it is with."""
+    """The same call gives the same bits, and past four rows a row's bits do not depend on the rows it is with."""
     g = _gen(11)
     sizes, N, K = [300, 20, 0, 77], 384, 640
     x, w = torch.randn((397, K), generator=g).to(BF).cuda(), torch.randn((4, N, K), generator=g).to(BF).cuda()
@@ -157,8 +194,10 @@ def test_other_stream_and_graph_capture():
     y, dx = torch.empty((105, N), dtype=BF, device="cuda"), torch.empty((105, K), dtype=BF, device="cuda")
     dw = torch.empty((4, N, K), device="cuda")
     moe.moe_grouped_mm(x, w, off, y=y, stream=s)
+    own = moe.moe_grouped_mm(x, w, off, stream=s)              # its result is allocated for that stream
     torch.cuda.current_stream().wait_stream(s)
     _same(y, ref.mm(x.cpu(), w.cpu(), sizes)[0], "y on another stream")
+    _same(own, ref.mm(x.cpu(), w.cpu(), sizes)[0], "a new y on another stream")
     gr = torch.cuda.CUDAGraph()
     with torch.cuda.graph(gr):
         moe.moe_grouped_mm(x, w, off, y=y)

@@ -677,13 +677,20 @@ def _groups(offsets, dev) -> int:
     return n - 1
 
 
-def _result(t, name: str, shape, dtype, dtypes, dev):
-    """The output: a new one of `dtype`, or the caller's after its check."""
+def _result(t, name: str, shape, dtype, dtypes, dev, stream):
+    """The output: a new one of `dtype`, or the caller's after its check.  One
+    that is first written on a given stream comes from that stream's memory,
+    and is not reused before the current stream, which gets it, is past it."""
     if t is not None:
         return _need(t, name, dtypes, shape, device=dev)
     if dtype not in dtypes:
         raise ValueError(f"{name} cannot be {dtype}; expected {' or '.join(str(d) for d in dtypes)}")
-    return torch.empty(shape, dtype=dtype, device=dev)
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_dtype=None, y=None, dev_status=None,
@@ -697,7 +704,7 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_
     e, N, k = _arg(w, "w", (dt,), 3, dev)
     if e != E or k != K:
         raise ValueError(f"w must be [E={E}, N, K={K}], not {tuple(w.shape)}")
-    y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev)
+    y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev, stream)
     _launch(dev, "moe_grouped_mm", x.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K, y.data_ptr(),
             _DT[y.dtype], _status(dev_status, dev), _stream(stream, dev))
     return y
@@ -713,7 +720,7 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     e, n, K = _arg(w, "w", (dt,), 3, dev)
     if e != E or n != N:
         raise ValueError(f"w must be [E={E}, N={N}, K], not {tuple(w.shape)}")
-    dx = _result(dx, "dx", (R, K), out_dtype or dt, (dt, torch.float32), dev)
+    dx = _result(dx, "dx", (R, K), out_dtype or dt, (dt, torch.float32), dev, stream)
     _launch(dev, "moe_grouped_mm_dgrad", dy.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
             dx.data_ptr(), _DT[dx.dtype], _status(dev_status, dev), _stream(stream, dev))
     return dx
@@ -732,7 +739,7 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     E = _groups(offsets, dev)
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
-    dw = _result(dw, "dw", (E, N, K), out_dtype, (dt, torch.float32), dev)
+    dw = _result(dw, "dw", (E, N, K), out_dtype, (dt, torch.float32), dev, stream)
     _launch(dev, "moe_grouped_mm_wgrad", dy.data_ptr(), x.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
             dw.data_ptr(), _DT[dw.dtype], 1 if accumulate else 0, _status(dev_status, dev), _stream(stream, dev))
     return dw
@@ -807,8 +814,8 @@ def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stre
     Ks = _fp4_shape(K, fmt, "v")
     rows = v.numel() // K
     groups = _fp4_alpha(alpha, fmt, rows, dev)
-    q = _result(q, "q", (*lead, K // 2), torch.uint8, _U8, dev)
-    s = _result(s, "s", (*lead, Ks), torch.uint8, _U8, dev)
+    q = _result(q, "q", (*lead, K // 2), torch.uint8, _U8, dev, stream)
+    s = _result(s, "s", (*lead, Ks), torch.uint8, _U8, dev, stream)
     _launch(dev, "moe_fp4_quantize", v.data_ptr(), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, q.data_ptr(),
             s.data_ptr(), _stream(stream, dev))
     return q, s
@@ -823,7 +830,7 @@ def moe_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, fmt: int, alpha=None, o
     _need(s, "s", _U8, (*lead, Ks), device=dev)
     rows = q.numel() // half
     groups = _fp4_alpha(alpha, fmt, rows, dev)
-    v = _result(v, "v", (*lead, K), out_dtype, _DT, dev)
+    v = _result(v, "v", (*lead, K), out_dtype, _DT, dev, stream)
     _launch(dev, "moe_fp4_dequantize", q.data_ptr(), s.data_ptr(), rows, K, fmt, _ptr(alpha), groups, v.data_ptr(),
             _DT[v.dtype], _stream(stream, dev))
     return v
@@ -843,7 +850,7 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
     K = half * 2
     if e != E or xh != half:
         raise ValueError(f"w is [{e}, {N}, {K}]; offsets are for {E} experts and x has K = {xh * 2}")
-    y = _result(y, "y", (R, N), out_dtype, _DT, dev)
+    y = _result(y, "y", (R, N), out_dtype, _DT, dev, stream)
     _launch(dev, "moe_grouped_mm_fp4", x.q.data_ptr(), x.s.data_ptr(), _ptr(x.alpha), w.q.data_ptr(), w.s.data_ptr(),
             _ptr(w.alpha), x.fmt, offsets.data_ptr(), R, E, N, K, y.data_ptr(), _DT[y.dtype], _status(dev_status,
             dev), _stream(stream, dev))

@@ -45,14 +45,25 @@ enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kStageBytes = 32768;             // 128 x 64 of each operand, 16 bits
 constexpr int kMaxStages = 6;
 
-// Ring stages, and bytes of each draining warp's staging tiles: wgrad writes far
-// more per tile of MMA work and has two tiles of 128-byte rows in place of a
-// stage (4 stages: 8 to 12 % slower where the MMAs bound it; 64-byte rows or
-// one tile: 10 to 25 % slower where dw does).
-constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
-constexpr int staging_of(int op) { return op == kWgrad ? 8192 : 4096; }
-constexpr int kDrain = 4;                      // draining warps, one to a quadrant of tensor memory
-constexpr int kThreads = 32 * (4 + kDrain);
+// The tensor cores add to an FP32 accumulator without rounding to nearest, so a
+// long sum drifts (measured: 1.1e-9 of the result per contracted element, 4.4e-6
+// at 4096).  SUM kernels end the accumulation every kSpan steps (768 elements)
+// and add the parts in registers, rounded to nearest: 7e-7 at any length.  FP32
+// results take them always, 16-bit ones -- whose own rounding is 2^-9 or 2^-12 --
+// where the contraction can be longer than kLong.
+constexpr int kSpan = 12;
+constexpr int kLong = 16384;
+
+// Draining warps, one to a quadrant of tensor memory, or two with half of the
+// columns each where they hold the sums; ring stages; bytes of a draining
+// warp's staging tiles.  wgrad writes far more per tile of MMA work and has
+// two tiles of 128-byte rows in place of a stage (4 stages: 8 to 12 % slower
+// where the MMAs bound it; 64-byte rows or one tile: 10 to 25 % slower where
+// dw does).
+constexpr int drain_of(bool sum) { return sum ? 8 : 4; }
+constexpr int stages_of(int op, bool sum) { return op == kWgrad || sum ? 5 : 6; }
+constexpr int staging_of(int op, bool sum) { return op == kWgrad && !sum ? 8192 : 4096; }
+constexpr int threads_of(bool sum) { return 32 * (4 + drain_of(sum)); }
 
 constexpr int kTileM = 256, kTileN = 256, kStep = 64;
 constexpr uint32_t kTmemCols = 512;
@@ -77,11 +88,12 @@ struct Shared {
     ragged::List list;
 };
 
-constexpr int smem_of(int op)
+constexpr int smem_of(int op, bool sum)
 {
-    return 1024 + stages_of(op) * kStageBytes + kDrain * staging_of(op) + static_cast<int>(sizeof(Shared));
+    return 1024 + stages_of(op, sum) * kStageBytes + drain_of(sum) * staging_of(op, sum) + static_cast<int>(sizeof(Shared));
 }
-static_assert(smem_of(kFwd) <= 232448 && smem_of(kWgrad) <= 232448, "shared memory of one CTA");
+static_assert(smem_of(kFwd, false) <= 232448 && smem_of(kWgrad, false) <= 232448 && smem_of(kFwd, true) <= 232448,
+              "shared memory of one CTA");
 
 struct Tile {
     int e, m0, lo, rows;       // expert, first left row, the expert's rows
@@ -113,48 +125,87 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, i
 
 __device__ __forceinline__ int n_mma(int n) { return (n + 31) & ~31; }
 
-// This lane's row of a 32 x 128-byte staging tile (128-byte swizzle): eight
-// 16-byte words, word u at u ^ (row % 8).
-__device__ __forceinline__ void stage_row(uint8_t *tile, int lane, const uint32_t (&w)[32])
+// Up to 32 rows of y or dx from row r0 on (n of them are the group's): through
+// TMA where all 32 are, which would reach into the next group's rows otherwise.
+template <typename OT>
+__device__ __forceinline__ void store_y(const uint32_t (&v)[32], uint8_t *tiles, int &flip, const CUtensorMap *map, OT *out,
+                                        int r0, int n, int m, int M, int lane)
 {
+    if (n < 32)
+        store_rows<OT>(v, out + static_cast<int64_t>(r0) * M, M, m, M, n, lane);
+    else
+        drain_rows<OT>(v, tiles, flip, map, m - lane, r0, M, lane);
+}
+
+// 128 bytes of this lane's row of dw (row m of expert e, columns from c on) in
+// w: through a staging tile (32 rows, 128-byte swizzle) and out, or added, by
+// TMA, which cuts them at the expert's last row and column.  two: the warp has
+// two tiles and alternates.
+template <typename OT>
+__device__ __forceinline__ void store_tile(const uint32_t (&w)[32], uint8_t *tile, bool two, const CUtensorMap *map, int c, int m,
+                                           int e, int M, int lane, bool add)
+{
+    if (two)
+        tc::bulk_wait_read<1>();
+    else
+        tc::bulk_wait_read<0>();
+    __syncwarp();
 #pragma unroll
     for (int u = 0; u < 8; ++u)
         *reinterpret_cast<uint4 *>(tile + lane * 128 + ((u ^ (lane & 7)) << 4)) =
             make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (m < M) {
+            if (add)
+                tc::tma_add_3d(map, tc::smem_u32(tile), c, m, e);
+            else
+                tc::tma_store_3d(map, tc::smem_u32(tile), c, m, e);
+        }
+        tc::bulk_commit();
+    }
 }
 
-// 32 FP32 sums v of this lane's row of dw plus the old elements, rounded once,
-// into w (n of them exist, n % 8 == 0).
+// 32 FP32 sums of this lane's row of dw as 16-bit values in w; accumulate: plus
+// the old elements, rounded once (C % 8 == 0).
 template <typename OT>
-__device__ __forceinline__ void add_row(const uint32_t (&v)[32], const OT *old, int n, uint32_t *w)
+__device__ __forceinline__ void round_dw(const uint32_t (&v)[32], uint32_t *w, const OT *out, int c, int m, int e, int M, int C,
+                                         bool accumulate)
 {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-        if (i < n) {
-            const uint4 o = *reinterpret_cast<const uint4 *>(old + i);
-            const OT *p = reinterpret_cast<const OT *>(&o);
+    for (int i = 0; i < 16; ++i)
+        w[i] = pack2<OT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+    if (accumulate && m < M) {
+        const OT *old = out + (static_cast<int64_t>(e) * M + m) * C + c;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2)
-                w[(i + j) / 2] = pack2<OT>(__uint_as_float(v[i + j]) + fp4::to_float(p[j]),
-                                           __uint_as_float(v[i + j + 1]) + fp4::to_float(p[j + 1]));
+        for (int i = 0; i < 32; i += 8) {
+            if (c + i < C) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(old + i);
+                const OT *p = reinterpret_cast<const OT *>(&o);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2)
+                    w[(i + j) / 2] = pack2<OT>(__uint_as_float(v[i + j]) + fp4::to_float(p[j]),
+                                               __uint_as_float(v[i + j + 1]) + fp4::to_float(p[j + 1]));
+            }
         }
     }
 }
 
-template <int OP, typename OT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int OP, typename OT, bool SUM>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(SUM), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
     // tmB16: B in boxes of 16 rows (fwd, dgrad); tmY: the result
-    constexpr int kStages = stages_of(OP);
+    constexpr int kStages = stages_of(OP, SUM), kDrain = drain_of(SUM), kStaging = staging_of(OP, SUM);
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const uint32_t raw = tc::smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);      // the same offset in both CTAs
     const uint32_t ring = tc::smem_u32(smem);
-    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes + kDrain * staging_of(OP));
+    Shared &s = *reinterpret_cast<Shared *>(smem + kStages * kStageBytes + kDrain * kStaging);
     volatile int *abort = &s.abort;
     auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
 
@@ -277,30 +328,32 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
                 if (T.steps == 0)
                     continue;
-                const int buf = tix & 1;
-                if (!tc::mbar_wait_cluster(bar(s.acce[buf]), ((tix >> 1) & 1) ^ 1u, abort, kWaitNs))
-                    break;
-                tc::tc_fence_after();
-                ++tix;
-                const uint32_t acc = tmem + 256 * buf;
                 const uint32_t id = tc::idesc_f16_major(256, n_mma(T.n), a.bf16, OP != kFwd, OP == kWgrad);
-                for (int j = 0; j < T.steps; ++j) {
-                    if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
+                for (int j0 = 0; j0 < T.steps; j0 += SUM ? kSpan : T.steps) {
+                    const int buf = tix & 1, j1 = SUM ? min(j0 + kSpan, T.steps) : T.steps;
+                    if (!tc::mbar_wait_cluster(bar(s.acce[buf]), ((tix >> 1) & 1) ^ 1u, abort, kWaitNs))
                         break;
                     tc::tc_fence_after();
-                    const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
-                    const int nk = OP == kWgrad ? min(4, (T.rows - j * kStep + 15) >> 4) : 4;
+                    ++tix;
+                    const uint32_t acc = tmem + 256 * buf;
+                    for (int j = j0; j < j1; ++j) {
+                        if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
+                            break;
+                        tc::tc_fence_after();
+                        const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
+                        const int nk = OP == kWgrad ? min(4, (T.rows - j * kStep + 15) >> 4) : 4;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (OP != kWgrad || kk < nk)
-                            tc::mma_f16_pair(acc, ad + kk * kAStep, bd + kk * kBStep, id, (j | kk) != 0 ? 1u : 0u);
-                    tc::tc_commit_pair(bar(s.empty[st]));
-                    if (++st == kStages) {
-                        st = 0;
-                        ph ^= 1u;
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (OP != kWgrad || kk < nk)
+                                tc::mma_f16_pair(acc, ad + kk * kAStep, bd + kk * kBStep, id, (j - j0) | kk ? 1u : 0u);
+                        tc::tc_commit_pair(bar(s.empty[st]));
+                        if (++st == kStages) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
                     }
+                    tc::tc_commit_pair(bar(s.accf[buf]));
                 }
-                tc::tc_commit_pair(bar(s.accf[buf]));
             }
         }
     } else if (warp == 2) {
@@ -342,85 +395,122 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         const int q = warp & 3;                         // TMEM lane quadrant
         int tix = 0, flip = 0;
         OT *out = static_cast<OT *>(a.out);
-        uint8_t *tiles = smem + kStages * kStageBytes + (warp - 4) * staging_of(OP);
+        uint8_t *tiles = smem + kStages * kStageBytes + (warp - 4) * kStaging;
         for (int t = cid; t < total; t += n_cl) {
             const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
             const int m = T.m0 + 128 * rank + 32 * q + lane;
-            const int buf = tix & 1;
-            if (T.steps) {
-                if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
+            if constexpr (SUM) {
+                // this warp's 128 columns: the spans' parts added in registers
+                const int h0 = 128 * ((warp - 4) >> 2);
+                float sum[4][32];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        sum[g][i] = 0.f;
+                bool ok = true;
+                for (int j0 = 0; j0 < T.steps; j0 += kSpan, ++tix) {
+                    const int buf = tix & 1;
+                    ok = tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs);
+                    if (!ok)
+                        break;
+                    tc::tc_fence_after();
+                    const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16) + h0;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        if (h0 + 32 * g < T.n) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16];
+                                tc::tmem_ld_32x32b_x16(acc + 32 * g + h, v);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    sum[g][h + i] += __uint_as_float(v[i]);
+                            }
+                        }
+                    }
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
+                }
+                if (!ok) {
                     if (a.dev_status)
                         atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
                     break;
                 }
-                tc::tc_fence_after();
-                ++tix;
-            }
-            const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16);
-            if (OP == kWgrad) {
-                // 128 bytes of 32 rows of dw at a time go through a staging
-                // tile of this warp's and out by TMA, which cuts them at the
-                // expert's last row and column
-                constexpr int kCols = 128 / sizeof(OT);
-                if (T.steps || !a.accumulate) {
-                    for (int c0 = 0; c0 < T.n; c0 += kCols) {
+                auto bits = [&](int g, uint32_t (&v)[32]) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __float_as_uint(sum[g][i]);
+                };
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int c0 = h0 + 32 * g;
+                    if (c0 >= T.n || (OP == kWgrad && T.steps == 0 && a.accumulate))
+                        continue;
+                    uint32_t v[32];
+                    bits(g, v);
+                    if constexpr (OP != kWgrad) {
+                        store_y<OT>(v, tiles, flip, &tmY, out, T.lo + T.n0 + c0, T.n - c0, m, a.M, lane);
+                    } else if constexpr (sizeof(OT) == 4) {
+                        store_tile<OT>(v, tiles, false, &tmY, T.n0 + c0, m, T.e, a.M, lane, a.accumulate);
+                    } else if (g % 2 == 0) {
                         uint32_t w[32];
-                        if (T.steps == 0) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                w[i] = 0;
-                        } else if constexpr (sizeof(OT) == 4) {
-                            tc::tmem_ld_32x32b_x32(acc + c0, w);
-                            tc::tmem_ld_wait();
-                        } else {
-                            uint32_t v[32];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                tc::tmem_ld_32x32b_x32(acc + c0 + 32 * h, v);
-                                tc::tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    w[16 * h + i] = pack2<OT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                                if (a.accumulate && m < a.M)
-                                    add_row<OT>(v, out + (static_cast<int64_t>(T.e) * a.M + m) * a.C + T.n0 + c0 + 32 * h,
-                                                T.n - c0 - 32 * h, w + 16 * h);
-                            }
-                        }
-                        uint8_t *tile = tiles + flip * 4096;
-                        flip ^= 1;
-                        tc::bulk_wait_read<1>();            // the store of two chunks ago has read this tile
-                        __syncwarp();
-                        stage_row(tile, lane, w);
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && m < a.M) {
-                            if (sizeof(OT) == 4 && a.accumulate)
-                                tc::tma_add_3d(&tmY, tc::smem_u32(tile), T.n0 + c0, m, T.e);
-                            else
-                                tc::tma_store_3d(&tmY, tc::smem_u32(tile), T.n0 + c0, m, T.e);
-                        }
-                        if (lane == 0)
-                            tc::bulk_commit();
+                        round_dw<OT>(v, w, out, T.n0 + c0, m, T.e, a.M, a.C, a.accumulate);
+                        bits(g + 1 < 4 ? g + 1 : g, v);
+                        round_dw<OT>(v, w + 16, out, T.n0 + c0 + 32, m, T.e, a.M, a.C, a.accumulate);
+                        store_tile<OT>(w, tiles, false, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
                     }
                 }
             } else {
-                for (int c0 = 0; c0 < T.n; c0 += 32) {
-                    uint32_t v[32];
-                    tc::tmem_ld_32x32b_x32(acc + c0, v);
-                    tc::tmem_ld_wait();
-                    const int64_t r0 = T.lo + T.n0 + c0;
-                    if (T.n - c0 < 32) {                  // a TMA store would reach into the next group's rows
-                        store_rows<OT>(v, out + r0 * a.M, a.M, m, a.M, T.n - c0, lane);
+                const int buf = tix & 1;
+                if (T.steps) {
+                    if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
+                        if (a.dev_status)
+                            atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
                         break;
                     }
-                    drain_rows<OT>(v, tiles, flip, &tmY, m - lane, static_cast<int>(r0), a.M, lane);
+                    tc::tc_fence_after();
+                    ++tix;
                 }
-            }
-            if (T.steps) {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
+                const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16);
+                if (OP == kWgrad) {
+                    if (T.steps || !a.accumulate) {
+                        for (int c0 = 0; c0 < T.n; c0 += 64) {
+                            uint32_t w[32];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t v[32];
+                                if (T.steps) {
+                                    tc::tmem_ld_32x32b_x32(acc + c0 + 32 * h, v);
+                                    tc::tmem_ld_wait();
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        v[i] = 0;
+                                }
+                                round_dw<OT>(v, w + 16 * h, out, T.n0 + c0 + 32 * h, m, T.e, a.M, a.C, a.accumulate);
+                            }
+                            store_tile<OT>(w, tiles + 4096 * flip, true, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
+                            flip ^= 1;
+                        }
+                    }
+                } else {
+                    for (int c0 = 0; c0 < T.n; c0 += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld_32x32b_x32(acc + c0, v);
+                        tc::tmem_ld_wait();
+                        store_y<OT>(v, tiles, flip, &tmY, out, T.lo + T.n0 + c0, T.n - c0, m, a.M, lane);
+                    }
+                }
+                if (T.steps) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
+                }
             }
         }
         tc::bulk_wait<0>();
@@ -470,25 +560,32 @@ static moe_status_t check(const void *a, const void *b, const void *out, int32_t
     return MOE_OK;
 }
 
-template <int OP, typename OT>
+template <int OP, typename OT, bool SUM>
 static moe_status_t launch(const CUtensorMap (&tm)[4], const Args &a, int64_t most_tiles, cudaStream_t s)
 {
-    auto k = gemm_kernel<OP, OT>;
+    auto k = gemm_kernel<OP, OT, SUM>;
+    constexpr int kSmem = smem_of(OP, SUM);
     static std::atomic<uint64_t> done{0};
-    if (!smem_attr_once(done, reinterpret_cast<const void *>(k), smem_of(OP)))
+    if (!smem_attr_once(done, reinterpret_cast<const void *>(k), kSmem))
         return MOE_ERR_CUDA;
     const int pairs = device_sm_count() / 2;
     const int grid = 2 * static_cast<int>(most_tiles < pairs ? most_tiles : pairs);
-    return launch_pdl(k, dim3(grid), dim3(kThreads), smem_of(OP), s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
-                                                                                                            : MOE_ERR_CUDA;
+    return launch_pdl(k, dim3(grid), dim3(threads_of(SUM)), kSmem, s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
+                                                                                                              : MOE_ERR_CUDA;
 }
 
+// longest: an upper bound of the contraction
 template <int OP>
-static moe_status_t launch_as(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int64_t most_tiles, cudaStream_t s)
+static moe_status_t launch_as(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int longest, int64_t most_tiles,
+                              cudaStream_t s)
 {
     if (odt == MOE_FP32)
-        return launch<OP, float>(tm, a, most_tiles, s);
-    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16>(tm, a, most_tiles, s) : launch<OP, __half>(tm, a, most_tiles, s);
+        return launch<OP, float, true>(tm, a, most_tiles, s);
+    if (longest > kLong)
+        return odt == MOE_BF16 ? launch<OP, __nv_bfloat16, true>(tm, a, most_tiles, s)
+                               : launch<OP, __half, true>(tm, a, most_tiles, s);
+    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16, false>(tm, a, most_tiles, s)
+                           : launch<OP, __half, false>(tm, a, most_tiles, s);
 }
 
 static CUtensorMapDataType map_type(int32_t dt)
@@ -511,7 +608,7 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
         return MOE_ERR_CUDA;
     const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
     const int64_t n_mt = (C + kTileM - 1) / kTileM;
-    return launch_as<OP>(tm, a, ydt, n_mt * (static_cast<int64_t>(R) / kTileN + (E < R ? E : R)), s);
+    return launch_as<OP>(tm, a, ydt, J, n_mt * (static_cast<int64_t>(R) / kTileN + (E < R ? E : R)), s);
 }
 
 }  // namespace gmm
@@ -563,5 +660,5 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
     const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + kTileN - 1) / kTileN);
     if (tiles > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    return launch_as<kWgrad>(tm, a, wdt, tiles, as_stream(stream));
+    return launch_as<kWgrad>(tm, a, wdt, R, tiles, as_stream(stream));
 }
