@@ -6,7 +6,7 @@
 // for the rows r of expert e.  Sums are FP32, rounded once.
 //
 // One persistent kernel on the tensor cores (tcgen05 kind::f16), one CTA per
-// SM, two CTAs (a cluster) per 256 x 256 tile.  The left operand is the
+// SM, two CTAs (a cluster) per tile of 256 x 256 (256 x 128).  The left operand is the
 // expert's matrix (w, w^T, or dy^T), 128 of its rows per CTA; the rows of x or
 // dy -- or, for wgrad, the columns of x -- are the right operand's N, half of
 // them held by each CTA.  A group's last tile takes N down to the next 32, so
@@ -21,8 +21,8 @@
 // to the next 16 (both operands, so that a NaN there stays out) and the 16-row
 // MMA steps past them are left out.
 //
-// Roles: warp 0 loads (TMA, 128-byte swizzle, a ring of 6 stages of 64 along
-// the contraction, 5 for wgrad), warp 1 of the pair's leader issues the MMAs into two
+// Roles: warp 0 loads (TMA, 128-byte swizzle, a ring of 5 to 8 stages of 64 along
+// the contraction), warp 1 of the pair's leader issues the MMAs into two
 // accumulators of 256 TMEM columns, warps 4..7 drain one while the next tile
 // fills the other, warp 2 zeroes wgrad's row tails.  Every wait is bounded; an
 // expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
@@ -42,12 +42,11 @@ namespace gmm {
 
 enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kStageBytes = 32768;             // 128 x 64 of each operand, 16 bits
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 8;
 
 // The tensor cores add to an FP32 accumulator without rounding to nearest, so a
 // long sum drifts (measured: 1.1e-9 of the result per contracted element, 4.4e-6
-// at 4096).  SUM kernels end the accumulation every kSpan steps (768 elements)
+// at 4096).  Sum kernels end the accumulation every kSpan steps (768 elements)
 // and add the parts in registers, rounded to nearest: 7e-7 at any length.  FP32
 // results take them always, 16-bit ones -- whose own rounding is 2^-9 or 2^-12 --
 // where the contraction can be longer than kLong.
@@ -60,12 +59,22 @@ constexpr int kLong = 16384;
 // two tiles of 128-byte rows in place of a stage (4 stages: 8 to 12 % slower
 // where the MMAs bound it; 64-byte rows or one tile: 10 to 25 % slower where
 // dw does).
-constexpr int drain_of(bool sum) { return sum ? 8 : 4; }
-constexpr int stages_of(int op, bool sum) { return op == kWgrad || sum ? 5 : 6; }
-constexpr int staging_of(int op, bool sum) { return op == kWgrad && !sum ? 8192 : 4096; }
-constexpr int threads_of(bool sum) { return 32 * (4 + drain_of(sum)); }
+//
+// Narrow kernels take tiles of 128 rows of x or dy and use the room for more
+// stages: with few rows per expert the time is that of streaming the weights,
+// and more of them are on the way (8 stages of 24 KB; 16 KB each are weights).
+// 127 us rather than 132 for 4096 rows over 128 experts of 1536 x 2048, 13.6
+// rather than 16.1 (dgrad) for 800 rows over 40 of 1000 x 520; at more than 64
+// rows per expert they read the weights' tiles twice.
+enum Kind { kPlain = 0, kNarrow = 1, kSum = 2 };
+constexpr int drain_of(int kind) { return kind == kSum ? 8 : 4; }
+constexpr int tile_n(int kind) { return kind == kNarrow ? 128 : 256; }
+constexpr int stages_of(int op, int kind) { return kind == kNarrow ? 8 : op == kWgrad || kind == kSum ? 5 : 6; }
+constexpr int stage_bytes(int kind) { return 16384 + 64 * tile_n(kind); }   // 128 rows and half a tile's, 128 bytes each
+constexpr int staging_of(int op, int kind) { return op == kWgrad && kind != kSum ? 8192 : 4096; }
+constexpr int threads_of(int kind) { return 32 * (4 + drain_of(kind)); }
 
-constexpr int kTileM = 256, kTileN = 256, kStep = 64;
+constexpr int kTileM = 256, kStep = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -88,12 +97,12 @@ struct Shared {
     ragged::List list;
 };
 
-constexpr int smem_of(int op, bool sum)
+constexpr int smem_of(int op, int kind)
 {
-    return 1024 + stages_of(op, sum) * kStageBytes + drain_of(sum) * staging_of(op, sum) + static_cast<int>(sizeof(Shared));
+    return 1024 + stages_of(op, kind) * stage_bytes(kind) + drain_of(kind) * staging_of(op, kind) + static_cast<int>(sizeof(Shared));
 }
-static_assert(smem_of(kFwd, false) <= 232448 && smem_of(kWgrad, false) <= 232448 && smem_of(kFwd, true) <= 232448,
-              "shared memory of one CTA");
+static_assert(smem_of(kFwd, kPlain) <= 232448 && smem_of(kFwd, kNarrow) <= 232448 && smem_of(kWgrad, kPlain) <= 232448 &&
+              smem_of(kFwd, kSum) <= 232448, "shared memory of one CTA");
 
 struct Tile {
     int e, m0, lo, rows;       // expert, first left row, the expert's rows
@@ -101,7 +110,7 @@ struct Tile {
     int steps;
 };
 
-template <int OP>
+template <int OP, int kTileN>
 __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, int n_mt, int n_nt)
 {
     Tile T;
@@ -192,13 +201,15 @@ __device__ __forceinline__ void round_dw(const uint32_t (&v)[32], uint32_t *w, c
     }
 }
 
-template <int OP, typename OT, bool SUM>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(SUM), 1)
+template <int OP, typename OT, int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(KIND), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
     // tmB16: B in boxes of 16 rows (fwd, dgrad); tmY: the result
-    constexpr int kStages = stages_of(OP, SUM), kDrain = drain_of(SUM), kStaging = staging_of(OP, SUM);
+    constexpr bool SUM = KIND == kSum;
+    constexpr int kStages = stages_of(OP, KIND), kDrain = drain_of(KIND), kStaging = staging_of(OP, KIND);
+    constexpr int kTileN = tile_n(KIND), kStageBytes = stage_bytes(KIND);
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -250,14 +261,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t ph = 0;
             const uint32_t full_lead = tc::mapa(bar(s.full[0]), 0);
             for (int t = cid; t < total && !*abort; t += n_cl) {
-                const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+                const Tile T = tile_of<OP, kTileN>(a, s, t, n_mt, n_nt);
                 const int m0 = T.m0 + 128 * rank, nh = n_mma(T.n) / 2;
                 const int tail = OP == kWgrad && (T.rows & 15) ? T.steps - 1 : -1;
                 uint32_t bytes = 16384;
                 if (OP == kWgrad)
                     bytes += nh > 64 ? 16384 : 8192;
                 else
-                    bytes += nh > 64 ? 16384 : nh * 128;
+                    bytes += (nh > kTileN / 4 ? kTileN / 2 : nh) * 128;
                 for (int j = 0; j < T.steps; ++j, ++issued) {
                     if (!tc::mbar_wait(bar(s.empty[st]), ph ^ 1u, abort, kWaitNs))
                         break;
@@ -291,7 +302,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             tc::tma_load_2d_pair(sb + 8192, &tmB, c0 + 64, T.lo + j * kStep, fb);
                     } else {
                         const int r0 = T.lo + T.n0 + rank * nh;
-                        if (nh > 64)
+                        if (nh > kTileN / 4)
                             tc::tma_load_2d_pair(sb, &tmB, j * kStep, r0, fb);
                         else
                             for (int i = 0; i < nh; i += 16)
@@ -325,7 +336,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             int st = 0, tix = 0;
             uint32_t ph = 0;
             for (int t = cid; t < total && !*abort; t += n_cl) {
-                const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+                const Tile T = tile_of<OP, kTileN>(a, s, t, n_mt, n_nt);
                 if (T.steps == 0)
                     continue;
                 const uint32_t id = tc::idesc_f16_major(256, n_mma(T.n), a.bf16, OP != kFwd, OP == kWgrad);
@@ -362,7 +373,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             int st = 0;
             uint32_t phases = 0;
             for (int t = cid; t < total; t += n_cl) {
-                const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+                const Tile T = tile_of<OP, kTileN>(a, s, t, n_mt, n_nt);
                 if (T.steps == 0)
                     continue;
                 const int q = (st + T.steps - 1) % kStages;
@@ -397,7 +408,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         OT *out = static_cast<OT *>(a.out);
         uint8_t *tiles = smem + kStages * kStageBytes + (warp - 4) * kStaging;
         for (int t = cid; t < total; t += n_cl) {
-            const Tile T = tile_of<OP>(a, s, t, n_mt, n_nt);
+            const Tile T = tile_of<OP, kTileN>(a, s, t, n_mt, n_nt);
             const int m = T.m0 + 128 * rank + 32 * q + lane;
             if constexpr (SUM) {
                 // this warp's 128 columns: the spans' parts added in registers
@@ -560,32 +571,24 @@ static moe_status_t check(const void *a, const void *b, const void *out, int32_t
     return MOE_OK;
 }
 
-template <int OP, typename OT, bool SUM>
+template <int OP, typename OT, int KIND>
 static moe_status_t launch(const CUtensorMap (&tm)[4], const Args &a, int64_t most_tiles, cudaStream_t s)
 {
-    auto k = gemm_kernel<OP, OT, SUM>;
-    constexpr int kSmem = smem_of(OP, SUM);
+    auto k = gemm_kernel<OP, OT, KIND>;
+    constexpr int kSmem = smem_of(OP, KIND);
     static std::atomic<uint64_t> done{0};
     if (!smem_attr_once(done, reinterpret_cast<const void *>(k), kSmem))
         return MOE_ERR_CUDA;
     const int pairs = device_sm_count() / 2;
     const int grid = 2 * static_cast<int>(most_tiles < pairs ? most_tiles : pairs);
-    return launch_pdl(k, dim3(grid), dim3(threads_of(SUM)), kSmem, s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
-                                                                                                              : MOE_ERR_CUDA;
+    return launch_pdl(k, dim3(grid), dim3(threads_of(KIND)), kSmem, s, tm[0], tm[1], tm[2], tm[3], a) == cudaSuccess ? MOE_OK
+                                                                                                               : MOE_ERR_CUDA;
 }
 
-// longest: an upper bound of the contraction
-template <int OP>
-static moe_status_t launch_as(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int longest, int64_t most_tiles,
-                              cudaStream_t s)
+template <int OP, int KIND>
+static moe_status_t launch_16(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int64_t most_tiles, cudaStream_t s)
 {
-    if (odt == MOE_FP32)
-        return launch<OP, float, true>(tm, a, most_tiles, s);
-    if (longest > kLong)
-        return odt == MOE_BF16 ? launch<OP, __nv_bfloat16, true>(tm, a, most_tiles, s)
-                               : launch<OP, __half, true>(tm, a, most_tiles, s);
-    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16, false>(tm, a, most_tiles, s)
-                           : launch<OP, __half, false>(tm, a, most_tiles, s);
+    return odt == MOE_BF16 ? launch<OP, __nv_bfloat16, KIND>(tm, a, most_tiles, s) : launch<OP, __half, KIND>(tm, a, most_tiles, s);
 }
 
 static CUtensorMapDataType map_type(int32_t dt)
@@ -601,14 +604,21 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
                          const int32_t *off, void *y, int32_t ydt, int32_t *dev_status, cudaStream_t s)
 {
     const CUtensorMapDataType t = map_type(dt);
+    const int kind = ydt == MOE_FP32 || J > kLong ? kSum : R <= 64 * static_cast<int64_t>(E) ? kNarrow : kPlain;
+    const int tn = tile_n(kind);
     CUtensorMap tm[4];
     const bool ok = OP == kFwd ? tmap_tile(&tm[0], 3, t, 2, w, J, C, E, 64, 128) : tmap_tile(&tm[0], 3, t, 2, w, C, J, E, 64, 64);
-    if (!ok || !tmap_tile(&tm[1], 2, t, 2, x, J, R, 1, 64, 128) || !tmap_tile(&tm[2], 2, t, 2, x, J, R, 1, 64, 16) ||
+    if (!ok || !tmap_tile(&tm[1], 2, t, 2, x, J, R, 1, 64, tn / 2) || !tmap_tile(&tm[2], 2, t, 2, x, J, R, 1, 64, 16) ||
         !tmap_rows_out(&tm[3], map_type(ydt), ydt == MOE_FP32 ? 4 : 2, y, C, R))
         return MOE_ERR_CUDA;
     const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
     const int64_t n_mt = (C + kTileM - 1) / kTileM;
-    return launch_as<OP>(tm, a, ydt, J, n_mt * (static_cast<int64_t>(R) / kTileN + (E < R ? E : R)), s);
+    const int64_t tiles = n_mt * (static_cast<int64_t>(R) / tn + (E < R ? E : R));
+    if (ydt == MOE_FP32)
+        return launch<OP, float, kSum>(tm, a, tiles, s);
+    return kind == kSum      ? launch_16<OP, kSum>(tm, a, ydt, tiles, s)
+           : kind == kNarrow ? launch_16<OP, kNarrow>(tm, a, ydt, tiles, s)
+                             : launch_16<OP, kPlain>(tm, a, ydt, tiles, s);
 }
 
 }  // namespace gmm
@@ -657,8 +667,11 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
         return MOE_ERR_CUDA;
     tm[2] = tm[1];
     const Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
-    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + kTileN - 1) / kTileN);
+    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + tile_n(kPlain) - 1) / tile_n(kPlain));
     if (tiles > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    return launch_as<kWgrad>(tm, a, wdt, R, tiles, as_stream(stream));
+    if (wdt == MOE_FP32)
+        return launch<kWgrad, float, kSum>(tm, a, tiles, as_stream(stream));
+    return R > kLong ? launch_16<kWgrad, kSum>(tm, a, wdt, tiles, as_stream(stream))
+                     : launch_16<kWgrad, kPlain>(tm, a, wdt, tiles, as_stream(stream));
 }
