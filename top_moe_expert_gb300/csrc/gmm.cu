@@ -398,7 +398,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (lane == 0)
                         tc::mbar_arrive(bar(s.full[q]));
                 } else if (lane == 0) {
-                    tc::mbar_arrive_cluster(tc::mapa(bar(s.peer[q]), 0));
+                    tc::mbar_arrive_cluster_smem(tc::mapa(bar(s.peer[q]), 0));
                 }
             }
         }
@@ -490,20 +490,18 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 if (OP == kWgrad) {
                     if (T.steps || !a.accumulate) {
                         for (int c0 = 0; c0 < T.n; c0 += 64) {
-                            uint32_t w[32];
+                            uint32_t v[2][32], w[32];
+                            if (T.steps) {
+                                tc::tmem_ld_32x32b_x32(acc + c0, v[0]);
+                                tc::tmem_ld_32x32b_x32(acc + c0 + 32, v[1]);
+                                tc::tmem_ld_wait();
+                            } else {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t v[32];
-                                if (T.steps) {
-                                    tc::tmem_ld_32x32b_x32(acc + c0 + 32 * h, v);
-                                    tc::tmem_ld_wait();
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i)
-                                        v[i] = 0;
-                                }
-                                round_dw<OT>(v, w + 16 * h, out, T.n0 + c0 + 32 * h, m, T.e, a.M, a.C, a.accumulate);
+                                for (int i = 0; i < 32; ++i)
+                                    v[0][i] = v[1][i] = 0;
                             }
+                            round_dw<OT>(v[0], w, out, T.n0 + c0, m, T.e, a.M, a.C, a.accumulate);
+                            round_dw<OT>(v[1], w + 16, out, T.n0 + c0 + 32, m, T.e, a.M, a.C, a.accumulate);
                             store_tile<OT>(w, tiles + 4096 * flip, true, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
                             flip ^= 1;
                         }

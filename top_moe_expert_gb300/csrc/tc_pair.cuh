@@ -31,23 +31,19 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Arrivals on a barrier of either CTA (cluster address).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// The same at CTA scope: for hand-overs of this CTA's shared memory to this SM's
-// own tensor core, when the other CTA's thread only issues the instruction.
-// The writes are complete in that memory once fence.proxy.async has returned,
-// and no cache lies between; a cluster-scope release makes the same promise for
-// all memory and takes about 1750 cycles.
+// Arrival on a barrier of either CTA (cluster address) after writes to this CTA's
+// shared memory that this SM's own tensor core will read, when the other CTA's
+// thread only issues the instruction.  The writers have executed
+// fence.proxy.async, upon which the writes are complete in that memory, and no
+// cache lies between; the arrival itself is ordered at CTA scope.  (A release at
+// cluster scope makes the same promise for all memory, global memory included,
+// and takes about 1750 cycles.)
 __device__ __forceinline__ void mbar_arrive_cluster_smem(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same without ordering this thread's memory operations before it: for
+// An arrival that orders none of this thread's memory operations: for
 // hand-overs of tensor memory, whose reads tcgen05.wait::ld has completed.  A
 // releasing arrival would wait for the thread's global stores to be done.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar)
