@@ -122,10 +122,11 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, i
         T.e = ragged::expert_of(s.list, a.E, t);
         at = t - s.list.tiles[T.e];
     }
-    const int nt = at / n_mt;
-    T.m0 = (at - nt * n_mt) * kTileM;
     T.lo = s.list.lo[T.e];
     T.rows = s.list.rows(T.e);
+    int mt, nt;
+    ragged::place(at, n_mt, OP == kWgrad ? n_nt : (T.rows + kTileN - 1) / kTileN, mt, nt);
+    T.m0 = mt * kTileM;
     T.n0 = nt * kTileN;
     T.n = min(kTileN, (OP == kWgrad ? a.C : T.rows) - T.n0);
     T.steps = ((OP == kWgrad ? T.rows : a.J) + kStep - 1) / kStep;

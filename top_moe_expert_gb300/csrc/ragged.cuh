@@ -77,5 +77,19 @@ __device__ __forceinline__ int expert_of(const List &l, int E, int t)
     return a;
 }
 
+// The place of the at-th tile of a grid of n_mt x n_nt tiles: bands of kBand tiles
+// along mt, each walked along nt, so that the tiles that run at the same time
+// form a near-square of the grid and share their operands' rows in the L2 (one
+// product of 8192 x 8192 x 8192 in bf16: 567 us, 611 along mt first; at half and
+// at twice the band 582 and 579).
+constexpr int kBand = 8;
+__device__ __forceinline__ void place(int at, int n_mt, int n_nt, int &mt, int &nt)
+{
+    const int band = at / (kBand * n_nt), width = min(kBand, n_mt - band * kBand);
+    at -= band * kBand * n_nt;
+    nt = at / width;
+    mt = band * kBand + at - nt * width;
+}
+
 }  // namespace ragged
 }  // namespace moe
