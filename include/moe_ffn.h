@@ -485,7 +485,7 @@ moe_status_t moe_ffn_decode_noalloc(const void *x, int32_t xdt, int32_t M, int32
  *                         accumulate = 1; an expert without rows adds zero)
  *   for the rows r of expert e.  y [R][N], dx [R][K] and dw [E][N][K] are of dt
  *   or MOE_FP32; sums are FP32, rounded once (for FP32 results, and for
- *   16-bit ones past 16384 contracted elements, in parts of 768 elements added
+ *   16-bit ones past 16384 contracted elements, in parts of 512 elements added
  *   to nearest, so that long sums do not drift); padding rows of y and dx are
  *   set to zero.  The same call gives the same bits, and among calls
  *   of more than four rows (and among those of at most four, which have their

@@ -650,16 +650,39 @@ def _arg(t, name: str, dtypes, dim, device=None):
     return t.shape
 
 
-def _launch(dev, name: str, *args) -> None:
-    """The entry point `name` with dev current; raises on a refusal."""
+# The calls of a single token take about as long on the host as on the GPU, so
+# the functions below check their arguments in one expression where all is in
+# order, and go to the checks that name what is not only when it fails.
+_raw_stream, _current_gpu = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _launch(gpu: int, name: str, *args) -> None:
+    """The entry point `name` on the GPU of that index; raises on a refusal."""
     fn = getattr(lib(), name)
-    if dev.type == "cuda" and dev.index != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+    if gpu >= 0 and gpu != _current_gpu():
+        with torch.cuda.device(gpu):
             status = fn(*args)
     else:
         status = fn(*args)
     if status != MOE_OK:
         raise MoeError(status, name)
+
+
+def _on(stream, gpu: int, dev):
+    """The handle of the stream to launch on."""
+    return _raw_stream(gpu) if stream is None and gpu >= 0 else _stream(stream, dev)
+
+
+def _fit(a, b, b_dim: int, offsets) -> bool:
+    """Whether a [., .] and b are 16-bit tensors of one type and offsets [.]
+    int32, all contiguous and on one GPU."""
+    try:
+        gpu, dt = a.get_device(), a.dtype
+        return (gpu >= 0 and dt in _DT16 and b.dtype is dt and offsets.dtype is torch.int32 and b.get_device() == gpu
+                and offsets.get_device() == gpu and a.is_contiguous() and b.is_contiguous() and offsets.is_contiguous()
+                and a.dim() == 2 and b.dim() == b_dim and offsets.dim() == 1)
+    except AttributeError:
+        return False
 
 
 def _status(dev_status, dev):
@@ -669,9 +692,15 @@ def _status(dev_status, dev):
     return _need(dev_status, "dev_status", _IDS, min_numel=2, device=dev).data_ptr()
 
 
-def _groups(offsets, dev) -> int:
-    """Check the group offsets; returns the number of experts."""
-    n, = _arg(offsets, "offsets", _IDS, 1, dev)
+def _need_pair(a, a_name: str, b, b_name: str, b_dim: int, offsets) -> None:
+    """What _fit asks, with the reason why not."""
+    _arg(a, a_name, _DT16, 2)
+    _arg(b, b_name, (a.dtype,), b_dim, a.device)
+    _arg(offsets, "offsets", _IDS, 1, a.device)
+
+
+def _experts(offsets) -> int:
+    n = offsets.shape[0]
     if n < 2:
         raise ValueError(f"offsets must be [E + 1], not [{n}]")
     return n - 1
@@ -683,10 +712,10 @@ def _result(t, name: str, shape, dtype, dtypes, dev, stream):
     and is not reused before the current stream, which gets it, is past it."""
     if t is not None:
         return _need(t, name, dtypes, shape, device=dev)
+    if stream is None and dtype in dtypes:
+        return torch.empty(shape, dtype=dtype, device=dev)
     if dtype not in dtypes:
         raise ValueError(f"{name} cannot be {dtype}; expected {' or '.join(str(d) for d in dtypes)}")
-    if stream is None or dev.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream(dev))
@@ -698,15 +727,15 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_
     """y [R, N]: rows offsets[e] .. offsets[e+1] - 1 of x [R, K] times w[e]^T,
     w [E, N, K] of x's type (bf16 or fp16); rows past offsets[E] give zeros.
     out_dtype: x's type (default) or float32."""
-    R, K = _arg(x, "x", _DT16, 2)
-    dev, dt = x.device, x.dtype
-    E = _groups(offsets, dev)
-    e, N, k = _arg(w, "w", (dt,), 3, dev)
+    if not _fit(x, w, 3, offsets):
+        _need_pair(x, "x", w, "w", 3, offsets)
+    (R, K), (e, N, k), E = x.shape, w.shape, _experts(offsets)
     if e != E or k != K:
         raise ValueError(f"w must be [E={E}, N, K={K}], not {tuple(w.shape)}")
+    gpu, dev, dt = x.get_device(), x.device, x.dtype
     y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev, stream)
-    _launch(dev, "moe_grouped_mm", x.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K, y.data_ptr(),
-            _DT[y.dtype], _status(dev_status, dev), _stream(stream, dev))
+    _launch(gpu, "moe_grouped_mm", x.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K, y.data_ptr(),
+            _DT[y.dtype], _status(dev_status, dev), _on(stream, gpu, dev))
     return y
 
 
@@ -714,15 +743,15 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
                          dev_status=None, stream=None):
     """dx [R, K], the gradient of moe_grouped_mm's x: rows of dy [R, N] times
     their expert's w[e] [N, K]; rows past offsets[E] give zeros."""
-    R, N = _arg(dy, "dy", _DT16, 2)
-    dev, dt = dy.device, dy.dtype
-    E = _groups(offsets, dev)
-    e, n, K = _arg(w, "w", (dt,), 3, dev)
+    if not _fit(dy, w, 3, offsets):
+        _need_pair(dy, "dy", w, "w", 3, offsets)
+    (R, N), (e, n, K), E = dy.shape, w.shape, _experts(offsets)
     if e != E or n != N:
         raise ValueError(f"w must be [E={E}, N={N}, K], not {tuple(w.shape)}")
+    gpu, dev, dt = dy.get_device(), dy.device, dy.dtype
     dx = _result(dx, "dx", (R, K), out_dtype or dt, (dt, torch.float32), dev, stream)
-    _launch(dev, "moe_grouped_mm_dgrad", dy.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
-            dx.data_ptr(), _DT[dx.dtype], _status(dev_status, dev), _stream(stream, dev))
+    _launch(gpu, "moe_grouped_mm_dgrad", dy.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
+            dx.data_ptr(), _DT[dx.dtype], _status(dev_status, dev), _on(stream, gpu, dev))
     return dx
 
 
@@ -731,17 +760,17 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     """dw [E, N, K], the gradient of moe_grouped_mm's w: over each expert's
     rows the sum of dy [R, N] outer x [R, K].  accumulate adds it to the dw
     given."""
-    R, N = _arg(dy, "dy", _DT16, 2)
-    dev, dt = dy.device, dy.dtype
-    r, K = _arg(x, "x", (dt,), 2, dev)
+    if not _fit(dy, x, 2, offsets):
+        _need_pair(dy, "dy", x, "x", 2, offsets)
+    (R, N), (r, K), E = dy.shape, x.shape, _experts(offsets)
     if r != R:
         raise ValueError(f"x must be [R={R}, K], not {tuple(x.shape)}")
-    E = _groups(offsets, dev)
+    gpu, dev, dt = dy.get_device(), dy.device, dy.dtype
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
     dw = _result(dw, "dw", (E, N, K), out_dtype, (dt, torch.float32), dev, stream)
-    _launch(dev, "moe_grouped_mm_wgrad", dy.data_ptr(), x.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
-            dw.data_ptr(), _DT[dw.dtype], 1 if accumulate else 0, _status(dev_status, dev), _stream(stream, dev))
+    _launch(gpu, "moe_grouped_mm_wgrad", dy.data_ptr(), x.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
+            dw.data_ptr(), _DT[dw.dtype], 1 if accumulate else 0, _status(dev_status, dev), _on(stream, gpu, dev))
     return dw
 
 
@@ -790,6 +819,24 @@ class Fp4:
     alpha: torch.Tensor | None = None
 
     def __post_init__(self):
+        q, s, alpha, block = self.q, self.s, self.alpha, _FP4_BLOCK.get(self.fmt)
+        try:
+            gpu, (*lead, half), (*slead, cols) = q.get_device(), q.shape, s.shape
+            ok = (gpu >= 0 and block is not None and q.dtype is torch.uint8 and s.dtype is torch.uint8
+                  and s.get_device() == gpu and q.is_contiguous() and s.is_contiguous() and len(lead) in (1, 2) and half > 0
+                  and half % 16 == 0 and slead == lead and cols == (2 * half // block + 15) // 16 * 16)
+            if ok and alpha is not None:
+                ok = (block == 16 and alpha.dtype is torch.float32 and alpha.get_device() == gpu and alpha.is_contiguous()
+                      and alpha.dim() == 1 and alpha.shape[0] == (lead[0] if len(lead) == 2 else 1))
+            elif ok:
+                ok = block == 32
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            self._need()
+
+    def _need(self):
+        """What __post_init__ asks, with the reason why not."""
         dim = 3 if isinstance(self.q, torch.Tensor) and self.q.dim() == 3 else 2
         *lead, half = _arg(self.q, "fp4.q", _U8, dim)
         dev = self.q.device
@@ -810,14 +857,14 @@ def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stre
     (q uint8 [..., K/2], s uint8 [..., Ks]).  alpha (NVFP4): float32 [groups],
     each for an equal run of rows."""
     *lead, K = _arg(v, "v", _DT, None)
-    dev = v.device
+    gpu, dev = v.get_device(), v.device
     Ks = _fp4_shape(K, fmt, "v")
     rows = v.numel() // K
     groups = _fp4_alpha(alpha, fmt, rows, dev)
     q = _result(q, "q", (*lead, K // 2), torch.uint8, _U8, dev, stream)
     s = _result(s, "s", (*lead, Ks), torch.uint8, _U8, dev, stream)
-    _launch(dev, "moe_fp4_quantize", v.data_ptr(), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, q.data_ptr(),
-            s.data_ptr(), _stream(stream, dev))
+    _launch(gpu, "moe_fp4_quantize", v.data_ptr(), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, q.data_ptr(),
+            s.data_ptr(), _on(stream, gpu, dev))
     return q, s
 
 
@@ -825,14 +872,15 @@ def moe_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, fmt: int, alpha=None, o
                        stream=None):
     """The values v [..., K] that codes and scales stand for."""
     *lead, half = _arg(q, "q", _U8, None)
-    dev, K = q.device, half * 2
+    gpu, dev, K = q.get_device(), q.device, half * 2
     Ks = _fp4_shape(K, fmt, "q")
-    _need(s, "s", _U8, (*lead, Ks), device=dev)
+    if _arg(s, "s", _U8, None, dev) != (*lead, Ks):
+        raise ValueError(f"s has shape {tuple(s.shape)}; expected {(*lead, Ks)}")
     rows = q.numel() // half
     groups = _fp4_alpha(alpha, fmt, rows, dev)
     v = _result(v, "v", (*lead, K), out_dtype, _DT, dev, stream)
-    _launch(dev, "moe_fp4_dequantize", q.data_ptr(), s.data_ptr(), rows, K, fmt, _ptr(alpha), groups, v.data_ptr(),
-            _DT[v.dtype], _stream(stream, dev))
+    _launch(gpu, "moe_fp4_dequantize", q.data_ptr(), s.data_ptr(), rows, K, fmt, _ptr(alpha), groups, v.data_ptr(),
+            _DT[v.dtype], _on(stream, gpu, dev))
     return v
 
 
@@ -840,18 +888,19 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
                        stream=None):
     """y [R, N]: moe_grouped_mm on 4-bit operands, x [R, K] and w [E, N, K] of
     the same format (offsets [0, R] with E = 1: the dense product)."""
-    dev = x.q.device
-    E = _groups(offsets, dev)
+    gpu, dev = x.q.get_device(), x.q.device
+    _arg(offsets, "offsets", _IDS, 1, dev)
+    E = _experts(offsets)
     if x.q.dim() != 2 or w.q.dim() != 3 or x.fmt != w.fmt:
         raise ValueError("x must be [R, K] and w [E, N, K] of one format")
-    if w.q.device != dev:
+    if w.q.get_device() != gpu:
         raise ValueError(f"w is on {w.q.device}; the call's tensors are on {dev}")
     (R, xh), (e, N, half) = x.q.shape, w.q.shape
     K = half * 2
     if e != E or xh != half:
         raise ValueError(f"w is [{e}, {N}, {K}]; offsets are for {E} experts and x has K = {xh * 2}")
     y = _result(y, "y", (R, N), out_dtype, _DT, dev, stream)
-    _launch(dev, "moe_grouped_mm_fp4", x.q.data_ptr(), x.s.data_ptr(), _ptr(x.alpha), w.q.data_ptr(), w.s.data_ptr(),
-            _ptr(w.alpha), x.fmt, offsets.data_ptr(), R, E, N, K, y.data_ptr(), _DT[y.dtype], _status(dev_status,
-            dev), _stream(stream, dev))
+    _launch(gpu, "moe_grouped_mm_fp4", x.q.data_ptr(), x.s.data_ptr(), _ptr(x.alpha), w.q.data_ptr(), w.s.data_ptr(),
+            _ptr(w.alpha), x.fmt, offsets.data_ptr(), R, E, N, K, y.data_ptr(), _DT[y.dtype], _status(dev_status, dev),
+            _on(stream, gpu, dev))
     return y

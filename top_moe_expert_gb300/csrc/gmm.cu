@@ -46,11 +46,11 @@ constexpr int kMaxStages = 8;
 
 // The tensor cores add to an FP32 accumulator without rounding to nearest, so a
 // long sum drifts (measured: 1.1e-9 of the result per contracted element, 4.4e-6
-// at 4096).  Sum kernels end the accumulation every kSpan steps (768 elements)
-// and add the parts in registers, rounded to nearest: 7e-7 at any length.  FP32
+// at 4096).  Sum kernels end the accumulation every kSpan steps (512 elements)
+// and add the parts in registers, rounded to nearest: 5e-7 at any length.  FP32
 // results take them always, 16-bit ones -- whose own rounding is 2^-9 or 2^-12 --
 // where the contraction can be longer than kLong.
-constexpr int kSpan = 12;
+constexpr int kSpan = 8;
 constexpr int kLong = 16384;
 
 // Draining warps, one to a quadrant of tensor memory, or two with half of the
