@@ -59,7 +59,7 @@ struct Args {
 struct Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t sfull[kSlots], sdone[kSlots], sready[kSlots], sempty[kSlots];
-    uint64_t accf[2], acce[2];
+    uint64_t accf[2], acce[2], fin;
     uint32_t tmem;
     int abort;
     ragged::List list;
@@ -120,6 +120,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             tc::mbar_init(bar(s.accf[i]), 1);
             tc::mbar_init(bar(s.acce[i]), 8);
         }
+        tc::mbar_init(bar(s.fin), 1);
         s.abort = 0;
         tc::fence_mbar_init();
         tc::prefetch_tmap(&tmA);
@@ -264,6 +265,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 }
                 tc::tc_commit_pair(bar(s.accf[buf]));
             }
+            tc::tc_commit_pair(bar(s.fin));
         }
     } else if (warp == 3) {
         // tell the leader of every arranged slot, one thread for the three
@@ -373,6 +375,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) {
+        // the leader's last MMA is done and has told both CTAs so
+        volatile int never = 0;
+        tc::mbar_wait(bar(s.fin), 0, &never, kWaitNs);
+    }
     tc::cluster_sync();                                  // neither CTA ends while the other still reaches into it
     if (warp == 1) {
         tc::tc_fence_after();
