@@ -215,6 +215,32 @@ def test_other_stream_and_graph_capture():
     _same(dw, ref.wgrad(dy.cpu(), x.cpu(), sizes)[0], "dw replayed")
 
 
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, forward, gradients and few rows, each with the result it has alone."""
+    g = _gen(19)
+    jobs = []
+    for sizes, N, K in (([300, 0, 77], 512, 640), ([3], 1024, 2048), ([40] * 9, 256, 512), ([1, 0, 700], 768, 256)):
+        R, E = sum(sizes), len(sizes)
+        x, w, dy = _ints((R, K), g, BF).cuda(), _ints((E, N, K), g, BF).cuda(), _ints((R, N), g, BF).cuda()
+        jobs.append((x, w, dy, ref.offsets_of(sizes).cuda()))
+
+    def run(job, stream=None):
+        x, w, dy, off = job
+        return (moe.moe_grouped_mm(x, w, off, stream=stream), moe.moe_grouped_mm_dgrad(dy, w, off, stream=stream),
+                moe.moe_grouped_mm_wgrad(dy, x, off, stream=stream))
+
+    alone = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(40):
+        got.append((i % 4, run(jobs[i % 4], streams[(i // 2) % 2])))
+    torch.cuda.synchronize()
+    for j, out in got:
+        for a, b in zip(out, alone[j]):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("bad", [[0, 10, 5, 20], [-3, 4, 9, 20], [0, 8, 12, 4000], [2, 8, 12, 20]])
 def test_offsets_out_of_contract_are_clamped_and_reported(bad):
     g = _gen(13)

@@ -37,7 +37,7 @@ struct Unit {
 // rather than 142 for 98304 x 2048 values back).
 __device__ __forceinline__ void ld32(const void *p, uint4 &a, uint4 &b)
 {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(p));
 }
 
@@ -60,7 +60,7 @@ struct Alpha {
         const uint32_t i = rows_per ? r / rows_per : 0;            // 0: one alpha for all rows
         if (i != at) {
             at = i;
-            a = __ldg(alpha + i);
+            a = alpha[i];
             g = 1.0f / (6.0f * a);
         }
     }
@@ -157,9 +157,12 @@ struct Place {
 
 template <typename VT, int FMT>
 __global__ void __launch_bounds__(256)
-quantize_kernel(const VT *__restrict__ v, int64_t units, uint32_t nq, int Ks, const float *__restrict__ alpha,
-                uint32_t rows_per_alpha, bool wide, uint32_t *__restrict__ q, uint8_t *__restrict__ s)
+quantize_kernel(const VT *v, int64_t units, uint32_t nq, int Ks, const float *alpha,
+                uint32_t rows_per_alpha, bool wide, uint32_t *q, uint8_t *s)
 {
+    // chained by programmatic dependent launch
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     Alpha al(alpha, rows_per_alpha);
     constexpr int kLanes = block_of(FMT) / 8, kPer = 32 / block_of(FMT);
     const int lane = threadIdx.x & 31;
@@ -180,7 +183,7 @@ quantize_kernel(const VT *__restrict__ v, int64_t units, uint32_t nq, int Ks, co
                 } else {
 #pragma unroll
                     for (int k = 0; k < static_cast<int>(sizeof(VT) / 2); ++k)
-                        in[j].w[k] = ld_stream_u4(p + k);
+                        in[j].w[k] = ld_once_u4(p + k);
                 }
             }
         }
@@ -220,9 +223,12 @@ quantize_kernel(const VT *__restrict__ v, int64_t units, uint32_t nq, int Ks, co
 
 template <typename VT, int FMT>
 __global__ void __launch_bounds__(256)
-dequantize_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ s, int64_t units, uint32_t nq, int Ks,
-                  const float *__restrict__ alpha, uint32_t rows_per_alpha, bool wide, VT *__restrict__ v)
+dequantize_kernel(const uint32_t *q, const uint8_t *s, int64_t units, uint32_t nq, int Ks,
+                  const float *alpha, uint32_t rows_per_alpha, bool wide, VT *v)
 {
+    // chained by programmatic dependent launch
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     constexpr int kPer = 32 / block_of(FMT);
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -237,7 +243,7 @@ dequantize_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ s,
             if (u < units) {
                 c[j] = __ldcs(q + u);
                 f[j] = scale_value<FMT>(s[static_cast<int64_t>(at.row) * Ks + at.piece * kPer + (kPer == 2 ? (lane >> 1) & 1 : 0)]);
-                al[j] = FMT == MOE_FP4_NVFP4 ? __ldg(alpha + (rows_per_alpha ? at.row / rows_per_alpha : 0u)) : 1.f;
+                al[j] = FMT == MOE_FP4_NVFP4 ? alpha[rows_per_alpha ? at.row / rows_per_alpha : 0u] : 1.f;
             }
         }
 #pragma unroll
@@ -331,14 +337,16 @@ MOE_API moe_status_t moe_fp4_quantize(const void *v, int32_t vdt, int64_t rows, 
     if (st != MOE_OK || rows == 0)
         return st;
     const int64_t units = rows * (K / 8);
+    cudaError_t e = cudaSuccess;
     by_type(vdt, [&](auto t) {
         using T = decltype(t);
         auto k = fmt == MOE_FP4_NVFP4 ? quantize_kernel<T, MOE_FP4_NVFP4> : quantize_kernel<T, MOE_FP4_MXFP4>;
-        k<<<grid_of(units), 256, 0, as_stream(stream)>>>(static_cast<const T *>(v), units, K / 32, scale_cols(K, fmt), alpha,
-                                                         groups == 1 ? 0u : static_cast<uint32_t>(rows / groups), aligned(v, 32),
-                                                         reinterpret_cast<uint32_t *>(q), s);
+        e = launch_pdl(k, dim3(grid_of(units)), dim3(256), 0, as_stream(stream), static_cast<const T *>(v), units,
+                       static_cast<uint32_t>(K / 32), scale_cols(K, fmt), alpha,
+                       groups == 1 ? 0u : static_cast<uint32_t>(rows / groups), aligned(v, 32),
+                       reinterpret_cast<uint32_t *>(q), s);
     });
-    return launch_status();
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 MOE_API moe_status_t moe_fp4_dequantize(const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t fmt,
@@ -348,12 +356,13 @@ MOE_API moe_status_t moe_fp4_dequantize(const uint8_t *q, const uint8_t *s, int6
     if (st != MOE_OK || rows == 0)
         return st;
     const int64_t units = rows * (K / 8);
+    cudaError_t e = cudaSuccess;
     by_type(vdt, [&](auto t) {
         using T = decltype(t);
         auto k = fmt == MOE_FP4_NVFP4 ? dequantize_kernel<T, MOE_FP4_NVFP4> : dequantize_kernel<T, MOE_FP4_MXFP4>;
-        k<<<grid_of(units), 256, 0, as_stream(stream)>>>(reinterpret_cast<const uint32_t *>(q), s, units, K / 32,
-                                                         scale_cols(K, fmt), alpha, groups == 1 ? 0u : static_cast<uint32_t>(rows / groups), aligned(v, 32),
-                                                         static_cast<T *>(v));
+        e = launch_pdl(k, dim3(grid_of(units)), dim3(256), 0, as_stream(stream), reinterpret_cast<const uint32_t *>(q), s, units,
+                       static_cast<uint32_t>(K / 32), scale_cols(K, fmt), alpha,
+                       groups == 1 ? 0u : static_cast<uint32_t>(rows / groups), aligned(v, 32), static_cast<T *>(v));
     });
-    return launch_status();
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -11,6 +11,16 @@ namespace fp4 {
 __host__ __device__ constexpr int block_of(int fmt) { return fmt == MOE_FP4_NVFP4 ? 16 : 32; }
 __host__ __device__ constexpr int scale_cols(int K, int fmt) { return (K / block_of(fmt) + 15) / 16 * 16; }
 
+// 16-byte load of data that is read once.  Not of the non-coherent kind, here and
+// in the other kernels that start before their predecessor on the stream has
+// ended: what they read may be what it wrote.
+__device__ __forceinline__ uint4 ld_once_u4(const void *p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }

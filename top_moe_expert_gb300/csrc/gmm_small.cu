@@ -31,7 +31,7 @@ struct Groups {
 
 // The groups that have rows, the same list in every CTA.  Offsets are clamped
 // as in ragged.cuh.
-__device__ __forceinline__ void make_groups(Groups &g, const int32_t *__restrict__ off, int E, int R)
+__device__ __forceinline__ void make_groups(Groups &g, const int32_t *off, int E, int R)
 {
     if (threadIdx.x < kRows)
         g.expert[threadIdx.x] = -1;
@@ -91,11 +91,11 @@ __device__ __forceinline__ void pair_of(const Args &a, int e, int r0, int n, int
     float acc[2][NT] = {};
 #pragma unroll kUnroll
     for (int k = lane * 8; k < a.K; k += 256) {
-        const uint4 w0 = ld_stream_u4(w + k), w1 = ld_stream_u4(w + a.K + k);
+        const uint4 w0 = fp4::ld_once_u4(w + k), w1 = fp4::ld_once_u4(w + a.K + k);
         uint4 xv[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-            xv[t] = __ldg(reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(t) * a.K + k));
+            xv[t] = *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(t) * a.K + k);
         float f0[8], f1[8];
         unpack8<T>(w0, f0);
         unpack8<T>(w1, f1);

@@ -10,7 +10,7 @@ namespace ragged {
 constexpr int kMaxExperts = 1024;
 
 // Whether offsets are what the contract says; a call reports it once.
-__device__ __forceinline__ void report_bad(const int32_t *__restrict__ off, int R, int e, int32_t *dev_status)
+__device__ __forceinline__ void report_bad(const int32_t *off, int R, int e, int32_t *dev_status)
 {
     if (dev_status && (off[e] < 0 || off[e] > off[e + 1] || off[e + 1] > R || (e == 0 && off[0] != 0)))
         atomicCAS(dev_status + 1, 0, static_cast<int32_t>(MOE_ERR_BOUNDS));
@@ -27,7 +27,7 @@ struct List {
     __device__ __forceinline__ int rows(int e) const { return max(lo[e + 1] - lo[e], 0); }
 };
 
-__device__ __forceinline__ void make_list(List &l, const int32_t *__restrict__ off, int E, int R, int mt, int nt)
+__device__ __forceinline__ void make_list(List &l, const int32_t *off, int E, int R, int mt, int nt)
 {
     const int per = (E + blockDim.x - 1) / blockDim.x;
     const int e0 = min(static_cast<int>(threadIdx.x) * per, E), e1 = min(e0 + per, E);

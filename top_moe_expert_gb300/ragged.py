@@ -10,6 +10,8 @@ Routes are ordered by expert (moe_align_block_size with blocks of one row, no
 padding between groups), the experts' products run on the groups as they are
 (moe_grouped_mm, its gradients, moe_grouped_mm_fp4), and each token sums its
 slots in slot order.  Routes to experts outside [0, E) contribute nothing.
+moe_topk_softmax has no gradient; a router is trained through weights formed
+from its choice, w = logits.gather(1, ids.long()).softmax(-1) (the same values).
 Gathers, SwiGLU and the sum over slots are torch operations.
 """
 from __future__ import annotations
