@@ -437,7 +437,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             for (int h = 0; h < 32; h += 16) {
                                 uint32_t v[16];
                                 tc::tmem_ld_32x32b_x16(acc + 32 * g + h, v);
-                                tc::tmem_ld_wait();
+                                tc::tmem_ld_wait_for(v);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
                                     sum[g][h + i] += __uint_as_float(v[i]);
@@ -497,7 +497,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             if (T.steps) {
                                 tc::tmem_ld_32x32b_x32(acc + c0, v[0]);
                                 tc::tmem_ld_32x32b_x32(acc + c0 + 32, v[1]);
-                                tc::tmem_ld_wait();
+                                tc::tmem_ld_wait_for(v[0]);
+                                tc::tmem_ld_wait_for(v[1]);
                             } else {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
@@ -513,7 +514,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (int c0 = 0; c0 < T.n; c0 += 32) {
                         uint32_t v[32];
                         tc::tmem_ld_32x32b_x32(acc + c0, v);
-                        tc::tmem_ld_wait();
+                        tc::tmem_ld_wait_for(v);
                         store_y<OT>(v, tiles, flip, &tmY, out, T.lo + T.n0 + c0, T.n - c0, m, a.M, lane);
                     }
                 }

@@ -346,7 +346,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (int c0 = 0; c0 < T.n; c0 += 32) {
                 uint32_t v[32];
                 tc::tmem_ld_32x32b_x32(acc + c0, v);
-                tc::tmem_ld_wait();
+                tc::tmem_ld_wait_for(v);
                 if (T.n - c0 < 32) {                     // a TMA store would reach into the next group's rows
                     gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f);
                     break;

@@ -208,6 +208,17 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar)
                  ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
+// Waits for this thread's tensor-memory loads, v's among them.  v passes through
+// the wait, so that nothing computed from it can be moved before it.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N])
+{
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+r"(v[i]));
+}
+
 // Each thread of the warp reads 16 consecutive columns of its TMEM lane.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16])
 {
