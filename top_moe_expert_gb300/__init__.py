@@ -807,36 +807,33 @@ def _fp4_alpha(alpha, fmt, rows, dev):
     return n
 
 
-@dataclasses.dataclass(frozen=True)
 class Fp4:
     """Rows in NVFP4 or MXFP4: q uint8 [..., K/2], s uint8 [..., Ks] and, for
     NVFP4, alpha float32 (one for activations [R, .], one per expert for
     weights [E, N, .]), as moe_fp4_quantize returns them.  Checked when the
-    object is made."""
-    fmt: int
-    q: torch.Tensor
-    s: torch.Tensor
-    alpha: torch.Tensor | None = None
+    object is made; its fields are not to be changed."""
+    __slots__ = ("fmt", "q", "s", "alpha")
 
-    def __post_init__(self):
-        q, s, alpha, block = self.q, self.s, self.alpha, _FP4_BLOCK.get(self.fmt)
+    def __init__(self, fmt: int, q: torch.Tensor, s: torch.Tensor, alpha: torch.Tensor | None = None):
+        self.fmt, self.q, self.s, self.alpha = fmt, q, s, alpha
         try:
-            gpu, (*lead, half), (*slead, cols) = q.get_device(), q.shape, s.shape
-            ok = (gpu >= 0 and block is not None and q.dtype is torch.uint8 and s.dtype is torch.uint8
-                  and s.get_device() == gpu and q.is_contiguous() and s.is_contiguous() and len(lead) in (1, 2) and half > 0
-                  and half % 16 == 0 and slead == lead and cols == (2 * half // block + 15) // 16 * 16)
+            gpu, qs, ss, block, n = q.get_device(), q.shape, s.shape, _FP4_BLOCK[fmt], q.dim()
+            half, rows = qs[-1], qs[0]
+            ok = (gpu >= 0 and q.dtype is torch.uint8 and s.dtype is torch.uint8 and s.get_device() == gpu
+                  and q.is_contiguous() and s.is_contiguous() and (n == 2 or n == 3) and s.dim() == n and half > 0
+                  and half % 16 == 0 and ss[0] == rows and ss[-2] == qs[-2] and ss[-1] == (2 * half // block + 15) // 16 * 16)
             if ok and alpha is not None:
                 ok = (block == 16 and alpha.dtype is torch.float32 and alpha.get_device() == gpu and alpha.is_contiguous()
-                      and alpha.dim() == 1 and alpha.shape[0] == (lead[0] if len(lead) == 2 else 1))
+                      and alpha.dim() == 1 and alpha.shape[0] == (rows if n == 3 else 1))
             elif ok:
                 ok = block == 32
-        except (AttributeError, ValueError):
+        except (AttributeError, IndexError, KeyError, TypeError):
             ok = False
         if not ok:
             self._need()
 
     def _need(self):
-        """What __post_init__ asks, with the reason why not."""
+        """What the constructor asks, with the reason why not."""
         dim = 3 if isinstance(self.q, torch.Tensor) and self.q.dim() == 3 else 2
         *lead, half = _arg(self.q, "fp4.q", _U8, dim)
         dev = self.q.device
