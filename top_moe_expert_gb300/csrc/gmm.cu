@@ -64,8 +64,9 @@ constexpr int kLong = 16384;
 // stages: with few rows per expert the time is that of streaming the weights,
 // and more of them are on the way (8 stages of 24 KB; 16 KB each are weights).
 // 127 us rather than 132 for 4096 rows over 128 experts of 1536 x 2048, 13.6
-// rather than 16.1 (dgrad) for 800 rows over 40 of 1000 x 520; at more than 64
-// rows per expert they read the weights' tiles twice.
+// rather than 16.1 (dgrad) for 800 rows over 40 of 1000 x 520.  Past 64 rows per
+// expert more and more groups take two tiles, which read the weights twice: 169
+// rather than 158 us at 80 rows (Zipf) over 16 of 4096 x 7168.
 enum Kind { kPlain = 0, kNarrow = 1, kSum = 2 };
 constexpr int drain_of(int kind) { return kind == kSum ? 8 : 4; }
 constexpr int tile_n(int kind) { return kind == kNarrow ? 128 : 256; }

@@ -83,9 +83,10 @@ __device__ __forceinline__ int expert_of(const List &l, int E, int t)
 // product of 8192 x 8192 x 8192 in bf16: 567 us, 611 along mt first; at half and
 // at twice the band 582 and 579).
 constexpr int kBand = 8;
-__device__ __forceinline__ void place(int at, int n_mt, int n_nt, int &mt, int &nt)
+__host__ __device__ __forceinline__ void place(int at, int n_mt, int n_nt, int &mt, int &nt)
 {
-    const int band = at / (kBand * n_nt), width = min(kBand, n_mt - band * kBand);
+    const int band = at / (kBand * n_nt), left = n_mt - band * kBand;
+    const int width = left < kBand ? left : kBand;
     at -= band * kBand * n_nt;
     nt = at / width;
     mt = band * kBand + at - nt * width;
