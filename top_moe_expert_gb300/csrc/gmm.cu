@@ -72,11 +72,21 @@ constexpr int kLong = 16384;
 // rather than 16.1 (dgrad) for 800 rows over 40 of 1000 x 520.  Past 64 rows per
 // expert more and more groups take two tiles, which read the weights twice: 169
 // rather than 158 us at 80 rows (Zipf) over 16 of 4096 x 7168.
-enum Kind { kPlain = 0, kNarrow = 1, kSum = 2 };
-constexpr int drain_of(int kind) { return kind == kSum ? 8 : 4; }
-constexpr int tile_n(int kind) { return kind == kNarrow ? 128 : 256; }
-constexpr int stages_of(int op, int kind) { return kind == kNarrow ? 8 : op == kWgrad || kind == kSum ? 5 : 6; }
-constexpr int stage_bytes(int kind) { return 16384 + 64 * tile_n(kind); }   // 128 rows and half a tile's, 128 bytes each
+//
+// Sum kernels have both forms: of the forward and dgrad with tiles of 128 rows,
+// of wgrad with a second staging tile per warp in place of a stage, as with few
+// rows per expert dw's stream bounds it (FP32 results, 32 rows for each of 128
+// experts of 1536 x 2048: forward 132 rather than 137 us, wgrad 287 rather than
+// 292; 20 rows for each of 40 of 1000 x 520: wgrad 19.6 rather than 20.6).
+enum Kind { kPlain = 0, kNarrow = 1, kSum = 2, kSumFew = 3 };
+constexpr bool sums(int kind) { return kind == kSum || kind == kSumFew; }
+constexpr int drain_of(int kind) { return sums(kind) ? 8 : 4; }
+constexpr int tile_n(int op, int kind) { return kind == kNarrow || (kind == kSumFew && op != kWgrad) ? 128 : 256; }
+constexpr int stages_of(int op, int kind)
+{
+    return kind == kNarrow ? 8 : kind == kSumFew ? (op == kWgrad ? 4 : 7) : op == kWgrad || kind == kSum ? 5 : 6;
+}
+constexpr int stage_bytes(int op, int kind) { return 16384 + 64 * tile_n(op, kind); }   // 128 rows and half a tile's
 constexpr int staging_of(int op, int kind) { return op == kWgrad && kind != kSum ? 8192 : 4096; }
 constexpr int threads_of(int kind) { return 32 * (4 + drain_of(kind)); }
 
@@ -105,10 +115,11 @@ struct Shared {
 
 constexpr int smem_of(int op, int kind)
 {
-    return 1024 + stages_of(op, kind) * stage_bytes(kind) + drain_of(kind) * staging_of(op, kind) + static_cast<int>(sizeof(Shared));
+    return 1024 + stages_of(op, kind) * stage_bytes(op, kind) + drain_of(kind) * staging_of(op, kind) + static_cast<int>(sizeof(Shared));
 }
 static_assert(smem_of(kFwd, kPlain) <= 232448 && smem_of(kFwd, kNarrow) <= 232448 && smem_of(kWgrad, kPlain) <= 232448 &&
-              smem_of(kFwd, kSum) <= 232448, "shared memory of one CTA");
+              smem_of(kFwd, kSum) <= 232448 && smem_of(kFwd, kSumFew) <= 232448 && smem_of(kWgrad, kSumFew) <= 232448,
+              "shared memory of one CTA");
 
 struct Tile {
     int e, m0, lo, rows;       // expert, first left row, the expert's rows
@@ -155,16 +166,15 @@ __device__ __forceinline__ void store_y(const uint32_t (&v)[32], uint8_t *tiles,
 
 // 128 bytes of this lane's row of dw (row m of expert e, columns from c on) in
 // w: through a staging tile (32 rows, 128-byte swizzle) and out, or added, by
-// TMA, which cuts them at the expert's last row and column.  two: the warp has
-// two tiles and alternates.
-template <typename OT>
-__device__ __forceinline__ void store_tile(const uint32_t (&w)[32], uint8_t *tile, bool two, const CUtensorMap *map, int c, int m,
+// TMA, which cuts them at the expert's last row and column.  TWO: the warp has
+// two tiles and alternates; the last but one store has read its tile by then.
+template <typename OT, bool TWO>
+__device__ __forceinline__ void store_tile(const uint32_t (&w)[32], uint8_t *tiles, int &flip, const CUtensorMap *map, int c, int m,
                                            int e, int M, int lane, bool add)
 {
-    if (two)
-        tc::bulk_wait_read<1>();
-    else
-        tc::bulk_wait_read<0>();
+    uint8_t *tile = tiles + (TWO ? 4096 * flip : 0);
+    flip ^= 1;
+    tc::bulk_wait_read<TWO ? 1 : 0>();
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < 8; ++u)
@@ -214,9 +224,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
     // tmB16: B in boxes of 16 rows (fwd, dgrad); tmY: the result
-    constexpr bool SUM = KIND == kSum;
+    constexpr bool SUM = sums(KIND);
     constexpr int kStages = stages_of(OP, KIND), kDrain = drain_of(KIND), kStaging = staging_of(OP, KIND);
-    constexpr int kTileN = tile_n(KIND), kStageBytes = stage_bytes(KIND);
+    constexpr bool kTwo = kStaging == 8192;             // wgrad: two staging tiles of 128-byte rows
+    constexpr int kTileN = tile_n(OP, KIND), kStageBytes = stage_bytes(OP, KIND);
     extern __shared__ uint8_t smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -420,11 +431,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const Tile T = tile_of<OP, kTileN>(a, s, t, n_mt, n_nt);
             const int m = T.m0 + 128 * rank + 32 * q + lane;
             if constexpr (SUM) {
-                // this warp's 128 columns: the spans' parts added in registers
-                const int h0 = 128 * ((warp - 4) >> 2);
-                float sum[4][32];
+                // this warp's half of the columns: the spans' parts added in
+                // registers
+                constexpr int kGroups = kTileN / 64;
+                const int h0 = kTileN / 2 * ((warp - 4) >> 2);
+                float sum[kGroups][32];
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int g = 0; g < kGroups; ++g)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         sum[g][i] = 0.f;
@@ -437,7 +450,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tc::tc_fence_after();
                     const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16) + h0;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
+                    for (int g = 0; g < kGroups; ++g) {
                         if (h0 + 32 * g < T.n) {
 #pragma unroll
                             for (int h = 0; h < 32; h += 16) {
@@ -466,7 +479,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         v[i] = __float_as_uint(sum[g][i]);
                 };
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < kGroups; ++g) {
                     const int c0 = h0 + 32 * g;
                     if (c0 >= T.n || (OP == kWgrad && T.steps == 0 && a.accumulate))
                         continue;
@@ -475,13 +488,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if constexpr (OP != kWgrad) {
                         store_y<OT>(v, tiles, flip, &tmY, out, T.lo + T.n0 + c0, T.n - c0, m, a.M, lane);
                     } else if constexpr (sizeof(OT) == 4) {
-                        store_tile<OT>(v, tiles, false, &tmY, T.n0 + c0, m, T.e, a.M, lane, a.accumulate);
+                        store_tile<OT, kTwo>(v, tiles, flip, &tmY, T.n0 + c0, m, T.e, a.M, lane, a.accumulate);
                     } else if (g % 2 == 0) {
                         uint32_t w[32];
                         round_dw<OT>(v, w, out, T.n0 + c0, m, T.e, a.M, a.C, a.accumulate);
-                        bits(g + 1 < 4 ? g + 1 : g, v);
+                        bits(g + 1 < kGroups ? g + 1 : g, v);
                         round_dw<OT>(v, w + 16, out, T.n0 + c0 + 32, m, T.e, a.M, a.C, a.accumulate);
-                        store_tile<OT>(w, tiles, false, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
+                        store_tile<OT, kTwo>(w, tiles, flip, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
                     }
                 }
             } else {
@@ -512,8 +525,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             }
                             round_dw<OT>(v[0], w, out, T.n0 + c0, m, T.e, a.M, a.C, a.accumulate);
                             round_dw<OT>(v[1], w + 16, out, T.n0 + c0 + 32, m, T.e, a.M, a.C, a.accumulate);
-                            store_tile<OT>(w, tiles + 4096 * flip, true, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
-                            flip ^= 1;
+                            store_tile<OT, kTwo>(w, tiles, flip, &tmY, T.n0 + c0, m, T.e, a.M, lane, false);
                         }
                     }
                 } else {
@@ -599,9 +611,26 @@ static moe_status_t launch(const CUtensorMap (&tm)[4], const Args &a, int64_t mo
 }
 
 template <int OP, int KIND>
-static moe_status_t launch_16(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int64_t most_tiles, cudaStream_t s)
+static moe_status_t launch_as(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int64_t most_tiles, cudaStream_t s)
 {
+    if constexpr (sums(KIND))
+        if (odt == MOE_FP32)
+            return launch<OP, float, KIND>(tm, a, most_tiles, s);
     return odt == MOE_BF16 ? launch<OP, __nv_bfloat16, KIND>(tm, a, most_tiles, s) : launch<OP, __half, KIND>(tm, a, most_tiles, s);
+}
+
+template <int OP>
+static moe_status_t launch_kind(const CUtensorMap (&tm)[4], const Args &a, int32_t odt, int kind, int64_t most_tiles,
+                                cudaStream_t s)
+{
+    if (kind == kSum)
+        return launch_as<OP, kSum>(tm, a, odt, most_tiles, s);
+    if (kind == kSumFew)
+        return launch_as<OP, kSumFew>(tm, a, odt, most_tiles, s);
+    if constexpr (OP != kWgrad)
+        if (kind == kNarrow)
+            return launch_as<OP, kNarrow>(tm, a, odt, most_tiles, s);
+    return launch_as<OP, kPlain>(tm, a, odt, most_tiles, s);
 }
 
 static CUtensorMapDataType map_type(int32_t dt)
@@ -617,8 +646,9 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
                          const int32_t *off, void *y, int32_t ydt, int32_t *dev_status, cudaStream_t s)
 {
     const CUtensorMapDataType t = map_type(dt);
-    const int kind = ydt == MOE_FP32 || J > kLong ? kSum : R <= 64 * static_cast<int64_t>(E) ? kNarrow : kPlain;
-    const int tn = tile_n(kind);
+    const bool few = R <= 64 * static_cast<int64_t>(E), sum = ydt == MOE_FP32 || J > kLong;
+    const int kind = sum ? (few ? kSumFew : kSum) : few ? kNarrow : kPlain;
+    const int tn = tile_n(OP, kind);
     CUtensorMap tm[4];
     const bool ok = OP == kFwd ? tmap_tile(&tm[0], 3, t, 2, w, J, C, E, 64, 128) : tmap_tile(&tm[0], 3, t, 2, w, C, J, E, 64, 64);
     if (!ok || !tmap_tile(&tm[1], 2, t, 2, x, J, R, 1, 64, tn / 2) || !tmap_tile(&tm[2], 2, t, 2, x, J, R, 1, 64, 16) ||
@@ -627,11 +657,7 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
     const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
     const int64_t n_mt = (C + kTileM - 1) / kTileM;
     const int64_t tiles = n_mt * (static_cast<int64_t>(R) / tn + (E < R ? E : R));
-    if (ydt == MOE_FP32)
-        return launch<OP, float, kSum>(tm, a, tiles, s);
-    return kind == kSum      ? launch_16<OP, kSum>(tm, a, ydt, tiles, s)
-           : kind == kNarrow ? launch_16<OP, kNarrow>(tm, a, ydt, tiles, s)
-                             : launch_16<OP, kPlain>(tm, a, ydt, tiles, s);
+    return launch_kind<OP>(tm, a, ydt, kind, tiles, s);
 }
 
 }  // namespace gmm
@@ -680,11 +706,9 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
         return MOE_ERR_CUDA;
     tm[2] = tm[1];
     const Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
-    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + tile_n(kPlain) - 1) / tile_n(kPlain));
+    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + 255) / 256);
     if (tiles > INT32_MAX)
         return MOE_ERR_UNSUPPORTED;
-    if (wdt == MOE_FP32)
-        return launch<kWgrad, float, kSum>(tm, a, tiles, as_stream(stream));
-    return R > kLong ? launch_16<kWgrad, kSum>(tm, a, wdt, tiles, as_stream(stream))
-                     : launch_16<kWgrad, kPlain>(tm, a, wdt, tiles, as_stream(stream));
+    const bool few = R <= 64 * static_cast<int64_t>(E), sum = wdt == MOE_FP32 || R > kLong;
+    return launch_kind<kWgrad>(tm, a, wdt, sum ? (few ? kSumFew : kSum) : kPlain, tiles, as_stream(stream));
 }
