@@ -434,7 +434,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 // this warp's half of the columns: the spans' parts added in
                 // registers
                 constexpr int kGroups = kTileN / 64;
-                const int h0 = kTileN / 2 * ((warp - 4) >> 2);
+                const int half = (warp - 4) >> 2;
+                // the column of group g: alternate 128 bytes of dw, so that the
+                // quadrant's two warps write next to each other
+                auto col = [&](int g) {
+                    return OP == kWgrad && sizeof(OT) == 2 ? (g / 2) * 128 + 64 * half + (g & 1) * 32 : 64 * g + 32 * half;
+                };
                 float sum[kGroups][32];
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g)
@@ -448,14 +453,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (!ok)
                         break;
                     tc::tc_fence_after();
-                    const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16) + h0;
+                    const uint32_t acc = tmem + 256 * buf + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        if (h0 + 32 * g < T.n) {
+                        if (col(g) < T.n) {
 #pragma unroll
                             for (int h = 0; h < 32; h += 16) {
                                 uint32_t v[16];
-                                tc::tmem_ld_32x32b_x16(acc + 32 * g + h, v);
+                                tc::tmem_ld_32x32b_x16(acc + col(g) + h, v);
                                 tc::tmem_ld_wait_for(v);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
@@ -480,7 +485,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 };
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
-                    const int c0 = h0 + 32 * g;
+                    const int c0 = col(g);
                     if (c0 >= T.n || (OP == kWgrad && T.steps == 0 && a.accumulate))
                         continue;
                     uint32_t v[32];
