@@ -849,15 +849,34 @@ class Fp4:
             raise ValueError("fp4.alpha is only for NVFP4")
 
 
+def _fp4_rows(t, name: str, dtypes, per: int, fmt: int, alpha):
+    """Check the tensor of values (per = 1) or codes (per = 2 elements a
+    byte) and alpha; returns the leading shape, K, Ks, rows and groups."""
+    try:
+        gpu, shape, block = t.get_device(), t.shape, _FP4_BLOCK[fmt]
+        K = shape[-1] * per
+        if (gpu >= 0 and t.dtype in dtypes and t.is_contiguous() and K > 0 and K % 32 == 0
+                and (block == 32 if alpha is None else
+                     block == 16 and alpha.dtype is torch.float32 and alpha.get_device() == gpu and alpha.is_contiguous()
+                     and alpha.dim() == 1)):
+            rows, groups = t.numel() * per // K, 1 if alpha is None else alpha.shape[0]
+            if groups and rows % groups == 0:
+                return shape[:-1], K, (K // block + 15) // 16 * 16, rows, groups
+    except (AttributeError, IndexError, KeyError):
+        pass
+    *lead, last = _arg(t, name, dtypes, None)                         # the same, with the reason why not
+    K = last * per
+    Ks = _fp4_shape(K, fmt, name)
+    rows = t.numel() * per // K
+    return tuple(lead), K, Ks, rows, _fp4_alpha(alpha, fmt, rows, t.device)
+
+
 def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stream=None):
     """NVFP4 or MXFP4 codes and scales of v [..., K] (fp32, bf16 or fp16):
     (q uint8 [..., K/2], s uint8 [..., Ks]).  alpha (NVFP4): float32 [groups],
     each for an equal run of rows."""
-    *lead, K = _arg(v, "v", _DT, None)
+    lead, K, Ks, rows, groups = _fp4_rows(v, "v", _DT, 1, fmt, alpha)
     gpu, dev = v.get_device(), v.device
-    Ks = _fp4_shape(K, fmt, "v")
-    rows = v.numel() // K
-    groups = _fp4_alpha(alpha, fmt, rows, dev)
     q = _result(q, "q", (*lead, K // 2), torch.uint8, _U8, dev, stream)
     s = _result(s, "s", (*lead, Ks), torch.uint8, _U8, dev, stream)
     _launch(gpu, "moe_fp4_quantize", v.data_ptr(), _DT[v.dtype], rows, K, fmt, _ptr(alpha), groups, q.data_ptr(),
@@ -868,13 +887,10 @@ def moe_fp4_quantize(v: torch.Tensor, fmt: int, alpha=None, q=None, s=None, stre
 def moe_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, fmt: int, alpha=None, out_dtype=torch.float32, v=None,
                        stream=None):
     """The values v [..., K] that codes and scales stand for."""
-    *lead, half = _arg(q, "q", _U8, None)
-    gpu, dev, K = q.get_device(), q.device, half * 2
-    Ks = _fp4_shape(K, fmt, "q")
+    lead, K, Ks, rows, groups = _fp4_rows(q, "q", _U8, 2, fmt, alpha)
+    gpu, dev = q.get_device(), q.device
     if _arg(s, "s", _U8, None, dev) != (*lead, Ks):
         raise ValueError(f"s has shape {tuple(s.shape)}; expected {(*lead, Ks)}")
-    rows = q.numel() // half
-    groups = _fp4_alpha(alpha, fmt, rows, dev)
     v = _result(v, "v", (*lead, K), out_dtype, _DT, dev, stream)
     _launch(gpu, "moe_fp4_dequantize", q.data_ptr(), s.data_ptr(), rows, K, fmt, _ptr(alpha), groups, v.data_ptr(),
             _DT[v.dtype], _on(stream, gpu, dev))
@@ -886,7 +902,9 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
     """y [R, N]: moe_grouped_mm on 4-bit operands, x [R, K] and w [E, N, K] of
     the same format (offsets [0, R] with E = 1: the dense product)."""
     gpu, dev = x.q.get_device(), x.q.device
-    _arg(offsets, "offsets", _IDS, 1, dev)
+    if not (offsets.dtype is torch.int32 and offsets.get_device() == gpu >= 0 and offsets.dim() == 1
+            and offsets.is_contiguous()):
+        _arg(offsets, "offsets", _IDS, 1, dev)
     E = _experts(offsets)
     if x.q.dim() != 2 or w.q.dim() != 3 or x.fmt != w.fmt:
         raise ValueError("x must be [R, K] and w [E, N, K] of one format")
