@@ -72,6 +72,23 @@ def test_layer_and_gradients(M, E, k, d, I, invalid):
         assert not y[3].any() and not leaves[0].grad[3].any()
 
 
+@pytest.mark.parametrize("M", [0, 1, 3])
+def test_no_valid_route(M):
+    """No tokens, or tokens all of whose routes are invalid: zeros forward and backward, whatever x and the weights hold."""
+    E, k, d, I = 4, 2, 64, 32
+    x, w = torch.full((M, d), float("nan")), torch.full((M, k), float("inf"))
+    ids = torch.tensor([[-1, E]], dtype=torch.int32).repeat(M, 1)
+    _, _, _, w13, w2 = _problem(1, E, k, d, I, 5, False)
+    leaves = [t.cuda().requires_grad_() for t in (x.to(BF), w, w13, w2)]
+    y = ragged.expert_layer(leaves[0], ids.cuda(), *leaves[1:])
+    y.sum().backward()
+    assert y.shape == (M, d) and not y.any()
+    assert all(t.grad.shape == t.shape and not t.grad.any() for t in leaves)
+    q13, q2 = (ragged.quantize_experts(t.cuda(), moe.MOE_FP4_MXFP4) for t in (w13, w2))
+    y4 = ragged.expert_layer_fp4(x.to(BF).cuda(), ids.cuda(), w.cuda(), q13, q2)
+    assert y4.shape == (M, d) and not y4.any()
+
+
 @pytest.mark.parametrize("fmt", [moe.MOE_FP4_NVFP4, moe.MOE_FP4_MXFP4])
 def test_fp4_layer_on_the_same_codes(fmt):
     """x and the weights as their codes stand; h is quantized by the layer, compared through the same quantizer."""

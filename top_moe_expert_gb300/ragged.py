@@ -73,7 +73,8 @@ def _swiglu(h: torch.Tensor) -> torch.Tensor:
 
 
 def _combine(rows: torch.Tensor, groups: Groups, topk_w: torch.Tensor) -> torch.Tensor:
-    rows = torch.cat([rows, rows.new_zeros((1, rows.shape[1]))])     # an invalid route reads the zero row
+    topk_w = topk_w.masked_fill(groups.row == rows.shape[0], 0.0)    # an invalid route: weight 0 of the zero row
+    rows = torch.cat([rows, rows.new_zeros((1, rows.shape[1]))])
     return (rows[groups.row].float() * topk_w.unsqueeze(-1)).sum(dim=1)
 
 
