@@ -72,6 +72,22 @@ def test_layer_and_gradients(M, E, k, d, I, invalid):
         assert not y[3].any() and not leaves[0].grad[3].any()
 
 
+def test_gradient_from_an_odd_address():
+    """The product's gradient as a contiguous view that does not start on 16 bytes: the same gradients bit for bit."""
+    g = torch.Generator().manual_seed(8)
+    x, w = torch.randn((19, 64), generator=g).to(BF).cuda(), torch.randn((3, 40, 64), generator=g).to(BF).cuda()
+    off = torch.tensor([0, 5, 5, 19], dtype=torch.int32, device="cuda")
+    dy = torch.randn((19, 40), generator=g).to(BF).cuda()
+    grads = []
+    for odd in (0, 3):
+        a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+        y = ragged.grouped_linear(a, b, off)
+        whole = torch.cat([y.new_ones(odd), y.flatten()])
+        whole.backward(torch.cat([dy.new_ones(odd), dy.flatten()]))
+        grads.append((a.grad, b.grad))
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
+
+
 @pytest.mark.parametrize("M", [0, 1, 3])
 def test_no_valid_route(M):
     """No tokens, or tokens all of whose routes are invalid: zeros forward and backward, whatever x and the weights hold."""

@@ -56,6 +56,8 @@ class _GroupedLinear(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
+        if dy.data_ptr() % 16:                                       # a view into a larger gradient
+            dy = dy.clone()
         dx = moe.moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = moe.moe_grouped_mm_wgrad(dy, x, offsets, out_dtype=w.dtype) if ctx.needs_input_grad[1] else None
         return dx, dw, None
