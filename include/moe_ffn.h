@@ -493,7 +493,9 @@ moe_status_t moe_ffn_decode_noalloc(const void *x, int32_t xdt, int32_t M, int32
  *   workspace.  (accumulate to MOE_FP32 adds in the L2, where a subnormal sum
  *   may be flushed to zero.)
  * R = 0 is a no-op for y and dx, and writes (or keeps) dw.
- * Limits: N % 8 == 0, K % 8 == 0, E <= 1024 (MOE_ERR_UNSUPPORTED); tensors
+ * Limits: N % 8 == 0, K % 8 == 0, E <= 1024, R, N and K <= 2^31 - 1024, and
+ * at most 2^31 - 1024 tiles: for y and dx of C columns E ceil(C / 256) (R / 128
+ * + 1), for dw E ceil(N / 256) ceil(K / 256) (MOE_ERR_UNSUPPORTED); tensors
  * 16-byte aligned (MOE_ERR_INVALID_ARG). */
 moe_status_t moe_grouped_mm(const void *x, const void *w, int32_t dt, const int32_t *offsets, int32_t R, int32_t E,
                             int32_t N, int32_t K, void *y, int32_t ydt, int32_t *dev_status, void *stream);
@@ -524,15 +526,16 @@ moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t dt, con
  *   v [rows][K] of vdt (MOE_FP32, MOE_BF16 or MOE_FP16; the values of
  *   moe_fp4_dequantize are rounded to it once).
  * Limits: K % 32 == 0, rows % groups == 0; tensors 16-byte aligned
- * (MOE_ERR_INVALID_ARG).
+ * (MOE_ERR_INVALID_ARG); K <= 2^31 - 1024, rows * K / 32 < 2^32
+ * (MOE_ERR_UNSUPPORTED).
  *
  * moe_grouped_mm_fp4: y[r][n] = x_alpha[0] * w_alpha[e] * sum over K of the
  * scaled codes of row r of x and row n of w[e], on the 4-bit tensor cores;
  * both operands of the same fmt.  x: xq [R][K/2], xs [R][Ks], x_alpha [1]; w:
  * wq [E][N][K/2], ws [E][N][Ks], w_alpha [E] (NULL for MXFP4); offsets, rows
  * and padding as moe_grouped_mm (E = 1: the dense product); y [R][N] MOE_BF16,
- * MOE_FP16 or MOE_FP32.  Limits: N % 8 == 0, K % 32 == 0, E <= 1024
- * (MOE_ERR_UNSUPPORTED); tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */
+ * MOE_FP16 or MOE_FP32.  Limits: N % 8 == 0, K % 32 == 0, E <= 1024, sizes as
+ * for moe_grouped_mm's y (MOE_ERR_UNSUPPORTED); tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */
 moe_status_t moe_fp4_scale_cols(int32_t K, int32_t fmt, int32_t *cols);
 moe_status_t moe_fp4_quantize(const void *v, int32_t vdt, int64_t rows, int32_t K, int32_t fmt, const float *alpha,
                               int64_t groups, uint8_t *q, uint8_t *s, void *stream);

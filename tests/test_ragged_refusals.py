@@ -32,6 +32,20 @@ def test_products_refuse_before_launch(L, fn, more):
         assert call(**bad) == 2, bad
 
 
+def test_sizes_past_32_bits(L):
+    """Sides whose tiles, or tile count with any offsets, would not count in 32 bits; the binding's that a C int cuts."""
+    top = 2 ** 31 - 8
+    for fn, more in (("moe_grouped_mm", ()), ("moe_grouped_mm_dgrad", ()), ("moe_grouped_mm_wgrad", (0,))):
+        for sides in ((top, 8, 8), (8, top, 8), (8, 8, top)):
+            assert _mm(L, fn, A, A, 0, A, sides[0], 2, *sides[1:], A, 0, *more) == 2, (fn, sides)
+        assert _mm(L, fn, A, A, 0, A, 2 ** 30, 1024, 2 ** 20, 2 ** 20, A, 0, *more) == 2
+    for sides in ((top, 8, 32), (8, top, 32), (8, 8, 2 ** 31 - 32), (2 ** 30, 2 ** 20, 32)):
+        assert L.moe_grouped_mm_fp4(A, A, None, A, A, None, 1, A, sides[0], 1024, *sides[1:], A, 0, None, None) == 2, sides
+    for rows, K in ((2 ** 62, 64), (2 ** 32, 32), (1, 2 ** 31 - 32)):
+        assert L.moe_fp4_quantize(A, 0, rows, K, 1, None, 1, A, A, None) == 2, (rows, K)
+        assert L.moe_fp4_dequantize(A, A, rows, K, 1, None, 1, A, 0, None) == 2, (rows, K)
+
+
 def test_wgrad_flag(L):
     assert _mm(L, "moe_grouped_mm_wgrad", A, A, 0, A, 4, 2, 64, 32, A, 0, 2) == 1
 
@@ -145,6 +159,23 @@ def test_binding_checks(rec):
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was not refused")
+    assert len(rec.calls) == n
+
+
+def test_binding_refuses_sizes_that_would_be_cut(rec):
+    """Meta tensors of 2^32 + 8 rows or columns, which a C int takes for 8."""
+    big = 2 ** 32 + 8
+    m = lambda *s, t=BF: torch.empty(s, dtype=t, device="meta")  # noqa: E731
+    off = m(2, t=torch.int32)
+    n = len(rec.calls)
+    for f in (lambda: moe.moe_grouped_mm(m(big, 8), m(1, 8, 8), off),
+              lambda: moe.moe_grouped_mm(m(8, big), m(1, 8, big), off),
+              lambda: moe.moe_grouped_mm_dgrad(m(8, 8), m(1, 8, big), off),
+              lambda: moe.moe_grouped_mm_wgrad(m(big, 8), m(big, 8), off),
+              lambda: moe.moe_fp4_quantize(m(1, 2 ** 32 + 32), 1),
+              lambda: moe.moe_fp4_dequantize(m(1, 2 ** 31 + 16, t=torch.uint8), m(1, 16, t=torch.uint8), 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            f()
     assert len(rec.calls) == n
 
 

@@ -706,6 +706,10 @@ def _experts(offsets) -> int:
     return n - 1
 
 
+def _too_long(*sizes) -> None:
+    raise ValueError(f"sizes {sizes} do not fit in 32 bits")          # the C call would get them cut
+
+
 def _result(t, name: str, shape, dtype, dtypes, dev, stream):
     """The output: a new one of `dtype`, or the caller's after its check.  One
     that is first written on a given stream comes from that stream's memory,
@@ -732,6 +736,8 @@ def moe_grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out_
     (R, K), (e, N, k), E = x.shape, w.shape, _experts(offsets)
     if e != E or k != K:
         raise ValueError(f"w must be [E={E}, N, K={K}], not {tuple(w.shape)}")
+    if (R | E | N | K) >> 31:
+        _too_long(R, E, N, K)
     gpu, dev, dt = x.get_device(), x.device, x.dtype
     y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev, stream)
     _launch(gpu, "moe_grouped_mm", x.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K, y.data_ptr(),
@@ -748,6 +754,8 @@ def moe_grouped_mm_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     (R, N), (e, n, K), E = dy.shape, w.shape, _experts(offsets)
     if e != E or n != N:
         raise ValueError(f"w must be [E={E}, N={N}, K], not {tuple(w.shape)}")
+    if (R | E | N | K) >> 31:
+        _too_long(R, E, N, K)
     gpu, dev, dt = dy.get_device(), dy.device, dy.dtype
     dx = _result(dx, "dx", (R, K), out_dtype or dt, (dt, torch.float32), dev, stream)
     _launch(gpu, "moe_grouped_mm_dgrad", dy.data_ptr(), w.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
@@ -765,6 +773,8 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     (R, N), (r, K), E = dy.shape, x.shape, _experts(offsets)
     if r != R:
         raise ValueError(f"x must be [R={R}, K], not {tuple(x.shape)}")
+    if (R | E | N | K) >> 31:
+        _too_long(R, E, N, K)
     gpu, dev, dt = dy.get_device(), dy.device, dy.dtype
     if accumulate and dw is None:
         raise ValueError("accumulate needs the dw to add to")
@@ -792,6 +802,8 @@ def _fp4_shape(K: int, fmt: int, what: str) -> int:
         raise ValueError(f"{what}: unknown format {fmt}")
     if K < 1 or K % 32:
         raise ValueError(f"{what}: K = {K} is not a positive multiple of 32")
+    if K >> 31:
+        _too_long(K)
     return (K // b + 15) // 16 * 16
 
 
@@ -855,7 +867,7 @@ def _fp4_rows(t, name: str, dtypes, per: int, fmt: int, alpha):
     try:
         gpu, shape, block = t.get_device(), t.shape, _FP4_BLOCK[fmt]
         K = shape[-1] * per
-        if (gpu >= 0 and t.dtype in dtypes and t.is_contiguous() and K > 0 and K % 32 == 0
+        if (gpu >= 0 and t.dtype in dtypes and t.is_contiguous() and 0 < K < 1 << 31 and K % 32 == 0
                 and (block == 32 if alpha is None else
                      block == 16 and alpha.dtype is torch.float32 and alpha.get_device() == gpu and alpha.is_contiguous()
                      and alpha.dim() == 1)):
@@ -914,6 +926,8 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
     K = half * 2
     if e != E or xh != half:
         raise ValueError(f"w is [{e}, {N}, {K}]; offsets are for {E} experts and x has K = {xh * 2}")
+    if (R | E | N | K) >> 31:
+        _too_long(R, E, N, K)
     y = _result(y, "y", (R, N), out_dtype, _DT, dev, stream)
     _launch(gpu, "moe_grouped_mm_fp4", x.q.data_ptr(), x.s.data_ptr(), _ptr(x.alpha), w.q.data_ptr(), w.s.data_ptr(),
             _ptr(w.alpha), x.fmt, offsets.data_ptr(), R, E, N, K, y.data_ptr(), _DT[y.dtype], _status(dev_status, dev),

@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "gmm_common.cuh"
+#include "ragged.cuh"
 
 namespace moe {
 namespace fp4 {
@@ -307,7 +308,7 @@ static moe_status_t check(const void *v, int32_t vdt, int64_t rows, int32_t K, i
         return MOE_ERR_UNSUPPORTED;
     if ((fmt == MOE_FP4_NVFP4) != (alpha != nullptr) && rows)
         return MOE_ERR_INVALID_ARG;
-    if (rows * (K / 32) > UINT32_MAX)
+    if (K > ragged::kMaxSide || rows > UINT32_MAX / (K / 32))
         return MOE_ERR_UNSUPPORTED;
     if (rows && (!v || !q || !s || !aligned(v, 16) || !aligned(q, 16) || !aligned(s, 16)))
         return MOE_ERR_INVALID_ARG;

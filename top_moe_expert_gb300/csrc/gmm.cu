@@ -592,7 +592,8 @@ static moe_status_t check(const void *a, const void *b, const void *out, int32_t
 {
     if (R < 0 || E < 1 || N < 1 || K < 1)
         return MOE_ERR_INVALID_ARG;
-    if (!type16(dt) || !out_type(odt, dt) || E > ragged::kMaxExperts || N % 8 || K % 8)
+    if (!type16(dt) || !out_type(odt, dt) || E > ragged::kMaxExperts || N % 8 || K % 8 || R > ragged::kMaxSide ||
+        N > ragged::kMaxSide || K > ragged::kMaxSide)
         return MOE_ERR_UNSUPPORTED;
     if (!offsets || !out || !aligned(out, 16) || !aligned(offsets, 4))
         return MOE_ERR_INVALID_ARG;
@@ -654,13 +655,15 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
     const bool few = R <= 64 * static_cast<int64_t>(E), sum = ydt == MOE_FP32 || J > kLong;
     const int kind = sum ? (few ? kSumFew : kSum) : few ? kNarrow : kPlain;
     const int tn = tile_n(OP, kind);
+    const int64_t n_mt = (C + kTileM - 1) / kTileM;
+    if (!ragged::list_fits(E, R, n_mt, tn))
+        return MOE_ERR_UNSUPPORTED;
     CUtensorMap tm[4];
     const bool ok = OP == kFwd ? tmap_tile(&tm[0], 3, t, 2, w, J, C, E, 64, 128) : tmap_tile(&tm[0], 3, t, 2, w, C, J, E, 64, 64);
     if (!ok || !tmap_tile(&tm[1], 2, t, 2, x, J, R, 1, 64, tn / 2) || !tmap_tile(&tm[2], 2, t, 2, x, J, R, 1, 64, 16) ||
         !tmap_rows_out(&tm[3], map_type(ydt), ydt == MOE_FP32 ? 4 : 2, y, C, R))
         return MOE_ERR_CUDA;
     const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
-    const int64_t n_mt = (C + kTileM - 1) / kTileM;
     const int64_t tiles = n_mt * (static_cast<int64_t>(R) / tn + (E < R ? E : R));
     return launch_kind<OP>(tm, a, ydt, kind, tiles, s);
 }
@@ -701,6 +704,9 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
     const moe_status_t st = check(dy, x, dw, dt, wdt, R, E, N, K, offsets);
     if (st != MOE_OK)
         return st;
+    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + 255) / 256);
+    if (tiles > ragged::kMaxTiles)
+        return MOE_ERR_UNSUPPORTED;
     const CUtensorMapDataType t = map_type(dt);
     const int size = wdt == MOE_FP32 ? 4 : 2;
     CUtensorMap tm[4];
@@ -711,9 +717,6 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
         return MOE_ERR_CUDA;
     tm[2] = tm[1];
     const Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
-    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileM - 1) / kTileM) * ((K + 255) / 256);
-    if (tiles > INT32_MAX)
-        return MOE_ERR_UNSUPPORTED;
     const bool few = R <= 64 * static_cast<int64_t>(E), sum = wdt == MOE_FP32 || R > kLong;
     return launch_kind<kWgrad>(tm, a, wdt, sum ? (few ? kSumFew : kSum) : kPlain, tiles, as_stream(stream));
 }

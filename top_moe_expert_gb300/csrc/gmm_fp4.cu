@@ -458,7 +458,7 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
     if (R < 0 || E < 1 || N < 1 || K < 1)
         return MOE_ERR_INVALID_ARG;
     if ((fmt != MOE_FP4_NVFP4 && fmt != MOE_FP4_MXFP4) || (ydt != MOE_BF16 && ydt != MOE_FP16 && ydt != MOE_FP32) ||
-        E > ragged::kMaxExperts || N % 8 || K % 32)
+        E > ragged::kMaxExperts || N % 8 || K % 32 || R > ragged::kMaxSide || N > ragged::kMaxSide || K > ragged::kMaxSide)
         return MOE_ERR_UNSUPPORTED;
     if (R == 0)
         return MOE_OK;
@@ -473,6 +473,8 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
                                    : ydt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const bool few = R <= 64 * static_cast<int64_t>(E);
     const int tn = few ? Shape<true>::kTileN : Shape<false>::kTileN;
+    if (!ragged::list_fits(E, R, (N + kTileM - 1) / kTileM, tn))
+        return MOE_ERR_UNSUPPORTED;
     CUtensorMap tm[6];
     if (!tmap_tile(&tm[0], 3, u8, 1, wq, K / 2, N, E, 128, 128) || !tmap_tile(&tm[1], 2, u8, 1, xq, K / 2, R, 1, 128, tn / 2) ||
         !tmap_tile(&tm[2], 2, u8, 1, xq, K / 2, R, 1, 128, 16) || !tmap_tile(&tm[3], 3, u8, 1, ws, Ks, N, E, kSlotRow, 128, sw) ||

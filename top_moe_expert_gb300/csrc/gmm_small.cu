@@ -128,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) small_kernel(const Args a)
     asm volatile("griddepcontrol.launch_dependents;");
     make_groups(c, a.off, a.E, a.R);
     const int lane = threadIdx.x & 31;
-    const int half = a.N / 2;                            // N is even: pairs of rows
+    const uint32_t half = a.N / 2;                       // N is even: pairs of rows
     const int64_t total = static_cast<int64_t>(c.count) * half, warps = static_cast<int64_t>(gridDim.x) * kWarps;
     const int64_t me = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-    const int end = static_cast<int>(total * (me + 1) / warps);
-    for (int i = static_cast<int>(total * me / warps); i < end; ++i) {
+    const uint32_t end = static_cast<uint32_t>(total * (me + 1) / warps);
+    for (uint32_t i = static_cast<uint32_t>(total * me / warps); i < end; ++i) {
         const int m = i / half, n = 2 * (i - m * half);
         switch (c.n[m]) {
         case 1: pair_of<T, OT, 1>(a, c.e[m], c.r0[m], n, lane); break;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) small_kernel(const Args a)
     // rows outside every group
     for (int r = 0; r < a.R; ++r)
         if (c.expert[r] < 0)
-            for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.N; i += gridDim.x * kThreads)
+            for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < a.N; i += gridDim.x * kThreads)
                 static_cast<OT *>(a.y)[static_cast<int64_t>(r) * a.N + i] = fp4::from_float<OT>(0.f);
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e < a.E; e += kThreads)

@@ -8,6 +8,12 @@ namespace moe {
 namespace ragged {
 
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxSide = INT32_MAX - 1023;         // of a matrix, so that rounding a side up to a tile stays in 32 bits
+constexpr int kMaxTiles = kMaxSide;                // so that a step past the last does too
+
+// Whether the list of tiles (mt x ceil(rows / nt) for each expert) counts in 32
+// bits whatever the offsets hold: a group has at most R rows.
+inline bool list_fits(int E, int R, int64_t mt, int nt) { return mt * E <= kMaxTiles / (R / nt + 1); }
 
 // Whether offsets are what the contract says; a call reports it once.
 __device__ __forceinline__ void report_bad(const int32_t *off, int R, int e, int32_t *dev_status)
