@@ -1,5 +1,7 @@
 """The ragged expert layer (top_moe_expert_gb300.ragged): routing to groups, its outputs and gradients against a 64-bit
 layer, the 4-bit layer against a 64-bit layer on the same codes, and a captured training step."""
+import gc
+
 import pytest
 import torch
 
@@ -133,6 +135,28 @@ def test_fp4_layer_on_the_same_codes(fmt):
     rel = float((y - want).norm() / want.norm())
     assert rel <= (1 / 3) * 50 ** -0.5, rel
     assert not y[3].any()
+
+
+def test_capture_beside_an_eager_graph():
+    """Refused with an exception while the eager graph lives; captured, with the eager gradients, once it is dropped."""
+    g = torch.Generator().manual_seed(12)
+    x, w = torch.randn((19, 64), generator=g).to(BF).cuda(), torch.randn((3, 40, 64), generator=g).to(BF).cuda().requires_grad_()
+    off = torch.tensor([0, 5, 5, 19], dtype=torch.int32, device="cuda")
+    eager = ragged.grouped_linear(x, w, off).sum()
+    want, = torch.autograd.grad(eager, w, retain_graph=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="another stream lives"):
+        with torch.cuda.graph(graph):
+            y = ragged.grouped_linear(x, w, off).sum()
+            torch.autograd.grad(y, w)
+    del eager, y
+    gc.collect()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grad, = torch.autograd.grad(ragged.grouped_linear(x, w, off).sum(), w)
+    graph.replay()
+    assert torch.equal(grad, want)
 
 
 def test_captured_training_step_matches_eager():

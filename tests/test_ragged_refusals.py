@@ -179,6 +179,35 @@ def test_binding_refuses_sizes_that_would_be_cut(rec):
     assert len(rec.calls) == n
 
 
+def test_captured_backward_beside_an_eager_graph_is_refused(rec, monkeypatch):
+    """The leaves' accumulation belongs to the stream of a graph that lives: refused in a capture on another stream."""
+    from types import SimpleNamespace
+
+    from top_moe_expert_gb300 import ragged
+
+    state = SimpleNamespace(stream=1, capturing=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: SimpleNamespace(cuda_stream=state.stream))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state.capturing)
+    x = torch.zeros((5, 32), dtype=BF).requires_grad_()
+    w = torch.zeros((2, 64, 32), dtype=BF).requires_grad_()
+    off = torch.zeros(3, dtype=torch.int32)
+    eager = ragged.grouped_linear(x.detach(), w, off)
+    state.stream, state.capturing = 2, True
+    y = ragged.grouped_linear(x, w, off)
+    with pytest.raises(RuntimeError, match="another stream lives"):
+        y.sum().backward()
+    ragged.grouped_linear(x, w.detach(), off).sum().backward()          # x is not part of the eager graph
+    with torch.no_grad():
+        ragged.grouped_linear(x, w, off)
+    del eager, y
+    ragged.grouped_linear(x, w, off).sum().backward()                   # and w no longer is
+    state.stream, state.capturing = 1, False
+    kept = ragged.grouped_linear(x, w, off)
+    kept.sum().backward()
+    state.stream = 3
+    ragged.grouped_linear(x, w, off).sum().backward()                   # without a capture any stream will do
+
+
 def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="must be a CUDA tensor"):
         moe.moe_grouped_mm(torch.zeros((5, 32), dtype=BF), torch.zeros((2, 64, 32), dtype=BF), torch.zeros(3, dtype=torch.int32))

@@ -45,28 +45,56 @@ def group_routes(topk_ids: torch.Tensor, E: int) -> Groups:
     return Groups(torch.where(routes < R, routes // k, 0).long(), row[:R].view(M, k), offsets)
 
 
+# A leaf's gradient is accumulated on the stream of its first use, for as long as
+# any graph through it lives.  Where that is not the stream of a capture, the
+# accumulation would end the capture, and the process with it; the stream is kept
+# with the accumulating node so that the backward pass can refuse before that.
+_STREAM = "top_moe_expert_gb300.stream"
+
+
+def _accumulators(*inputs) -> list:
+    """The accumulating nodes of the inputs that are leaves, marked."""
+    if not torch.is_grad_enabled():
+        return []
+    nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in inputs
+             if t.is_leaf and t.requires_grad and moe._is_gpu(t)]
+    if nodes:
+        here = torch.cuda.current_stream(inputs[0].device).cuda_stream
+        for node in nodes:
+            node.metadata.setdefault(_STREAM, here)
+    return nodes
+
+
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets):
+    def forward(ctx, x, w, offsets, streams):
         ctx.save_for_backward(x, w, offsets)
+        ctx.streams = streams
         return moe.moe_grouped_mm(x, w, offsets)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
+        if ctx.streams and torch.cuda.is_current_stream_capturing():
+            here = torch.cuda.current_stream(x.device).cuda_stream
+            if any(s != here for s in ctx.streams):
+                raise RuntimeError("a backward pass cannot be captured while a graph of the same leaves from another "
+                                   "stream lives: drop its outputs, or warm up on the stream of the capture")
         dy = dy.contiguous()
         if dy.data_ptr() % 16:                                       # a view into a larger gradient
             dy = dy.clone()
         dx = moe.moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = moe.moe_grouped_mm_wgrad(dy, x, offsets, out_dtype=w.dtype) if ctx.needs_input_grad[1] else None
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
     """moe_grouped_mm with gradients: rows x [R, K] of each expert times its
-    w [E, N, K], transposed; first derivatives of x and w."""
-    return _GroupedLinear.apply(x, w, offsets)
+    w [E, N, K], transposed; first derivatives of x and w.  (To capture the
+    backward pass, drop earlier graphs of the same leaves first.)"""
+    nodes = _accumulators(x, w)                                       # alive until the new graph holds them
+    return _GroupedLinear.apply(x, w, offsets, [node.metadata[_STREAM] for node in nodes])
 
 
 def _swiglu(h: torch.Tensor) -> torch.Tensor:
