@@ -1,0 +1,71 @@
+"""Arithmetic that the ragged and 4-bit products share between host and device, run on the CPU."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SRC = os.path.join(ROOT, "tests", "host_products.cu")
+CSRC = os.path.join(ROOT, "top_moe_expert_gb300", "csrc")
+INCLUDE = os.path.join(ROOT, "include")
+DEPS = [SRC, *(os.path.join(CSRC, n) for n in ("fp4.cuh", "common.cuh"))]
+OUT = os.path.join(ROOT, "top_moe_expert_gb300", "_build", "host_products.so")
+
+
+@pytest.fixture(scope="module")
+def emu():
+    nvcc = next((c for c in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc")
+                 if c and os.path.exists(c)), None)
+    if nvcc is None:
+        pytest.skip("nvcc not available")
+    t = max(os.path.getmtime(p) for p in DEPS)
+    if not os.path.exists(OUT) or os.path.getmtime(OUT) < t:
+        os.makedirs(os.path.dirname(OUT), exist_ok=True)
+        subprocess.run([nvcc, "-O2", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC", "-shared",
+                        "-gencode", "arch=compute_103a,code=sm_103a", "-I", CSRC, "-I", INCLUDE, SRC, "-o", OUT],
+                       check=True, capture_output=True)
+    return ctypes.CDLL(OUT)
+
+
+def _factors(emu, a, b):
+    f, g = np.empty_like(a), np.empty_like(a)
+    p = lambda t: t.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+    emu.fp4_factors(ctypes.c_int64(a.size), p(a), p(b), p(f), p(g))
+    return f, g
+
+
+def test_two_constants_over_their_whole_range(emu):
+    """v * f * g of sums v (2^-20 .. 2^54) and constants from 2^-100 to 2^100: the value to three roundings wherever FP32
+    holds it, the bits of v * (a * b) where nothing on the way leaves FP32's normal range, 0 for 0."""
+    r = np.random.default_rng(1)
+    n = 400_000
+    f32 = np.float32
+    a, b = (np.ldexp(1 + r.random(n), r.integers(-100, 100, n)).astype(f32) for _ in range(2))
+    v = (np.ldexp(1 + r.random(n), r.integers(-20, 54, n)) * r.choice([-1, 1], n)).astype(f32)
+    f, g = _factors(emu, a, b)
+    with np.errstate(over="ignore", under="ignore"):
+        got = v * f * g
+        plain = v * (a * b)
+        want = v.astype(np.float64) * a.astype(np.float64) * b.astype(np.float64)
+        ab = a.astype(np.float64) * b
+        fits = np.abs(want) < 3.4e38
+        tol = 3.01 * 2.0 ** -24 * np.abs(want) + 2.0 ** -150
+        assert (np.abs(got - want) <= tol)[fits].all()
+        assert np.isinf(got[np.abs(want) > 3.41e38]).all()
+        normal = fits & (np.abs(want) > 2.0 ** -125) & (ab > 2.0 ** -125) & (ab < 2.0 ** 127)
+        assert normal.sum() > n // 4 and np.array_equal(got[normal], plain[normal])
+        lost = fits & (np.abs(want) > 2.0 ** -125) & ~normal
+        assert lost.sum() > n // 50                          # a * b alone would have left FP32's normal range
+        assert not (f32(0) * f * g).any()
+
+
+def test_zero_and_special_constants(emu):
+    a = np.array([0, 0, 1, np.nan, np.inf, 2.0 ** -126, 2.0 ** 127], dtype=np.float32)
+    b = np.array([0, 2.0 ** 100, 0, 1, 2.0 ** -100, 1, 2.0 ** -100], dtype=np.float32)
+    f, g = _factors(emu, a, b)
+    y = np.float32(3) * f * g
+    assert not y[:3].any() and np.isnan(y[3]) and np.isposinf(y[4])
+    assert y[5] == np.float32(3 * 2.0 ** -126) and y[6] == np.float32(3 * 2.0 ** 27)

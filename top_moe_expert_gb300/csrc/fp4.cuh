@@ -80,6 +80,22 @@ __device__ __forceinline__ uint32_t block_scale_mx(uint32_t amax, float &inv)
     return static_cast<uint32_t>(X + 127);
 }
 
+// The product a * b of two constants as two factors to apply one after the
+// other, v * f * g: each may lie anywhere in 2^-100 .. 2^100, where a * b alone
+// can leave FP32 while v * a * b does not.  f carries the significands and half
+// of the exponent, g the other half, a power of two.  For v of a product of codes
+// (0, or 2^-20 .. 2^60) neither f, g nor v * f is subnormal, and v * f overflows
+// only where the result does, so that the roundings are those of a * b and of its
+// product with v, with one more where the result itself is subnormal.
+__host__ __device__ __forceinline__ void factors(float a, float b, float &f, float &g)
+{
+    const int ia = ilogbf(a), ib = ilogbf(b);           // of 0, infinity and NaN far outside the limits
+    const int ea = ia < -100 ? -100 : ia > 100 ? 100 : ia, eb = ib < -100 ? -100 : ib > 100 ? 100 : ib;
+    const int half = (ea + eb) / 2;
+    f = ldexpf(ldexpf(a, -ea) * ldexpf(b, -eb), half);
+    g = ldexpf(1.f, ea + eb - half);
+}
+
 template <int FMT>
 __device__ __forceinline__ float scale_value(uint32_t b)
 {

@@ -25,23 +25,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 
 // 32 accumulator columns (rows of y or dx) of this lane's output element:
 // neighbouring lanes exchange halves so that each stores two elements of one
-// row, 64 contiguous bytes per row and warp.  f: a factor of every element.
+// row, 64 contiguous bytes per row and warp.  f, g: factors of every element,
+// applied in that order.
 template <typename OT>
 __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int64_t ld, int m, int M, int n, int lane,
-                                           float f = 1.f)
+                                           float f = 1.f, float g = 1.f)
 {
     if constexpr (sizeof(OT) == 4) {
         if (m < M) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
                 if (c < n)
-                    out[c * ld + m] = __uint_as_float(v[c]) * f;
+                    out[c * ld + m] = __uint_as_float(v[c]) * f * g;
         }
     } else {
         const int odd = lane & 1;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-            const uint32_t own = pack2<OT>(__uint_as_float(v[c]) * f, __uint_as_float(v[c + 1]) * f);
+            const uint32_t own = pack2<OT>(__uint_as_float(v[c]) * f * g, __uint_as_float(v[c + 1]) * f * g);
             const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
             const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
             if (m < M && c + odd < n)
@@ -56,14 +57,14 @@ __device__ __forceinline__ void store_rows(const uint32_t (&v)[32], OT *out, int
 // the warp's first element, r0 the first row.
 template <typename OT>
 __device__ __forceinline__ void drain_rows(const uint32_t (&v)[32], uint8_t *tiles, int &flip, const CUtensorMap *map, int m0,
-                                           int r0, int M, int lane, float f = 1.f)
+                                           int r0, int M, int lane, float f = 1.f, float g = 1.f)
 {
     if constexpr (sizeof(OT) == 4) {
         tc::bulk_wait_read<0>();
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-            *reinterpret_cast<float *>(tiles + c * 128 + ((lane * 4) ^ ((c & 7) << 4))) = __uint_as_float(v[c]) * f;
+            *reinterpret_cast<float *>(tiles + c * 128 + ((lane * 4) ^ ((c & 7) << 4))) = __uint_as_float(v[c]) * f * g;
     } else {
         tiles += flip * 2048;
         flip ^= 1;
@@ -72,7 +73,7 @@ __device__ __forceinline__ void drain_rows(const uint32_t (&v)[32], uint8_t *til
         const int odd = lane & 1;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-            const uint32_t own = pack2<OT>(__uint_as_float(v[c]) * f, __uint_as_float(v[c + 1]) * f);
+            const uint32_t own = pack2<OT>(__uint_as_float(v[c]) * f * g, __uint_as_float(v[c + 1]) * f * g);
             const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
             const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
             *reinterpret_cast<uint32_t *>(tiles + (c + odd) * 64 + (((lane & ~1) * 2) ^ (((c >> 1) & 3) << 4))) = w;

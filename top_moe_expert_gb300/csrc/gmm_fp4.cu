@@ -365,7 +365,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int t = cid; t < total; t += n_cl, ++tix) {
             const Tile T = tile_of<kTileN>(a, s, t, n_mt);
             const int m = T.m0 + 128 * rank + 32 * q + lane, buf = tix & 1;
-            const float f = kMx ? 1.f : *a.xa * a.wa[T.e];
+            float f = 1.f, g = 1.f;
+            if (!kMx)
+                fp4::factors(*a.xa, a.wa[T.e], f, g);
             if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
                 if (a.dev_status)
                     atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
@@ -379,10 +381,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 tc::tmem_ld_32x32b_x32(acc + c0, v);
                 tc::tmem_ld_wait_for(v);
                 if (T.n - c0 < 32) {                     // a TMA store would reach into the next group's rows
-                    gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f);
+                    gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f, g);
                     break;
                 }
-                gmm::drain_rows<OT>(v, tiles, flip, &tmY, m - lane, T.r0 + c0, a.N, lane, f);
+                gmm::drain_rows<OT>(v, tiles, flip, &tmY, m - lane, T.r0 + c0, a.N, lane, f, g);
             }
             tc::tc_fence_before();
             __syncwarp();
