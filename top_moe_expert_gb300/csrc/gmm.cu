@@ -24,8 +24,11 @@
 // Roles: warp 0 loads (TMA, 128-byte swizzle, a ring of 5 to 8 stages of 64
 // along the contraction), warp 1 of the pair's leader issues the MMAs into two
 // accumulators of 256 TMEM columns, warps from 4 on drain one while the next
-// tile fills the other, warp 2 zeroes wgrad's row tails.  Every wait is bounded; an
-// expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
+// tile fills the other, warp 2 zeroes wgrad's row tails.  Every wait is bounded.  A
+// role whose wait expires sets its CTA's abort flag, which ends the CTA's other
+// roles at their next wait; an unfinished accumulator is not handed on, so the
+// other CTA's waits expire too.  Each CTA reports its flag at its end, as
+// MOE_ERR_TIMEOUT in dev_status[1].
 //
 // Bound by the tensor pipe at the clock that the power cap leaves for many rows
 // per expert (8192 x 8192 x 8192 bf16: forward 567, dgrad 567, wgrad 596 us, 1.94
@@ -39,6 +42,7 @@
 #include "gmm_common.cuh"
 #include "gmm_internal.h"
 #include "gmm_small.h"
+#include "gmm_stall.h"
 #include "ragged.cuh"
 #include "tc_pair.cuh"
 
@@ -104,12 +108,14 @@ struct Args {
     int J;                     // fwd, dgrad: the contraction
     int accumulate;
     int bf16;
+    MOE_STALL_ARG
 };
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer[kMaxStages], accf[2], acce[2], fin;
     uint32_t tmem;
     int abort;
+    MOE_STALL_BARRIER
     ragged::List list;
 };
 
@@ -250,6 +256,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             tc::mbar_init(bar(s.acce[i]), 2 * kDrain); // of both CTAs
         }
         tc::mbar_init(bar(s.fin), 1);
+        MOE_STALL_INIT(s);
         s.abort = 0;
         tc::fence_mbar_init();
         tc::prefetch_tmap(&tmA);
@@ -341,6 +348,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     const int q = st - i < 0 ? st - i + kStages : st - i;
                     tc::mbar_wait(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
                 }
+                if (never)
+                    *abort = 1;
             }
         }
     } else if (warp == 1) {
@@ -366,8 +375,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     tc::tc_fence_after();
                     ++tix;
                     const uint32_t acc = tmem + 256 * buf;
+                    MOE_STALL(a, s, t >= n_cl);
+                    bool ok = true;
                     for (int j = j0; j < j1; ++j) {
-                        if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
+                        ok = tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs);
+                        if (!ok)
                             break;
                         tc::tc_fence_after();
                         const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
@@ -382,6 +394,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             ph ^= 1u;
                         }
                     }
+                    if (!ok)                             // a part of the sums: not to be drained
+                        break;
                     tc::tc_commit_pair(bar(s.accf[buf]));
                 }
             }
@@ -473,11 +487,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (lane == 0)
                         tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
                 }
-                if (!ok) {
-                    if (a.dev_status)
-                        atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
+                if (!ok)
                     break;
-                }
                 auto bits = [&](int g, uint32_t (&v)[32]) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -505,11 +516,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             } else {
                 const int buf = tix & 1;
                 if (T.steps) {
-                    if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
-                        if (a.dev_status)
-                            atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
+                    if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs))
                         break;
-                    }
                     tc::tc_fence_after();
                     ++tix;
                 }
@@ -573,6 +581,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // the leader's last MMA is done and has told both CTAs so
         volatile int never = 0;
         tc::mbar_wait(bar(s.fin), 0, &never, kWaitNs);
+        if ((never || *abort) && a.dev_status)
+            atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
     }
     tc::cluster_sync();                                  // neither CTA ends while the other still reaches into it
     if (warp == 1) {
@@ -663,7 +673,7 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
     if (!ok || !tmap_tile(&tm[1], 2, t, 2, x, J, R, 1, 64, tn / 2) || !tmap_tile(&tm[2], 2, t, 2, x, J, R, 1, 64, 16) ||
         !tmap_rows_out(&tm[3], map_type(ydt), ydt == MOE_FP32 ? 4 : 2, y, C, R))
         return MOE_ERR_CUDA;
-    const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16};
+    const Args a{off, y, dev_status, R, E, C, 0, J, 0, dt == MOE_BF16 MOE_STALL_VALUE};
     const int64_t tiles = n_mt * (static_cast<int64_t>(R) / tn + (E < R ? E : R));
     return launch_kind<OP>(tm, a, ydt, kind, tiles, s);
 }
@@ -673,6 +683,18 @@ static moe_status_t rows(const void *x, const void *w, int32_t dt, int32_t R, in
 
 using namespace moe;
 using namespace moe::gmm;
+
+#ifdef MOE_DEBUG_BOUNDS
+std::atomic<int> moe::g_products_stall{0};
+
+MOE_API moe_status_t moe_debug_products_stall(int32_t on)
+{
+    if (on != 0 && on != 1)
+        return MOE_ERR_INVALID_ARG;
+    g_products_stall.store(on, std::memory_order_relaxed);
+    return MOE_OK;
+}
+#endif
 
 MOE_API moe_status_t moe_grouped_mm(const void *x, const void *w, int32_t dt, const int32_t *offsets, int32_t R, int32_t E,
                                     int32_t N, int32_t K, void *y, int32_t ydt, int32_t *dev_status, void *stream)
@@ -716,7 +738,7 @@ MOE_API moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t
         !tmap_tile(&tm[3], 3, map_type(wdt), size, dw, K, N, E, 128 / size, 32))
         return MOE_ERR_CUDA;
     tm[2] = tm[1];
-    const Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16};
+    const Args a{offsets, dw, dev_status, R, E, N, K, 0, accumulate, dt == MOE_BF16 MOE_STALL_VALUE};
     const bool few = R <= 64 * static_cast<int64_t>(E), sum = wdt == MOE_FP32 || R > kLong;
     return launch_kind<kWgrad>(tm, a, wdt, sum ? (few ? kSumFew : kSum) : kPlain, tiles, as_stream(stream));
 }

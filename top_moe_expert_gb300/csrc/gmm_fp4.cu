@@ -29,7 +29,7 @@
 // Roles: warp 0 loads codes, warp 2 loads scales, warps 8..10 arrange them (w,
 // the first 128 rows of x, the rest) and warp 3 tells the leader, whose warp 1
 // issues copies and MMAs; warps 4..7 drain the accumulators.  Every wait is
-// bounded; an expired one is reported as MOE_ERR_TIMEOUT in dev_status[1].
+// bounded, and an expired one is reported, as in gmm.cu.
 //
 // Bound by feeding the tiles: 164 us at 8192 x 8192 x 8192 (NVFP4; MXFP4 149),
 // 128 us with every copy left out; by HBM for few rows per expert (42 us for 4096
@@ -41,6 +41,7 @@
 #include "fp4.cuh"
 #include "gmm_common.cuh"
 #include "gmm_internal.h"
+#include "gmm_stall.h"
 #include "ragged.cuh"
 #include "tc_pair.cuh"
 
@@ -75,6 +76,7 @@ struct Args {
     void *out;
     int32_t *dev_status;
     int R, E, N, K;
+    MOE_STALL_ARG
 };
 
 struct Shared {
@@ -83,6 +85,7 @@ struct Shared {
     uint64_t accf[2], acce[2], fin;
     uint32_t tmem;
     int abort;
+    MOE_STALL_BARRIER
     ragged::List list;
 };
 
@@ -152,6 +155,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             tc::mbar_init(bar(s.acce[i]), 8);
         }
         tc::mbar_init(bar(s.fin), 1);
+        MOE_STALL_INIT(s);
         s.abort = 0;
         tc::fence_mbar_init();
         tc::prefetch_tmap(&tmA);
@@ -212,6 +216,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     const int q = st - i < 0 ? st - i + kStages : st - i;
                     tc::mbar_wait(bar(s.full[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
                 }
+                if (never)
+                    *abort = 1;
             }
         }
     } else if (warp == 2) {
@@ -240,6 +246,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const int q = st - i < 0 ? st - i + kSlots : st - i;
                 tc::mbar_wait(bar(s.sfull[q]), st - i < 0 ? ph ^ 1u : ph, &never, kWaitNs);
             }
+            if (never)
+                *abort = 1;
         }
     } else if (warp == 1) {
         if (rank == 0 && tc::elect_one()) {
@@ -258,11 +266,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 tc::tc_fence_after();
                 const uint32_t acc = tmem + kTileN * buf;
                 const uint32_t id0 = tc::idesc_fp4(256, n, kMx, 0), id1 = kMx ? tc::idesc_fp4(256, n, kMx, 2) : id0;
+                MOE_STALL(a, s, t >= n_cl);
+                bool ok = true;
                 for (int j = 0; j < steps; ++j, ++g) {
                     const int js = j % kSlotSteps;
-                    if (js == 0 && !tc::mbar_wait_cluster(bar(s.sready[sst]), sph, abort, kWaitNs))
-                        break;
-                    if (!tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs))
+                    ok = (js != 0 || tc::mbar_wait_cluster(bar(s.sready[sst]), sph, abort, kWaitNs)) &&
+                         tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs);
+                    if (!ok)
                         break;
                     tc::tc_fence_after();
                     const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
@@ -294,6 +304,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     }
                 }
+                if (!ok)                                 // a part of the sums: not to be drained
+                    break;
                 tc::tc_commit_pair(bar(s.accf[buf]));
             }
             tc::tc_commit_pair(bar(s.fin));
@@ -368,11 +380,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             float f = 1.f, g = 1.f;
             if (!kMx)
                 fp4::factors(*a.xa, a.wa[T.e], f, g);
-            if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs)) {
-                if (a.dev_status)
-                    atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
+            if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs))
                 break;
-            }
             tc::tc_fence_after();
             const uint32_t acc = tmem + kTileN * buf + (static_cast<uint32_t>(32 * q) << 16);
             uint8_t *tiles = sf + kSlots * kSlotBytes + q * 4096;
@@ -412,6 +421,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // the leader's last MMA is done and has told both CTAs so
         volatile int never = 0;
         tc::mbar_wait(bar(s.fin), 0, &never, kWaitNs);
+        if ((never || *abort) && a.dev_status)
+            atomicCAS(a.dev_status + 1, 0, static_cast<int>(MOE_ERR_TIMEOUT));
     }
     tc::cluster_sync();                                  // neither CTA ends while the other still reaches into it
     if (warp == 1) {
@@ -483,7 +494,7 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
         !tmap_tile(&tm[4], 2, u8, 1, xs, Ks, R, 1, kSlotRow, 32, sw) ||
         !tmap_rows_out(&tm[5], ty, ydt == MOE_FP32 ? 4 : 2, y, N, R))
         return MOE_ERR_CUDA;
-    const Args a{offsets, x_alpha, w_alpha, y, dev_status, R, E, N, K};
+    const Args a{offsets, x_alpha, w_alpha, y, dev_status, R, E, N, K MOE_STALL_VALUE};
     if (fmt == MOE_FP4_NVFP4)
         return few ? launch_as<MOE_FP4_NVFP4, true>(tm, a, ydt, as_stream(stream))
                    : launch_as<MOE_FP4_NVFP4, false>(tm, a, ydt, as_stream(stream));
