@@ -48,53 +48,77 @@ def group_routes(topk_ids: torch.Tensor, E: int) -> Groups:
 # A leaf's gradient is accumulated on the stream of its first use, for as long as
 # any graph through it lives.  Where that is not the stream of a capture, the
 # accumulation would end the capture, and the process with it; the stream is kept
-# with the accumulating node so that the backward pass can refuse before that.
+# with the accumulating node, and an input that leads to one of another stream
+# goes through a node that refuses before its gradient gets there.
 _STREAM = "top_moe_expert_gb300.stream"
+_NEAR = 8                               # nodes looked at per input: a cast, a gather, a softmax lie between
 
 
-def _accumulators(*inputs) -> list:
-    """The accumulating nodes of the inputs that are leaves, marked."""
+def _accumulators(t: torch.Tensor) -> list:
+    """The accumulating nodes among the first _NEAR behind t."""
+    nodes = [torch.autograd.graph.get_gradient_edge(t).node if t.is_leaf else t.grad_fn]
+    for node in nodes:                                                # grows on the way
+        if len(nodes) >= _NEAR:
+            break
+        for n, _ in node.next_functions:
+            if n is not None:
+                nodes.append(n)
+    return [n for n in nodes if hasattr(n, "variable")]
+
+
+class _Refuse(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, t):
+        return t.view_as(t)
+
+    @staticmethod
+    def backward(ctx, dt):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a backward pass cannot be captured while a graph of the same leaves from another "
+                               "stream lives: drop its outputs, or warm up on the stream of the capture")
+        return dt
+
+
+def _guarded(*inputs):
+    """The inputs, behind a refusing node where they need one, and the
+    accumulating nodes, which the caller keeps until the new graph holds them."""
     if not torch.is_grad_enabled():
-        return []
-    nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in inputs
-             if t.is_leaf and t.requires_grad and moe._is_gpu(t)]
-    if nodes:
+        return inputs, None
+    nodes = [_accumulators(t) if t.requires_grad and moe._is_gpu(t) else () for t in inputs]
+    if any(nodes):
         here = torch.cuda.current_stream(inputs[0].device).cuda_stream
-        for node in nodes:
-            node.metadata.setdefault(_STREAM, here)
-    return nodes
+        inputs = [_Refuse.apply(t) if any([n.metadata.setdefault(_STREAM, here) != here for n in ns]) else t
+                  for t, ns in zip(inputs, nodes)]
+    return inputs, nodes
 
 
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets, streams):
+    def forward(ctx, x, w, offsets):
         ctx.save_for_backward(x, w, offsets)
-        ctx.streams = streams
         return moe.moe_grouped_mm(x, w, offsets)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
-        if ctx.streams and torch.cuda.is_current_stream_capturing():
-            here = torch.cuda.current_stream(x.device).cuda_stream
-            if any(s != here for s in ctx.streams):
-                raise RuntimeError("a backward pass cannot be captured while a graph of the same leaves from another "
-                                   "stream lives: drop its outputs, or warm up on the stream of the capture")
         dy = dy.contiguous()
         if dy.data_ptr() % 16:                                       # a view into a larger gradient
             dy = dy.clone()
         dx = moe.moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
         dw = moe.moe_grouped_mm_wgrad(dy, x, offsets, out_dtype=w.dtype) if ctx.needs_input_grad[1] else None
-        return dx, dw, None, None
+        return dx, dw, None
 
 
 def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
     """moe_grouped_mm with gradients: rows x [R, K] of each expert times its
-    w [E, N, K], transposed; first derivatives of x and w.  (To capture the
-    backward pass, drop earlier graphs of the same leaves first.)"""
-    nodes = _accumulators(x, w)                                       # alive until the new graph holds them
-    return _GroupedLinear.apply(x, w, offsets, [node.metadata[_STREAM] for node in nodes])
+    w [E, N, K], transposed; first derivatives of x and w.  To capture the
+    backward pass, drop earlier graphs of the same leaves first: one that came
+    through here on another stream is refused, for x, w and what they are made
+    of within a few operations (a leaf that only other operations have used,
+    or one further off, is not known here)."""
+    (x, w), kept = _guarded(x, w)
+    return _GroupedLinear.apply(x, w, offsets)
 
 
 def _swiglu(h: torch.Tensor) -> torch.Tensor:
@@ -102,10 +126,13 @@ def _swiglu(h: torch.Tensor) -> torch.Tensor:
     return torch.nn.functional.silu(g) * u
 
 
-def _combine(rows: torch.Tensor, groups: Groups, topk_w: torch.Tensor) -> torch.Tensor:
-    topk_w = topk_w.masked_fill(groups.row == rows.shape[0], 0.0)    # an invalid route: weight 0 of the zero row
+def _weights(topk_w: torch.Tensor, groups: Groups) -> torch.Tensor:
+    return topk_w.masked_fill(groups.row == groups.token.shape[0], 0.0)    # an invalid route: weight 0 of the zero row
+
+
+def _combine(rows: torch.Tensor, groups: Groups, weights: torch.Tensor) -> torch.Tensor:
     rows = torch.cat([rows, rows.new_zeros((1, rows.shape[1]))])
-    return (rows[groups.row].float() * topk_w.unsqueeze(-1)).sum(dim=1)
+    return (rows[groups.row].float() * weights.unsqueeze(-1)).sum(dim=1)
 
 
 def expert_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
@@ -114,8 +141,9 @@ def expert_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
     x [M, d], topk_w [M, k], w13 [E, 2I, d] and w2 [E, d, I] (one of bf16 and
     fp16; h is rounded to it)."""
     groups = group_routes(topk_ids, w13.shape[0])
-    h = _swiglu(grouped_linear(x[groups.token], w13, groups.offsets)).to(x.dtype)
-    return _combine(grouped_linear(h, w2, groups.offsets), groups, topk_w)
+    (rows, weights, w13, w2), kept = _guarded(x[groups.token], _weights(topk_w, groups), w13, w2)
+    h = _swiglu(_GroupedLinear.apply(rows, w13, groups.offsets)).to(x.dtype)
+    return _combine(_GroupedLinear.apply(h, w2, groups.offsets), groups, weights)
 
 
 def tensor_alpha(v: torch.Tensor) -> torch.Tensor:
@@ -140,7 +168,8 @@ def expert_layer_fp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tens
     rows = moe.Fp4(fmt, q[groups.token], s[groups.token], alpha_x)
     h = _swiglu(moe.moe_grouped_mm_fp4(rows, w13, groups.offsets, out_dtype=torch.float32))
     hq = moe.Fp4(fmt, *moe.moe_fp4_quantize(h, fmt, alpha_h), alpha_h)
-    return _combine(moe.moe_grouped_mm_fp4(hq, w2, groups.offsets, out_dtype=torch.float32), groups, topk_w)
+    return _combine(moe.moe_grouped_mm_fp4(hq, w2, groups.offsets, out_dtype=torch.float32), groups,
+                    _weights(topk_w, groups))
 
 
 def main() -> None:
