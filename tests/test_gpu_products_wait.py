@@ -64,3 +64,17 @@ def test_an_expired_wait_is_reported(debug):
 
 def test_the_hook_checks_its_argument(debug):
     assert debug.moe_debug_products_stall(2) == 1 and debug.moe_debug_products_stall(-1) == 1
+
+
+def test_ragged_tails_far_apart():
+    """A weight gradient whose ragged experts come after hundreds of tiles without a tail (the release build)."""
+    moe.use_library(build.LIB)
+    g = torch.Generator().manual_seed(2)
+    sizes = ([64] * 200 + [37] + [0] * 50 + [16] * 100 + [1]) * 2
+    R, E, N, K = sum(sizes) + 5, len(sizes), 256, 264
+    x, dy = (torch.randint(-2, 3, (R, c), generator=g).to(BF) for c in (K, N))
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for out in (BF, F32):
+        dw = moe.moe_grouped_mm_wgrad(dy.cuda(), x.cuda(), ref.offsets_of(sizes).cuda(), out_dtype=out, dev_status=st)
+        assert torch.equal(dw.cpu(), ref.wgrad(dy, x, sizes)[0].to(out))
+    assert st.tolist() == [0, 0]

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = os.path.join(ROOT, "tests", "host_products.cu")
 CSRC = os.path.join(ROOT, "top_moe_expert_gb300", "csrc")
 INCLUDE = os.path.join(ROOT, "include")
-DEPS = [SRC, *(os.path.join(CSRC, n) for n in ("fp4.cuh", "common.cuh"))]
+DEPS = [SRC, *(os.path.join(CSRC, n) for n in ("fp4.cuh", "ragged.cuh", "common.cuh"))]
 OUT = os.path.join(ROOT, "top_moe_expert_gb300", "_build", "host_products.so")
 
 
@@ -69,3 +69,23 @@ def test_zero_and_special_constants(emu):
     y = np.float32(3) * f * g
     assert not y[:3].any() and np.isnan(y[3]) and np.isposinf(y[4])
     assert y[5] == np.float32(3 * 2.0 ** -126) and y[6] == np.float32(3 * 2.0 ** 27)
+
+
+def test_a_limit_runs_from_the_last_progress(emu):
+    """A wait much longer than the limit goes on while the other role moves, however slowly, and ends a limit after it
+    last did."""
+    emu.limit_expires.restype = ctypes.c_int64
+    limit, n = 5_000_000_000, 4000
+    now = np.arange(n, dtype=np.int64) * 100_000_000            # 80 limits
+    p = lambda t: t.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+
+    def expires(progress):
+        t = progress.astype(np.int32)
+        return emu.limit_expires(ctypes.c_int64(n), p(now), p(t), ctypes.c_int64(limit))
+
+    assert expires(np.zeros(n)) == 51
+    assert expires(np.arange(n)) == n and expires(np.arange(n) // 50) == n
+    assert expires(np.minimum(np.arange(n), 1000)) == 1051
+    assert expires(np.arange(n) // 60) == 51                    # a role that rests for longer than the limit
+    wrap = (np.arange(n) + 2 ** 31 - 100).astype(np.int64).astype(np.uint32).astype(np.int64)
+    assert expires(np.where(wrap >= 2 ** 31, wrap - 2 ** 32, wrap)) == n

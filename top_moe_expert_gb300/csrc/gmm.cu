@@ -114,7 +114,7 @@ struct Args {
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages], peer[kMaxStages], accf[2], acce[2], fin;
     uint32_t tmem;
-    int abort;
+    int abort, loaded;         // loaded: stages that the loader has begun (wgrad)
     MOE_STALL_BARRIER
     ragged::List list;
 };
@@ -224,6 +224,25 @@ __device__ __forceinline__ void round_dw(const uint32_t (&v)[32], uint32_t *w, c
     }
 }
 
+// tc::mbar_wait for the next ragged tail.  Experts whose rows are a multiple of 16
+// have none, so it may be as far away as the end of the call: the limit runs anew
+// with each stage that the loader begins.
+__device__ __forceinline__ bool wait_tail(uint32_t bar, uint32_t parity, volatile int *loaded, volatile int *abort)
+{
+    ragged::Limit limit{clock64(), *loaded};
+    for (uint32_t i = 1; !tc::mbar_try_wait(bar, parity); ++i) {
+        if ((i & 3) == 0) {
+            if (*abort)
+                return false;
+            if (limit.expired(clock64(), *loaded, static_cast<long long>(kWaitNs) * 5 / 2)) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
 template <int OP, typename OT, int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(KIND), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -258,6 +277,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         tc::mbar_init(bar(s.fin), 1);
         MOE_STALL_INIT(s);
         s.abort = 0;
+        s.loaded = 0;
         tc::fence_mbar_init();
         tc::prefetch_tmap(&tmA);
         tc::prefetch_tmap(&tmB);
@@ -300,6 +320,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         break;
                     const uint32_t sa = ring + st * kStageBytes, sb = sa + 16384;
                     uint32_t fb;
+                    if (OP == kWgrad)
+                        *const_cast<volatile int *>(&s.loaded) = issued + 1;
                     if (j == tail) {
                         // this CTA's tail warp hears of the data first
                         fb = bar(s.tail[st]);
@@ -416,7 +438,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     continue;
                 const uint32_t ph = (phases >> q) & 1u;
                 phases ^= 1u << q;
-                if (!tc::mbar_wait(bar(s.tail[q]), ph, abort, kWaitNs))
+                if (!wait_tail(bar(s.tail[q]), ph, &s.loaded, abort))
                     break;
                 const int r0 = T.rows - (T.steps - 1) * kStep, r1 = (r0 + 15) & ~15;
                 for (int i = lane; i < (r1 - r0) * 32; i += 32) {

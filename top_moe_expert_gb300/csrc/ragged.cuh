@@ -98,5 +98,20 @@ __host__ __device__ __forceinline__ void place(int at, int n_mt, int n_nt, int &
     mt = band * kBand + at - nt * width;
 }
 
+// The limit of a wait for what another role brings after an unknown amount of
+// work: it runs from the last time that role was seen to have moved on.
+struct Limit {
+    long long since;
+    int seen;
+    __host__ __device__ __forceinline__ bool expired(long long now, int progress, long long limit)
+    {
+        if (progress != seen) {
+            seen = progress;
+            since = now;
+        }
+        return now - since > limit;
+    }
+};
+
 }  // namespace ragged
 }  // namespace moe
