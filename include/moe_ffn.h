@@ -531,7 +531,10 @@ moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t dt, con
  *
  * moe_grouped_mm_fp4: y[r][n] = x_alpha[0] * w_alpha[e] * sum over K of the
  * scaled codes of row r of x and row n of w[e], on the 4-bit tensor cores;
- * both operands of the same fmt.  x: xq [R][K/2], xs [R][Ks], x_alpha [1]; w:
+ * both operands of the same fmt.  Sums are FP32 and lose at most 2^-23 of
+ * the terms' magnitudes per 64 elements of K, or, past K = 8192 (FP32 results)
+ * or 32768 (16-bit ones), per 64 of a part of 2048 and 2^-24 per part; the
+ * constants' product with them, then y, are rounded once each.  x: xq [R][K/2], xs [R][Ks], x_alpha [1]; w:
  * wq [E][N][K/2], ws [E][N][Ks], w_alpha [E] (NULL for MXFP4); offsets, rows
  * and padding as moe_grouped_mm (E = 1: the dense product); y [R][N] MOE_BF16,
  * MOE_FP16 or MOE_FP32.  Limits: N % 8 == 0, K % 32 == 0, E <= 1024, sizes as

@@ -42,3 +42,44 @@ def test_constants_at_the_ends_of_their_range(xe, we, sizes):
                                        out_dtype=out).cpu()
             assert torch.equal(y, want.to(out)), (scales, out, int((y != want.to(out)).sum()))
         assert not y[3].any()
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("K,out", [(8192, F32), (8224, F32), (10336, F32), (16384, F32), (32768, BF), (32800, BF),
+                                   (34816, torch.float16)])
+@pytest.mark.parametrize("sizes,N", [([1, 0, 40], 136), ([130, 33], 264)])
+def test_long_sums_exact(fmt, K, out, sizes, N):
+    """Around the lengths from which the sums are added in parts: sums that are exact in FP32."""
+    g = torch.Generator().manual_seed(K + N)
+    R, E = sum(sizes) + 1, len(sizes)
+    scales = [0x30, 0x38, 0x40] if fmt == NV else [126, 127, 128]
+    xq, xs = _rows((R,), K, fmt, g, scales)
+    wq, ws = _rows((E, N), K, fmt, g, scales)
+    xa, wa = (torch.tensor([0.5], device="cuda"), torch.ones(E, device="cuda")) if fmt == NV else (None, None)
+    want, _ = ref.mm(torch.from_numpy(ref.values(xq, xs, fmt)), torch.from_numpy(ref.values(wq, ws, fmt)), sizes)
+    want = want * (0.5 if fmt == NV else 1.0)
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    y = moe.moe_grouped_mm_fp4(moe.Fp4(fmt, xq.cuda(), xs.cuda(), xa), moe.Fp4(fmt, wq.cuda(), ws.cuda(), wa),
+                               ref.offsets_of(sizes).cuda(), out_dtype=out, dev_status=st).cpu()
+    assert st.tolist() == [0, 0]
+    assert torch.equal(y, want.to(out)), int((y != want.to(out)).sum())
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("K", [2048, 7168, 8192, 8224, 32768, 131072])
+def test_long_sums_of_one_sign_do_not_drift(fmt, K):
+    """Codes of one sign, scales over a wide range.  An MMA adds 64 products and may lose 2^-23 of the sum; past 8192
+    elements a part has 32 of them, and adding the parts loses at most 2^-24 of the sum each."""
+    g = torch.Generator().manual_seed(K)
+    N, R = 64, 40
+    scales = list(range(0x01, 0x7F)) if fmt == NV else list(range(117, 138))
+    xq, xs = _rows((R,), K, fmt, g, scales)
+    wq, ws = _rows((1, N), K, fmt, g, scales)
+    xq, wq = xq & 0x77, wq & 0x77
+    one = torch.ones(1, device="cuda") if fmt == NV else None
+    y = moe.moe_grouped_mm_fp4(moe.Fp4(fmt, xq.cuda(), xs.cuda(), one), moe.Fp4(fmt, wq.cuda(), ws.cuda(), one),
+                               ref.offsets_of([R]).cuda(), out_dtype=F32).cpu().double()
+    want = torch.from_numpy(ref.values(xq, xs, fmt)) @ torch.from_numpy(ref.values(wq, ws, fmt))[0].T
+    bound = K / 64 * 2.0 ** -23 if K <= 8192 else 32 * 2.0 ** -23 + -(-K // 2048) * 2.0 ** -24
+    rel = ((y - want).abs() / want).max()
+    assert rel <= bound + 2.0 ** -24, (float(rel), bound)

@@ -21,10 +21,15 @@
 // with the room for only two of them 183 us, five of 32 bytes 164 us.
 // Both CTAs hold the scales of all 192 rows of x and of their own 128 of w.
 //
-// The accumulator does not round to nearest (gmm.cu), but sums of 4-bit products
-// mostly are exact in it: at K = 7168 results are 3e-8 to 4e-7 off for quantized
-// values of any spread and 2.8e-6 for scales drawn over the whole range, far
-// below the 4-bit rounding, so they are not added in parts.
+// The accumulator does not round to nearest (gmm.cu): each MMA of 64 along K can
+// lose 2^-23 of the sum.  For quantized normal values little of that adds up (3e-8
+// to 4e-7 at K = 7168), for values of one sign with scales over the whole range it
+// does: 3.9e-6 at K = 7168, 1.5e-5 at 32768, 5.3e-5 at 131072.  So the sum ends
+// every kSpan steps and the parts are added in registers, rounded to nearest, where
+// K is past kLong (FP32 results) or kLong16 (16-bit ones, whose own rounding is
+// 2^-9 or 2^-12).  Parts need the tiles of 128 rows, whose sums fit the registers:
+// with many rows 220 us rather than 180 (8192 rows over 4 experts of 4096 x 16384,
+// NVFP4; MXFP4 189 and 170), with few the time of one accumulation.
 //
 // Roles: warp 0 loads codes, warp 2 loads scales, warps 8..10 arrange them (w,
 // the first 128 rows of x, the rest) and warp 3 tells the leader, whose warp 1
@@ -50,6 +55,8 @@ namespace gmm4 {
 
 constexpr int kSlotRow = 32;                   // bytes of a row's scales in a slot
 constexpr int kTileM = 256, kStep = 256;
+constexpr int kSpan = 8;                       // steps of a part: 2048 elements
+constexpr int kLong = 8192, kLong16 = 32768;
 constexpr int kABytes = 128 * 128;
 constexpr int kBlockBytes = 128 * kSlotRow;    // scales of 128 rows
 constexpr int kDrainBytes = 16384;
@@ -60,6 +67,9 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // rows of x and have more stages of codes on the way: 39.6 us rather than 41.1
 // for 512 rows over 128 experts of 1536 x 2048 (NVFP4), 40.9 rather than 42.4 for
 // 4096 (MXFP4); past that many rows more groups take two tiles.
+enum Kind { kWide = 0, kFew = 1, kSum = 2 };   // kSum: FEW's shape, sums in parts
+constexpr bool few_of(int kind) { return kind != kWide; }
+
 template <bool FEW>
 struct Shape {
     static constexpr int kTileN = FEW ? 128 : 192, kStages = FEW ? 7 : 5, kSlots = FEW ? 4 : 5;
@@ -115,12 +125,13 @@ __device__ __forceinline__ Tile tile_of(const Args &a, const Shared &s, int t, i
 
 __device__ __forceinline__ int n_mma(int n) { return (n + 31) & ~31; }
 
-template <int FMT, typename OT, bool FEW>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<FEW>::kThreads, 1)
+template <int FMT, typename OT, int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<few_of(KIND)>::kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmSA,
             const __grid_constant__ CUtensorMap tmSB, const __grid_constant__ CUtensorMap tmY, const Args a)
 {
+    constexpr bool FEW = few_of(KIND), SUM = KIND == kSum;
     using S = Shape<FEW>;
     constexpr int kTileN = S::kTileN, kStages = S::kStages, kSlots = S::kSlots, kBlocks = S::kBlocks;
     constexpr int kStageBytes = S::kStageBytes, kSlotBytes = S::kSlotBytes;
@@ -258,55 +269,58 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const uint64_t s0 = tc::smem_desc(sfring, 0, 128, tc::kLayoutNone);
             int st = 0, sst = 0, tix = 0, g = 0;
             uint32_t ph = 0, sph = 0;
-            for (int t = cid; t < total && !*abort; t += n_cl, ++tix) {
+            for (int t = cid; t < total && !*abort; t += n_cl) {
                 const Tile T = tile_of<kTileN>(a, s, t, n_mt);
-                const int buf = tix & 1, n = n_mma(T.n);
-                if (!tc::mbar_wait_cluster(bar(s.acce[buf]), ((tix >> 1) & 1) ^ 1u, abort, kWaitNs))
-                    break;
-                tc::tc_fence_after();
-                const uint32_t acc = tmem + kTileN * buf;
+                const int n = n_mma(T.n);
                 const uint32_t id0 = tc::idesc_fp4(256, n, kMx, 0), id1 = kMx ? tc::idesc_fp4(256, n, kMx, 2) : id0;
-                MOE_STALL(a, s, t >= n_cl);
-                bool ok = true;
-                for (int j = 0; j < steps; ++j, ++g) {
-                    const int js = j % kSlotSteps;
-                    ok = (js != 0 || tc::mbar_wait_cluster(bar(s.sready[sst]), sph, abort, kWaitNs)) &&
-                         tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs);
-                    if (!ok)
+                for (int j0 = 0; j0 < steps; j0 += SUM ? kSpan : steps, ++tix) {
+                    const int buf = tix & 1, j1 = SUM ? min(j0 + kSpan, steps) : steps;
+                    if (!tc::mbar_wait_cluster(bar(s.acce[buf]), ((tix >> 1) & 1) ^ 1u, abort, kWaitNs))
                         break;
                     tc::tc_fence_after();
-                    const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
-                    const uint64_t sd = s0 + (sst * kSlotBytes + js * kWords * 512) / 16;
-                    const uint32_t ta = tmem + kTmemScales + (g & 1) * 48, tb = ta + 16;
+                    const uint32_t acc = tmem + kTileN * buf;
+                    MOE_STALL(a, s, t >= n_cl);
+                    bool ok = true;
+                    for (int j = j0; j < j1; ++j, ++g) {
+                        const int js = j % kSlotSteps;
+                        ok = (js != 0 || tc::mbar_wait_cluster(bar(s.sready[sst]), sph, abort, kWaitNs)) &&
+                             tc::mbar_wait(bar(s.full[st]), ph, abort, kWaitNs);
+                        if (!ok)
+                            break;
+                        tc::tc_fence_after();
+                        const uint64_t ad = a0 + st * (kStageBytes >> 4), bd = b0 + st * (kStageBytes >> 4);
+                        const uint64_t sd = s0 + (sst * kSlotBytes + js * kWords * 512) / 16;
+                        const uint32_t ta = tmem + kTmemScales + (g & 1) * 48, tb = ta + 16;
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w) {
-                        tc::tc_cp_32x128b_x4_pair(ta + 4 * w, sd + 32 * w);
-                        tc::tc_cp_32x128b_x4_pair(tb + 8 * w, sd + kBlockBytes / 16 + 32 * w);
-                        if (!FEW && n > 128)
-                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, sd + 2 * kBlockBytes / 16 + 32 * w);
-                    }
+                        for (int w = 0; w < kWords; ++w) {
+                            tc::tc_cp_32x128b_x4_pair(ta + 4 * w, sd + 32 * w);
+                            tc::tc_cp_32x128b_x4_pair(tb + 8 * w, sd + kBlockBytes / 16 + 32 * w);
+                            if (!FEW && n > 128)
+                                tc::tc_cp_32x128b_x4_pair(tb + 8 * w + 4, sd + 2 * kBlockBytes / 16 + 32 * w);
+                        }
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const int w = kMx ? kk >> 1 : kk;
-                        tc::mma_fp4_pair<kMx>(acc, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id1 : id0, ta + 4 * w, tb + 8 * w,
-                                              (j | kk) != 0 ? 1u : 0u);
-                    }
-                    tc::tc_commit_pair(bar(s.empty[st]));
-                    if (++st == kStages) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                    if (js == kSlotSteps - 1 || j == steps - 1) {
-                        tc::tc_commit_pair(bar(s.sempty[sst]));
-                        if (++sst == kSlots) {
-                            sst = 0;
-                            sph ^= 1u;
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const int w = kMx ? kk >> 1 : kk;
+                            tc::mma_fp4_pair<kMx>(acc, ad + 2 * kk, bd + 2 * kk, kk & 1 ? id1 : id0, ta + 4 * w, tb + 8 * w,
+                                                  ((j - j0) | kk) != 0 ? 1u : 0u);
+                        }
+                        tc::tc_commit_pair(bar(s.empty[st]));
+                        if (++st == kStages) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                        if (js == kSlotSteps - 1 || j == steps - 1) {
+                            tc::tc_commit_pair(bar(s.sempty[sst]));
+                            if (++sst == kSlots) {
+                                sst = 0;
+                                sph ^= 1u;
+                            }
                         }
                     }
+                    if (!ok)                             // a part of the sums: not to be drained
+                        break;
+                    tc::tc_commit_pair(bar(s.accf[buf]));
                 }
-                if (!ok)                                 // a part of the sums: not to be drained
-                    break;
-                tc::tc_commit_pair(bar(s.accf[buf]));
             }
             tc::tc_commit_pair(bar(s.fin));
         }
@@ -374,31 +388,71 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         const int q = warp & 3;                         // TMEM lane quadrant
         int tix = 0, flip = 0;
         OT *out = static_cast<OT *>(a.out);
-        for (int t = cid; t < total; t += n_cl, ++tix) {
+        for (int t = cid; t < total; t += n_cl) {
             const Tile T = tile_of<kTileN>(a, s, t, n_mt);
-            const int m = T.m0 + 128 * rank + 32 * q + lane, buf = tix & 1;
+            const int m = T.m0 + 128 * rank + 32 * q + lane;
             float f = 1.f, g = 1.f;
             if (!kMx)
                 fp4::factors(*a.xa, a.wa[T.e], f, g);
-            if (!tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs))
-                break;
-            tc::tc_fence_after();
-            const uint32_t acc = tmem + kTileN * buf + (static_cast<uint32_t>(32 * q) << 16);
             uint8_t *tiles = sf + kSlots * kSlotBytes + q * 4096;
-            for (int c0 = 0; c0 < T.n; c0 += 32) {
-                uint32_t v[32];
-                tc::tmem_ld_32x32b_x32(acc + c0, v);
-                tc::tmem_ld_wait_for(v);
-                if (T.n - c0 < 32) {                     // a TMA store would reach into the next group's rows
+            auto store = [&](int c0, const uint32_t (&v)[32]) {
+                if (T.n - c0 < 32)                       // a TMA store would reach into the next group's rows
                     gmm::store_rows<OT>(v, out + static_cast<int64_t>(T.r0 + c0) * a.N, a.N, m, a.N, T.n - c0, lane, f, g);
+                else
+                    gmm::drain_rows<OT>(v, tiles, flip, &tmY, m - lane, T.r0 + c0, a.N, lane, f, g);
+            };
+            constexpr int kGroups = kTileN / 32;
+            float sum[SUM ? kGroups : 1][32] = {};
+            bool ok = true;
+            for (int j0 = 0; j0 < steps; j0 += SUM ? kSpan : steps, ++tix) {
+                const int buf = tix & 1;
+                ok = tc::mbar_wait_cluster(bar(s.accf[buf]), (tix >> 1) & 1, abort, kWaitNs);
+                if (!ok)
                     break;
+                tc::tc_fence_after();
+                const uint32_t acc = tmem + kTileN * buf + (static_cast<uint32_t>(32 * q) << 16);
+                if constexpr (SUM) {
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c) {
+                        if (32 * c < T.n) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                uint32_t v[16];
+                                tc::tmem_ld_32x32b_x16(acc + 32 * c + h, v);
+                                tc::tmem_ld_wait_for(v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    sum[c][h + i] += __uint_as_float(v[i]);
+                            }
+                        }
+                    }
+                } else {
+                    for (int c0 = 0; c0 < T.n; c0 += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld_32x32b_x32(acc + c0, v);
+                        tc::tmem_ld_wait_for(v);
+                        store(c0, v);
+                    }
                 }
-                gmm::drain_rows<OT>(v, tiles, flip, &tmY, m - lane, T.r0 + c0, a.N, lane, f, g);
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
             }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive_cluster_relaxed(tc::mapa(bar(s.acce[buf]), 0));
+            if (!ok)
+                break;
+            if constexpr (SUM) {
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c) {
+                    if (32 * c < T.n) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(sum[c][i]);
+                        store(32 * c, v);
+                    }
+                }
+            }
         }
         tc::bulk_wait<0>();
         // rows outside every group
@@ -433,11 +487,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 
 // ---------------------------------------------------------------- host
 
-template <int FMT, typename OT, bool FEW>
+template <int FMT, typename OT, int KIND>
 static moe_status_t launch(const CUtensorMap (&tm)[6], const Args &a, cudaStream_t s)
 {
+    constexpr bool FEW = few_of(KIND);
     using S = Shape<FEW>;
-    auto k = gemm_kernel<FMT, OT, FEW>;
+    auto k = gemm_kernel<FMT, OT, KIND>;
     static std::atomic<uint64_t> done{0};
     if (!smem_attr_once(done, reinterpret_cast<const void *>(k), smem_of<FEW>()))
         return MOE_ERR_CUDA;
@@ -449,12 +504,20 @@ static moe_status_t launch(const CUtensorMap (&tm)[6], const Args &a, cudaStream
                ? MOE_OK : MOE_ERR_CUDA;
 }
 
-template <int FMT, bool FEW>
-static moe_status_t launch_as(const CUtensorMap (&tm)[6], const Args &a, int32_t ydt, cudaStream_t s)
+template <int FMT, int KIND>
+static moe_status_t launch_type(const CUtensorMap (&tm)[6], const Args &a, int32_t ydt, cudaStream_t s)
 {
     if (ydt == MOE_FP32)
-        return launch<FMT, float, FEW>(tm, a, s);
-    return ydt == MOE_BF16 ? launch<FMT, __nv_bfloat16, FEW>(tm, a, s) : launch<FMT, __half, FEW>(tm, a, s);
+        return launch<FMT, float, KIND>(tm, a, s);
+    return ydt == MOE_BF16 ? launch<FMT, __nv_bfloat16, KIND>(tm, a, s) : launch<FMT, __half, KIND>(tm, a, s);
+}
+
+template <int FMT>
+static moe_status_t launch_kind(const CUtensorMap (&tm)[6], const Args &a, int32_t ydt, int kind, cudaStream_t s)
+{
+    if (kind == kSum)
+        return launch_type<FMT, kSum>(tm, a, ydt, s);
+    return kind == kFew ? launch_type<FMT, kFew>(tm, a, ydt, s) : launch_type<FMT, kWide>(tm, a, ydt, s);
 }
 
 }  // namespace gmm4
@@ -484,8 +547,8 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_32B;
     const CUtensorMapDataType ty = ydt == MOE_FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : ydt == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const bool few = R <= 64 * static_cast<int64_t>(E);
-    const int tn = few ? Shape<true>::kTileN : Shape<false>::kTileN;
+    const int kind = K > (ydt == MOE_FP32 ? kLong : kLong16) ? kSum : R <= 64 * static_cast<int64_t>(E) ? kFew : kWide;
+    const int tn = few_of(kind) ? Shape<true>::kTileN : Shape<false>::kTileN;
     if (!ragged::list_fits(E, R, (N + kTileM - 1) / kTileM, tn))
         return MOE_ERR_UNSUPPORTED;
     CUtensorMap tm[6];
@@ -495,9 +558,6 @@ MOE_API moe_status_t moe_grouped_mm_fp4(const uint8_t *xq, const uint8_t *xs, co
         !tmap_rows_out(&tm[5], ty, ydt == MOE_FP32 ? 4 : 2, y, N, R))
         return MOE_ERR_CUDA;
     const Args a{offsets, x_alpha, w_alpha, y, dev_status, R, E, N, K MOE_STALL_VALUE};
-    if (fmt == MOE_FP4_NVFP4)
-        return few ? launch_as<MOE_FP4_NVFP4, true>(tm, a, ydt, as_stream(stream))
-                   : launch_as<MOE_FP4_NVFP4, false>(tm, a, ydt, as_stream(stream));
-    return few ? launch_as<MOE_FP4_MXFP4, true>(tm, a, ydt, as_stream(stream))
-               : launch_as<MOE_FP4_MXFP4, false>(tm, a, ydt, as_stream(stream));
+    return fmt == MOE_FP4_NVFP4 ? launch_kind<MOE_FP4_NVFP4>(tm, a, ydt, kind, as_stream(stream))
+                                : launch_kind<MOE_FP4_MXFP4>(tm, a, ydt, kind, as_stream(stream));
 }
