@@ -34,7 +34,7 @@ def state(monkeypatch):
     M, k, E = 3, 2, 2
     groups = ragged.Groups(torch.tensor([0, 1, 2, 0, 1, 2]), torch.tensor([[0, 3], [1, 4], [2, 5]]),
                            torch.tensor([0, 3, 6], dtype=torch.int32))
-    monkeypatch.setattr(ragged, "group_routes", lambda ids, E: groups)
+    monkeypatch.setattr(ragged, "group_routes", lambda ids, E, dev_status=None: groups)
     return st
 
 

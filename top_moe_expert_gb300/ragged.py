@@ -31,12 +31,12 @@ class Groups(NamedTuple):
     offsets: torch.Tensor
 
 
-def group_routes(topk_ids: torch.Tensor, E: int) -> Groups:
+def group_routes(topk_ids: torch.Tensor, E: int, dev_status=None) -> Groups:
     """Rows for the routes topk_ids [M, k]: R = M * k of them, the valid routes
     first, by expert and then by route; the rest are padding."""
     M, k = topk_ids.shape
     R = M * k
-    routes, experts, _ = moe.moe_align_block_size(topk_ids, E, 1)
+    routes, experts, _ = moe.moe_align_block_size(topk_ids, E, 1, dev_status=dev_status)
     routes, experts = routes[:R], experts[:R]
     e = torch.where(experts < 0, E, experts)
     offsets = torch.searchsorted(e, torch.arange(E + 1, device=e.device, dtype=e.dtype), out_int32=True)
@@ -94,9 +94,10 @@ def _guarded(*inputs):
 
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets):
+    def forward(ctx, x, w, offsets, dev_status):
         ctx.save_for_backward(x, w, offsets)
-        return moe.moe_grouped_mm(x, w, offsets)
+        ctx.dev_status = dev_status
+        return moe.moe_grouped_mm(x, w, offsets, dev_status=dev_status)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -105,20 +106,24 @@ class _GroupedLinear(torch.autograd.Function):
         dy = dy.contiguous()
         if dy.data_ptr() % 16:                                       # a view into a larger gradient
             dy = dy.clone()
-        dx = moe.moe_grouped_mm_dgrad(dy, w, offsets) if ctx.needs_input_grad[0] else None
-        dw = moe.moe_grouped_mm_wgrad(dy, x, offsets, out_dtype=w.dtype) if ctx.needs_input_grad[1] else None
-        return dx, dw, None
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = moe.moe_grouped_mm_dgrad(dy, w, offsets, dev_status=ctx.dev_status)
+        if ctx.needs_input_grad[1]:
+            dw = moe.moe_grouped_mm_wgrad(dy, x, offsets, out_dtype=w.dtype, dev_status=ctx.dev_status)
+        return dx, dw, None, None
 
 
-def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dev_status=None) -> torch.Tensor:
     """moe_grouped_mm with gradients: rows x [R, K] of each expert times its
-    w [E, N, K], transposed; first derivatives of x and w.  To capture the
+    w [E, N, K], transposed; first derivatives of x and w.  dev_status takes the
+    device errors of the forward pass and, later, of the backward pass.  To capture the
     backward pass, drop earlier graphs of the same leaves first: one that came
     through here on another stream is refused, for x, w and what they are made
     of within a few operations (a leaf that only other operations have used,
     or one further off, is not known here)."""
     (x, w), kept = _guarded(x, w)
-    return _GroupedLinear.apply(x, w, offsets)
+    return _GroupedLinear.apply(x, w, offsets, dev_status)
 
 
 def _swiglu(h: torch.Tensor) -> torch.Tensor:
@@ -136,14 +141,15 @@ def _combine(rows: torch.Tensor, groups: Groups, weights: torch.Tensor) -> torch
 
 
 def expert_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
-                 w2: torch.Tensor) -> torch.Tensor:
+                 w2: torch.Tensor, dev_status=None) -> torch.Tensor:
     """y [M, d] (fp32): sum_j w_j W2_e (SiLU(Wg_e x) * Wu_e x), differentiable in
     x [M, d], topk_w [M, k], w13 [E, 2I, d] and w2 [E, d, I] (one of bf16 and
-    fp16; h is rounded to it)."""
-    groups = group_routes(topk_ids, w13.shape[0])
+    fp16; h is rounded to it).  dev_status int32 [2]: invalid routes are counted
+    in the first, a device error of either pass is left in the second."""
+    groups = group_routes(topk_ids, w13.shape[0], dev_status)
     (rows, weights, w13, w2), kept = _guarded(x[groups.token], _weights(topk_w, groups), w13, w2)
-    h = _swiglu(_GroupedLinear.apply(rows, w13, groups.offsets)).to(x.dtype)
-    return _combine(_GroupedLinear.apply(h, w2, groups.offsets), groups, weights)
+    h = _swiglu(_GroupedLinear.apply(rows, w13, groups.offsets, dev_status)).to(x.dtype)
+    return _combine(_GroupedLinear.apply(h, w2, groups.offsets, dev_status), groups, weights)
 
 
 def tensor_alpha(v: torch.Tensor) -> torch.Tensor:
@@ -158,18 +164,19 @@ def quantize_experts(w: torch.Tensor, fmt: int) -> "moe.Fp4":
 
 
 def expert_layer_fp4(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: "moe.Fp4", w2: "moe.Fp4",
-                     alpha_x: torch.Tensor | None = None, alpha_h: torch.Tensor | None = None) -> torch.Tensor:
+                     alpha_x: torch.Tensor | None = None, alpha_h: torch.Tensor | None = None,
+                     dev_status=None) -> torch.Tensor:
     """expert_layer on 4-bit experts and activations: x and h are quantized to
     the experts' format; alpha_x, alpha_h [1]: NVFP4's constants of x and h,
-    e.g. tensor_alpha of calibration data."""
+    e.g. tensor_alpha of calibration data.  dev_status as expert_layer's."""
     fmt = w13.fmt
-    groups = group_routes(topk_ids, w13.q.shape[0])
+    groups = group_routes(topk_ids, w13.q.shape[0], dev_status)
     q, s = moe.moe_fp4_quantize(x, fmt, alpha_x)                      # a token's codes serve all its routes
     rows = moe.Fp4(fmt, q[groups.token], s[groups.token], alpha_x)
-    h = _swiglu(moe.moe_grouped_mm_fp4(rows, w13, groups.offsets, out_dtype=torch.float32))
+    h = _swiglu(moe.moe_grouped_mm_fp4(rows, w13, groups.offsets, out_dtype=torch.float32, dev_status=dev_status))
     hq = moe.Fp4(fmt, *moe.moe_fp4_quantize(h, fmt, alpha_h), alpha_h)
-    return _combine(moe.moe_grouped_mm_fp4(hq, w2, groups.offsets, out_dtype=torch.float32), groups,
-                    _weights(topk_w, groups))
+    y = moe.moe_grouped_mm_fp4(hq, w2, groups.offsets, out_dtype=torch.float32, dev_status=dev_status)
+    return _combine(y, groups, _weights(topk_w, groups))
 
 
 def main() -> None:
