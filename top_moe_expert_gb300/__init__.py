@@ -181,11 +181,17 @@ def _guard(device):
 _NO_GUARD = contextlib.nullcontext()
 
 
+# torch's own handles without the objects around them; a torch without CUDA, on
+# which the host-only functions run, has neither.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(stream=None, device=None):
     """The stream handle: `stream`, or the current stream of `device`."""
     if stream is None:
         # the handle alone: a Stream object costs more than a small launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device.index)
+        return _raw_stream(torch.cuda.current_device() if device is None else device.index)
     sd = getattr(stream, "device", None)
     if device is not None and sd is not None and sd != device:
         raise ValueError(f"stream is on {sd}; the call's tensors are on {device}")
@@ -653,7 +659,6 @@ def _arg(t, name: str, dtypes, dim, device=None):
 # The calls of a single token take about as long on the host as on the GPU, so
 # the functions below check their arguments in one expression where all is in
 # order, and go to the checks that name what is not only when it fails.
-_raw_stream, _current_gpu = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _launch(gpu: int, name: str, *args) -> None:
