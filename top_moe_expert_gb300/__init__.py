@@ -828,11 +828,15 @@ class Fp4:
     """Rows in NVFP4 or MXFP4: q uint8 [..., K/2], s uint8 [..., Ks] and, for
     NVFP4, alpha float32 (one for activations [R, .], one per expert for
     weights [E, N, .]), as moe_fp4_quantize returns them.  Checked when the
-    object is made; its fields are not to be changed."""
+    object is made, for every launch that takes it: its fields are fixed."""
     __slots__ = ("fmt", "q", "s", "alpha")
 
     def __init__(self, fmt: int, q: torch.Tensor, s: torch.Tensor, alpha: torch.Tensor | None = None):
-        self.fmt, self.q, self.s, self.alpha = fmt, q, s, alpha
+        put = object.__setattr__
+        put(self, "fmt", fmt)
+        put(self, "q", q)
+        put(self, "s", s)
+        put(self, "alpha", alpha)
         try:
             gpu, qs, ss, block, n = q.get_device(), q.shape, s.shape, _FP4_BLOCK[fmt], q.dim()
             half, rows = qs[-1], qs[0]
@@ -848,6 +852,15 @@ class Fp4:
             ok = False
         if not ok:
             self._need()
+
+    def __setattr__(self, name, value):
+        raise AttributeError("an Fp4's fields are fixed; make a new one")
+
+    def __delattr__(self, name):
+        raise AttributeError("an Fp4's fields are fixed; make a new one")
+
+    def __reduce__(self):                                             # copies are made, and checked, anew
+        return Fp4, (self.fmt, self.q, self.s, self.alpha)
 
     def _need(self):
         """What the constructor asks, with the reason why not."""
