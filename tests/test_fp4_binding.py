@@ -50,3 +50,20 @@ def test_copies_are_checked_again(rec):
         assert y is not w and y.fmt == w.fmt and torch.equal(y.q, w.q) and torch.equal(y.alpha, w.alpha)
         moe.moe_grouped_mm_fp4(x, y, off)
     assert len(rec.calls) == 3
+
+
+def test_arguments_of_other_kinds_are_refused(rec):
+    x, w, off = _pair()
+    for a in ((x.q, w, off), (x, w.q, off), (None, w, off), (x, None, off), (x, w, [0, 1, 2]), (x, w, None), (x, w, off.float())):
+        with pytest.raises(ValueError):
+            moe.moe_grouped_mm_fp4(*a)
+    t = torch.zeros((5, 32), dtype=torch.bfloat16)
+    for f in (moe.moe_grouped_mm, moe.moe_grouped_mm_dgrad, moe.moe_grouped_mm_wgrad):
+        for a in ((t, None, off), (None, t, off), (t, t, [0, 1, 2]), (t, t, None)):
+            with pytest.raises(ValueError):
+                f(*a)
+    for f in (lambda: moe.moe_fp4_quantize(None, 1), lambda: moe.moe_fp4_quantize(t, 0, [1.0]),
+              lambda: moe.moe_fp4_dequantize(x.q, None, 1), lambda: moe.Fp4(0, x.q, None, x.alpha), lambda: moe.Fp4(0, None, x.s)):
+        with pytest.raises(ValueError):
+            f()
+    assert not rec.calls

@@ -931,8 +931,10 @@ def moe_grouped_mm_fp4(x: Fp4, w: Fp4, offsets: torch.Tensor, out_dtype=torch.bf
                        stream=None):
     """y [R, N]: moe_grouped_mm on 4-bit operands, x [R, K] and w [E, N, K] of
     the same format (offsets [0, R] with E = 1: the dense product)."""
+    if not (isinstance(x, Fp4) and isinstance(w, Fp4)):
+        raise ValueError("x and w must be Fp4")
     gpu, dev = x.q.get_device(), x.q.device
-    if not (offsets.dtype is torch.int32 and offsets.get_device() == gpu >= 0 and offsets.dim() == 1
+    if not (isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.get_device() == gpu >= 0 and offsets.dim() == 1
             and offsets.is_contiguous()):
         _arg(offsets, "offsets", _IDS, 1, dev)
     E = _experts(offsets)
