@@ -484,10 +484,12 @@ moe_status_t moe_ffn_decode_noalloc(const void *x, int32_t xdt, int32_t M, int32
  *   moe_grouped_mm_wgrad: dw[e][n][k] = sum_r dy[r][n] x[r][k]  (+ dw with
  *                         accumulate = 1; an expert without rows adds zero)
  *   for the rows r of expert e.  y [R][N], dx [R][K] and dw [E][N][K] are of dt
- *   or MOE_FP32; sums are FP32, rounded once (for FP32 results, and for
- *   16-bit ones past 16384 contracted elements, in parts of 512 elements added
- *   to nearest, so that long sums do not drift); padding rows of y and dx are
- *   set to zero.  The same call gives the same bits, and among calls
+ *   or MOE_FP32; sums are FP32, rounded once; padding rows of y and dx are set
+ *   to zero.  A sum loses at most 2^-23 of the terms' magnitudes per 16
+ *   elements, or, for FP32 results and for 16-bit ones past 16384 contracted
+ *   elements, per 16 of a part of 512 and 2^-24 per part, as the parts are
+ *   added to nearest; moe_grouped_mm of at most four rows adds to nearest
+ *   throughout, 2^-24 per 32 elements.  The same call gives the same bits, and among calls
  *   of more than four rows (and among those of at most four, which have their
  *   own kernel) a row's result does not depend on the other rows.  No
  *   workspace.  (accumulate to MOE_FP32 adds in the L2, where a subnormal sum
@@ -523,8 +525,9 @@ moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t dt, con
  *     127], byte X + 127, code = E2M1(v 2^-X); value = 2^X * code; alpha NULL.
  *   A block that holds a NaN or an infinity gets the scale NaN (0x7F / 0xFF)
  *   and zero codes: it reads back, and multiplies, as NaN.
- *   v [rows][K] of vdt (MOE_FP32, MOE_BF16 or MOE_FP16; the values of
- *   moe_fp4_dequantize are rounded to it once).
+ *   v [rows][K] of vdt (MOE_FP32, MOE_BF16 or MOE_FP16; moe_fp4_dequantize
+ *   rounds alpha * (S * code), the product in brackets exact, to FP32 and that
+ *   to the 16-bit types).
  * Limits: K % 32 == 0, rows % groups == 0; tensors 16-byte aligned
  * (MOE_ERR_INVALID_ARG); K <= 2^31 - 1024, rows * K / 32 < 2^32
  * (MOE_ERR_UNSUPPORTED).

@@ -30,9 +30,10 @@
 // other CTA's waits expire too.  Each CTA reports its flag at its end, as
 // MOE_ERR_TIMEOUT in dev_status[1].
 //
-// Bound by the tensor pipe at the clock that the power cap leaves for many rows
-// per expert (8192 x 8192 x 8192 bf16: forward 567, dgrad 567, wgrad 596 us, 1.94
-// PFLOP/s), by HBM for few (4096 rows over 128 experts of 1536 x 2048: 126 us, 6.6
+// Bound by the tensor pipe for many rows per expert, at the clock that the power
+// cap leaves: 8192 x 8192 x 8192 bf16 in runs of a few calls forward 572, dgrad
+// 566, wgrad (FP32) 589 us, 1.9 PFLOP/s; back to back for 3 s 644, 641 and 663 us,
+// 1.7 PFLOP/s.  By HBM for few (4096 rows over 128 experts of 1536 x 2048: 126 us, 6.6
 // TB/s; dgrad 124; wgrad 139, its 805 MB of dw).
 #include <cuda.h>
 
@@ -56,9 +57,12 @@ constexpr int kMaxStages = 8;
 // The tensor cores add to an FP32 accumulator without rounding to nearest, so a
 // long sum drifts (measured: 1.1e-9 of the result per contracted element, 4.4e-6
 // at 4096).  Sum kernels end the accumulation every kSpan steps (512 elements)
-// and add the parts in registers, rounded to nearest: 5e-7 at any length.  FP32
-// results take them always, 16-bit ones -- whose own rounding is 2^-9 or 2^-12 --
-// where the contraction can be longer than kLong.
+// and add the parts in registers, rounded to nearest.  What is left grows with the
+// parts' own roundings alone: terms of one sign, drawn at random, are at worst
+// 9e-7 off at 4096 terms, 1.2e-6 at 65536 and 2.4e-6 at 2^20; equal terms, whose
+// parts all round the same way, 3.1e-5 at 2^20.  FP32 results take them always,
+// 16-bit ones -- whose own rounding is 2^-9 or 2^-12 -- where the contraction can
+// be longer than kLong.
 constexpr int kSpan = 8;
 constexpr int kLong = 16384;
 
@@ -75,7 +79,11 @@ constexpr int kLong = 16384;
 // 127 us rather than 132 for 4096 rows over 128 experts of 1536 x 2048, 13.6
 // rather than 16.1 (dgrad) for 800 rows over 40 of 1000 x 520.  Past 64 rows per
 // expert more and more groups take two tiles, which read the weights twice: 169
-// rather than 158 us at 80 rows (Zipf) over 16 of 4096 x 7168.
+// rather than 158 us at 80 rows (Zipf) over 16 of 4096 x 7168.  The rule knows the
+// mean alone, as the counts are on the device: rows that all go to a few of many
+// experts get narrow tiles where wide ones are faster (16384 rows on 8 of 256
+// experts: 74 rather than 66 us at 1536 x 2048, 317 rather than 287 at 4096 x
+// 4096).
 //
 // Sum kernels have both forms: of the forward and dgrad with tiles of 128 rows,
 // of wgrad with a second staging tile per warp in place of a stage, as with few

@@ -36,8 +36,9 @@
 // issues copies and MMAs; warps 4..7 drain the accumulators.  Every wait is
 // bounded, and an expired one is reported, as in gmm.cu.
 //
-// Bound by feeding the tiles: 164 us at 8192 x 8192 x 8192 (NVFP4; MXFP4 149),
-// 128 us with every copy left out; by HBM for few rows per expert (42 us for 4096
+// Bound by feeding the tiles: 168 us at 8192 x 8192 x 8192 (NVFP4; MXFP4 151) in
+// runs of a few calls, 128 us with every copy left out; back to back for 3 s 186
+// and 165 us under the power cap.  By HBM for few rows per expert (42 us for 4096
 // rows over 128 experts of 1536 x 2048, 34 us of bytes).
 #include <cuda.h>
 
@@ -66,7 +67,9 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // FEW kernels, for at most 64 rows per expert as in gmm.cu, take tiles of 128
 // rows of x and have more stages of codes on the way: 39.6 us rather than 41.1
 // for 512 rows over 128 experts of 1536 x 2048 (NVFP4), 40.9 rather than 42.4 for
-// 4096 (MXFP4); past that many rows more groups take two tiles.
+// 4096 (MXFP4); past that many rows more groups take two tiles.  As there, rows
+// on a few of many experts get these tiles all the same (16384 rows on 8 of 256
+// experts of 1536 x 2048, MXFP4: 31 us rather than 27).
 enum Kind { kWide = 0, kFew = 1, kSum = 2 };   // kSum: FEW's shape, sums in parts
 constexpr bool few_of(int kind) { return kind != kWide; }
 
