@@ -83,3 +83,29 @@ def test_long_sums_of_one_sign_do_not_drift(fmt, K):
     bound = K / 64 * 2.0 ** -23 if K <= 8192 else 32 * 2.0 ** -23 + -(-K // 2048) * 2.0 ** -24
     rel = ((y - want).abs() / want).max()
     assert rel <= bound + 2.0 ** -24, (float(rel), bound)
+
+
+@pytest.mark.parametrize("fmt", [NV, MX])
+@pytest.mark.parametrize("sizes", [[700, 0, 33, 900], [8] * 40])
+def test_same_bits_beside_other_work(fmt, sizes):
+    """Repeated calls, alone and beside a stream that keeps the memory busy, give the bits of the first, which are exact."""
+    g = torch.Generator().manual_seed(len(sizes))
+    R, E, N, K = sum(sizes), len(sizes), 1032, 4192
+    scales = [0x30, 0x38, 0x40] if fmt == NV else [126, 127, 128]
+    xq, xs = _rows((R,), K, fmt, g, scales)
+    wq, ws = _rows((E, N), K, fmt, g, scales)
+    a = (torch.ones(1, device="cuda"), torch.ones(E, device="cuda")) if fmt == NV else (None, None)
+    X, W = moe.Fp4(fmt, xq.cuda(), xs.cuda(), a[0]), moe.Fp4(fmt, wq.cuda(), ws.cuda(), a[1])
+    off = ref.offsets_of(sizes).cuda()
+    want, _ = ref.mm(torch.from_numpy(ref.values(xq, xs, fmt)), torch.from_numpy(ref.values(wq, ws, fmt)), sizes)
+    first = moe.moe_grouped_mm_fp4(X, W, off, out_dtype=F32)
+    assert torch.equal(first.cpu().double(), want)
+    side, buf = torch.cuda.Stream(), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(120):
+        if i >= 60:
+            with torch.cuda.stream(side):
+                buf.fill_(i)
+        differ += (moe.moe_grouped_mm_fp4(X, W, off, out_dtype=F32) != first).sum()
+    torch.cuda.synchronize()
+    assert int(differ) == 0

@@ -89,3 +89,18 @@ def test_a_limit_runs_from_the_last_progress(emu):
     assert expires(np.arange(n) // 60) == 51                    # a role that rests for longer than the limit
     wrap = (np.arange(n) + 2 ** 31 - 100).astype(np.int64).astype(np.uint32).astype(np.int64)
     assert expires(np.where(wrap >= 2 ** 31, wrap - 2 ** 32, wrap)) == n
+
+
+def test_arrivals_on_another_cta_name_their_scope():
+    """An mbarrier arrival without a scope is ordered at CTA scope, which on a barrier of another CTA of the cluster does not
+    order what it announces for the thread that waits there: each says which one it means, and wgrad's takes the cluster's."""
+    import glob
+    import re
+    arrivals = []
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        code = re.sub(r"//[^\n]*", "", open(path).read())
+        arrivals += [(os.path.basename(path), m) for m in re.findall(r"mbarrier\.arrive[\w.:]*", code) if "shared::cluster" in m]
+    assert arrivals
+    for path, a in arrivals:
+        assert re.search(r"\.(release|relaxed)\.(cta|cluster)\.", a) or "commit" in a, (path, a)
+    assert "mbar_arrive_cluster_smem" not in open(os.path.join(CSRC, "gmm.cu")).read()

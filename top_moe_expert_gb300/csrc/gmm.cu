@@ -89,7 +89,8 @@ constexpr int kLong = 16384;
 // of wgrad with a second staging tile per warp in place of a stage, as with few
 // rows per expert dw's stream bounds it (FP32 results, 32 rows for each of 128
 // experts of 1536 x 2048: forward 132 rather than 137 us, wgrad 287 rather than
-// 292; 20 rows for each of 40 of 1000 x 520: wgrad 19.6 rather than 20.6).
+// 292; 20 rows for each of 40 of 1000 x 520: wgrad 19.6 rather than 20.6,
+// and 20.3 since its tails are handed over at cluster scope).
 enum Kind { kPlain = 0, kNarrow = 1, kSum = 2, kSumFew = 3 };
 constexpr bool sums(int kind) { return kind == kSum || kind == kSumFew; }
 constexpr int drain_of(int kind) { return sums(kind) ? 8 : 4; }
@@ -462,7 +463,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (lane == 0)
                         tc::mbar_arrive(bar(s.full[q]));
                 } else if (lane == 0) {
-                    tc::mbar_arrive_cluster_smem(tc::mapa(bar(s.peer[q]), 0));
+                    tc::mbar_arrive_cluster(tc::mapa(bar(s.peer[q]), 0));
                 }
             }
         }
