@@ -33,8 +33,9 @@
 // Bound by the tensor pipe for many rows per expert, at the clock that the power
 // cap leaves: 8192 x 8192 x 8192 bf16 in runs of a few calls forward 572, dgrad
 // 566, wgrad (FP32) 589 us, 1.9 PFLOP/s; back to back for 3 s 644, 641 and 663 us,
-// 1.7 PFLOP/s.  By HBM for few (4096 rows over 128 experts of 1536 x 2048: 126 us, 6.6
-// TB/s; dgrad 124; wgrad 139, its 805 MB of dw).
+// 1.7 PFLOP/s.  By HBM for few: 4096 rows (Zipf) over 128 experts of 1536 x 2048
+// in bf16 128 us, 6.5 TB/s; dgrad 125; wgrad 161, its 805 MB of dw (154 with the
+// ragged tails announced at CTA scope, which PTX does not order).
 #include <cuda.h>
 
 #include "attr.h"
