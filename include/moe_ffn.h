@@ -96,6 +96,7 @@ typedef enum { MOE_W_MXFP8 = 0, MOE_W_AWQ4 = 1, MOE_W_NVFP4S = 3 } moe_wfmt_t;
 typedef enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 } moe_dtype_t;
 typedef enum { MOE_PATH_DECODE = 0, MOE_PATH_GROUPED = 1 } moe_path_t;
 typedef enum { MOE_FP4_NVFP4 = 0, MOE_FP4_MXFP4 = 1 } moe_fp4_t;
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 
 /* One projection of all experts; see "Weight formats" above. */
 typedef struct {
@@ -122,6 +123,41 @@ int32_t moe_abi_version(void);
  * Limits: 1 <= k <= min(E, 32), E <= 4096. */
 moe_status_t moe_topk_softmax(const float *logits, int32_t M, int32_t E, int32_t k,
                               int32_t *topk_ids, float *topk_w, void *stream);
+
+/* General routing (no counterpart on the pages): softmax or sigmoid scores, a
+ * bias that balances the experts, groups of experts, and the logits' gradient.
+ *   logits   [M][E] of ldt (MOE_FP32, MOE_BF16 or MOE_FP16)
+ *   score    MOE_SCORE_SOFTMAX: s_e = exp(l_e) / sum over the E experts;
+ *            MOE_SCORE_SIGMOID: s_e = 1 / (1 + exp(-l_e))
+ *   bias     fp32 [E] or NULL; only the choice sees it: experts are chosen by
+ *            s_e + bias[e], or by l_e without a bias
+ *   groups   equal groups of consecutive experts (E % groups == 0); a group is
+ *            worth the sum of its group_top (1 or 2) best values of s_e +
+ *            bias[e] (without a bias: its best l_e, or the sum of its two best
+ *            s_e), and only the topk_groups best groups are chosen from
+ *   topk_ids int32 [M][k], topk_w fp32 [M][k]: slots in descending order of
+ *            what the choice goes by; topk_w = scale * s, divided by the sum of
+ *            the chosen s with renorm = 1
+ *   load     int32 [E] or NULL: INCREASED by the number of slots each expert got
+ * All comparisons are of the values in binary64, equal ones by index.  An
+ * expert whose logit or bias is -inf is not available: where fewer than k are
+ * left the last slots get id -1 (an invalid route) and weight 0.  A logit or
+ * bias that is NaN or +inf is not chosen either, and makes all weights of the
+ * tokens that see it NaN.  scale is finite and > 0.
+ * moe_route_bwd: dlogits [M][E] (of ldt) from dw fp32 [M][k], the gradient of
+ * topk_w, at the same logits, ids, score, renorm and scale; the choice itself
+ * and the bias have no gradient.  Slots with ids outside [0, E) add nothing,
+ * an expert named by several slots gets their sum, every other element is 0
+ * (softmax with renorm = 0: all experts have a gradient).  A token with a NaN
+ * or +inf logit gets NaN.
+ * Limits: k <= topk_groups * (E / groups) (MOE_ERR_INVALID_ARG); E <= 1024,
+ * k <= 32, groups <= 32, M * k < 2^31 (MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_route(const void *logits, int32_t ldt, const float *bias, int32_t M, int32_t E, int32_t k,
+                       int32_t score, int32_t groups, int32_t topk_groups, int32_t group_top, int32_t renorm,
+                       float scale, int32_t *topk_ids, float *topk_w, int32_t *load, void *stream);
+moe_status_t moe_route_bwd(const float *dw, const void *logits, int32_t ldt, const int32_t *topk_ids, int32_t M,
+                           int32_t E, int32_t k, int32_t score, int32_t renorm, float scale, void *dlogits,
+                           void *stream);
 
 /* --------------------------------------------------------------- alignment
  * Route alignment by stable construction ("Route-Block Membership Selects
@@ -507,6 +543,44 @@ moe_status_t moe_grouped_mm_dgrad(const void *dy, const void *w, int32_t dt, con
 moe_status_t moe_grouped_mm_wgrad(const void *dy, const void *x, int32_t dt, const int32_t *offsets, int32_t R,
                                   int32_t E, int32_t N, int32_t K, void *dw, int32_t wdt, int32_t accumulate,
                                   int32_t *dev_status, void *stream);
+
+/* The experts' activation between the two products, with dropout:
+ *   gu [R][2I] of dt (MOE_BF16, MOE_FP16 or MOE_FP32), rows [g | u];
+ *   moe_swiglu_dropout:     h [R][I] of dt:    h = f silu(g) u
+ *   moe_swiglu_dropout_bwd: dgu [R][2I] of dt from dh [R][I] of dt:
+ *                           dg = f dh u silu'(g), du = f dh silu(g)
+ * with T = p * 65536 to the nearest whole number (halves up), f = 0 with chance T / 65536 and
+ * 65536 / (65536 - T) otherwise (T = 0: 1).  A dropped element and its
+ * gradients are 0 whatever g, u and dh hold.  What is dropped depends on rng
+ * int64 [2] (device; {seed, offset}) and on the element's place alone: both
+ * directions form it anew from Philox4x32-10 (element (r, i): 16 bits number
+ * i % 8, low half of the first word first, of counter words {i / 8, r, offset
+ * low, offset high}, key {seed low, seed high}; dropped where they are below T),
+ * and a captured graph follows rng.  A program gives every call of a step its
+ * own offset.  rng may be NULL where T = 0.  Computed in FP32, rounded once.
+ * dgu may be gu.  Limits: 0 <= p < 1 - 2^-17 (MOE_ERR_INVALID_ARG); I <=
+ * 2^31 - 1024, R * ceil(I / 8) < 2^32 (MOE_ERR_UNSUPPORTED); rng 8-byte
+ * aligned; rows of I % 8 == 0 elements in 16-byte aligned tensors go fastest. */
+moe_status_t moe_swiglu_dropout(const void *gu, int32_t dt, int32_t R, int32_t I, double p, const int64_t *rng, void *h,
+                                void *stream);
+moe_status_t moe_swiglu_dropout_bwd(const void *dh, const void *gu, int32_t dt, int32_t R, int32_t I, double p,
+                                    const int64_t *rng, void *dgu, void *stream);
+
+/* The grouped product of few rows per expert with 4-bit AWQ weights: rows of a
+ * token or a decode batch, or of a shared expert (E = 1).
+ *   y[r][n] = sum_k x[r][k] (q[e][n][k] - zero) scale   for the rows r of e
+ *   x [R][K] of dt (MOE_BF16 or MOE_FP16), w MOE_W_AWQ4 with N, K and E;
+ *   offsets, rows, padding and dev_status as moe_grouped_mm; y [R][N] of dt or
+ *   MOE_FP32.
+ * Codes less their zero and their products with x are exact, each group of 128
+ * is one FP32 sum of the tensor cores, times its scale in FP32, and the groups
+ * are added in FP32; y is rounded once.  The same call gives the same bits.
+ * Every further 32 rows of an expert read its weights again (from the L2 where
+ * they fit): for many rows use moe_ffn_grouped or 16-bit weights.
+ * R = 0 is a no-op.  Limits: E <= 1024, R, N, K and E (R / 8 + 1) <= 2^31 -
+ * 1024 (MOE_ERR_UNSUPPORTED); x, y and w's tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */
+moe_status_t moe_grouped_mm_awq(const void *x, int32_t dt, const moe_weights_t *w, const int32_t *offsets, int32_t R,
+                                void *y, int32_t ydt, int32_t *dev_status, void *stream);
 
 /* ------------------------------------------------- microscaled 4-bit floats
  * No counterpart on the pages (their NVFP4 weights are paired-sparse): dense

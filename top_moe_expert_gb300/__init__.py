@@ -29,6 +29,7 @@ MOE_W_MXFP8, MOE_W_AWQ4, MOE_W_NVFP4S = 0, 1, 3
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
 MOE_PATH_DECODE, MOE_PATH_GROUPED = 0, 1
 MOE_FP4_NVFP4, MOE_FP4_MXFP4 = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 _DT = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 
@@ -82,6 +83,11 @@ _PROTOS = {
     "moe_grouped_mm": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P]),
     "moe_grouped_mm_dgrad": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P]),
     "moe_grouped_mm_wgrad": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _P, _I32, _I32, _P, _P]),
+    "moe_route": (_I32, [_P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P, _P, _P]),
+    "moe_route_bwd": (_I32, [_P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P]),
+    "moe_swiglu_dropout": (_I32, [_P, _I32, _I32, _I32, ctypes.c_double, _P, _P, _P]),
+    "moe_swiglu_dropout_bwd": (_I32, [_P, _P, _I32, _I32, _I32, ctypes.c_double, _P, _P, _P]),
+    "moe_grouped_mm_awq": (_I32, [_P, _I32, ctypes.POINTER(moe_weights_t), _P, _I32, _P, _I32, _P, _P]),
     "moe_fp4_scale_cols": (_I32, [_I32, _I32, _P]),
     "moe_fp4_quantize": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _I64, _P, _P, _P]),
     "moe_fp4_dequantize": (_I32, [_P, _P, _I64, _I32, _I32, _P, _I64, _P, _I32, _P]),
@@ -787,6 +793,126 @@ def moe_grouped_mm_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     _launch(gpu, "moe_grouped_mm_wgrad", dy.data_ptr(), x.data_ptr(), _DT[dt], offsets.data_ptr(), R, E, N, K,
             dw.data_ptr(), _DT[dw.dtype], 1 if accumulate else 0, _status(dev_status, dev), _on(stream, gpu, dev))
     return dw
+
+
+def moe_grouped_mm_awq(x: torch.Tensor, w: Weights, offsets: torch.Tensor, out_dtype=None, y=None, dev_status=None,
+                       stream=None):
+    """y [R, N]: moe_grouped_mm with 4-bit AWQ weights, for few rows per expert:
+    x [R, K] bf16 or fp16, w of E experts (offsets [0, R] with E = 1: the dense
+    product).  out_dtype: x's type (default) or float32."""
+    if not isinstance(w, Weights) or w.fmt != MOE_W_AWQ4:
+        raise ValueError("w must be AWQ4 Weights")
+    _arg(x, "x", _DT16, 2)
+    gpu, dev, dt = x.get_device(), x.device, x.dtype
+    _arg(offsets, "offsets", _IDS, 1, dev)
+    w.on("w", dev)
+    (R, k), E = x.shape, _experts(offsets)
+    if w.E != E or w.K != k:
+        raise ValueError(f"w is [{w.E}, {w.N}, {w.K}]; offsets are for {E} experts and x has K = {k}")
+    if (R | E | w.N | k) >> 31:
+        _too_long(R, E, w.N, k)
+    y = _result(y, "y", (R, w.N), out_dtype or dt, (dt, torch.float32), dev, stream)
+    _launch(gpu, "moe_grouped_mm_awq", x.data_ptr(), _DT[dt], w.c_struct(), offsets.data_ptr(), R, y.data_ptr(),
+            _DT[y.dtype], _status(dev_status, dev), _on(stream, gpu, dev))
+    return y
+
+
+# ---------------------------------------------------------------- general routing, activation with dropout
+
+_SCORES = (MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID)
+
+
+def _route_how(k, E, score, scale) -> None:
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score}")
+    if not 0 < k <= E:
+        raise ValueError(f"k = {k} is not in 1 .. E = {E}")
+    if not 0.0 < scale < math.inf:
+        raise ValueError(f"scale must be finite and positive, not {scale}")
+
+
+def moe_route(logits: torch.Tensor, k: int, score: int = MOE_SCORE_SOFTMAX, bias=None, groups: int = 1,
+              topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0, topk_ids=None,
+              topk_w=None, load=None, stream=None):
+    """(topk_ids int32 [M, k], topk_w float32 [M, k]) of logits [M, E] (fp32, bf16
+    or fp16): experts by score + bias (float32 [E]; by logit without one) from the
+    topk_groups best of `groups` groups, each worth its group_top (1 or 2) best
+    values; weights scale * score, over their sum with renorm.  load int32 [E] is
+    increased by each expert's slots.  ragged.route has the gradient."""
+    M, E = _arg(logits, "logits", _DT, 2)
+    gpu, dev = logits.get_device(), logits.device
+    _route_how(k, E, score, scale)
+    if not 1 <= groups <= E or E % groups or not 1 <= topk_groups <= groups or group_top not in (1, 2):
+        raise ValueError(f"groups = {groups}, topk_groups = {topk_groups}, group_top = {group_top} do not fit E = {E}")
+    if k > topk_groups * (E // groups):
+        raise ValueError(f"k = {k} of {topk_groups} groups of {E // groups}")
+    if (M * k) >> 31:
+        _too_long(M, k)
+    _opt(bias, "bias", dtypes=_F32, shape=(E,), device=dev)
+    _opt(load, "load", dtypes=_IDS, shape=(E,), device=dev)
+    ids = _result(topk_ids, "topk_ids", (M, k), torch.int32, _IDS, dev, stream)
+    w = _result(topk_w, "topk_w", (M, k), torch.float32, _F32, dev, stream)
+    _launch(gpu, "moe_route", logits.data_ptr(), _DT[logits.dtype], _ptr(bias), M, E, k, score, groups, topk_groups,
+            group_top, 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(), _ptr(load), _on(stream, gpu, dev))
+    return ids, w
+
+
+def moe_route_bwd(dw: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, score: int = MOE_SCORE_SOFTMAX,
+                  renorm: bool = True, scale: float = 1.0, dlogits=None, stream=None):
+    """dlogits [M, E], of logits' type: the gradient of moe_route's logits from
+    that of its weights, dw float32 [M, k], at the ids it gave."""
+    M, E = _arg(logits, "logits", _DT, 2)
+    gpu, dev = logits.get_device(), logits.device
+    m, k = _arg(topk_ids, "topk_ids", _IDS, 2, dev)
+    if m != M:
+        raise ValueError(f"topk_ids is for {m} tokens, logits for {M}")
+    _route_how(k, E, score, scale)
+    if _arg(dw, "dw", _F32, 2, dev) != (M, k):
+        raise ValueError(f"dw has shape {tuple(dw.shape)}; expected {(M, k)}")
+    if (M * k) >> 31:
+        _too_long(M, k)
+    dl = _result(dlogits, "dlogits", (M, E), logits.dtype, (logits.dtype,), dev, stream)
+    _launch(gpu, "moe_route_bwd", dw.data_ptr(), logits.data_ptr(), _DT[logits.dtype], topk_ids.data_ptr(), M, E, k,
+            score, 1 if renorm else 0, scale, dl.data_ptr(), _on(stream, gpu, dev))
+    return dl
+
+
+def _swiglu_args(gu, p, rng):
+    R, cols = _arg(gu, "gu", _DT, 2)
+    if cols < 2 or cols % 2:
+        raise ValueError(f"gu must be [R, 2 I], not {tuple(gu.shape)}")
+    if (R | cols // 2) >> 31:
+        _too_long(R, cols // 2)
+    if not 0.0 <= p < 1.0 - 2.0 ** -17:
+        raise ValueError(f"p = {p} is not in [0, 1 - 2^-17)")
+    if rng is not None:
+        _need(rng, "rng", (torch.int64,), (2,), device=gu.device)
+    elif p >= 2.0 ** -17:
+        raise ValueError("dropout needs rng, int64 [2]: seed and offset")
+    return R, cols // 2, gu.get_device(), gu.device
+
+
+def moe_swiglu_dropout(gu: torch.Tensor, p: float = 0.0, rng=None, h=None, stream=None):
+    """h [R, I] of gu [R, 2 I] = [g | u] (fp32, bf16 or fp16): silu(g) u, dropped
+    with chance p (in steps of 2^-16) and divided by what is kept of 1.  rng int64
+    [2] on the GPU: {seed, offset}; each call of a step takes its own offset."""
+    R, I, gpu, dev = _swiglu_args(gu, p, rng)
+    h = _result(h, "h", (R, I), gu.dtype, (gu.dtype,), dev, stream)
+    _launch(gpu, "moe_swiglu_dropout", gu.data_ptr(), _DT[gu.dtype], R, I, p, _ptr(rng), h.data_ptr(),
+            _on(stream, gpu, dev))
+    return h
+
+
+def moe_swiglu_dropout_bwd(dh: torch.Tensor, gu: torch.Tensor, p: float = 0.0, rng=None, dgu=None, stream=None):
+    """dgu [R, 2 I], the gradient of moe_swiglu_dropout's gu from dh [R, I], with
+    the p and rng of that call.  dgu may be gu."""
+    R, I, gpu, dev = _swiglu_args(gu, p, rng)
+    if _arg(dh, "dh", (gu.dtype,), 2, dev) != (R, I):
+        raise ValueError(f"dh has shape {tuple(dh.shape)}; expected {(R, I)}")
+    dgu = _result(dgu, "dgu", (R, 2 * I), gu.dtype, (gu.dtype,), dev, stream)
+    _launch(gpu, "moe_swiglu_dropout_bwd", dh.data_ptr(), gu.data_ptr(), _DT[gu.dtype], R, I, p, _ptr(rng),
+            dgu.data_ptr(), _on(stream, gpu, dev))
+    return dgu
 
 
 # ---------------------------------------------------------------- microscaled 4-bit floats

@@ -10,9 +10,10 @@ Routes are ordered by expert (moe_align_block_size with blocks of one row, no
 padding between groups), the experts' products run on the groups as they are
 (moe_grouped_mm, its gradients, moe_grouped_mm_fp4), and each token sums its
 slots in slot order.  Routes to experts outside [0, E) contribute nothing.
-moe_topk_softmax has no gradient; a router is trained through weights formed
-from its choice, w = logits.gather(1, ids.long()).softmax(-1) (the same values).
-Gathers, SwiGLU and the sum over slots are torch operations.
+moe_topk_softmax has no gradient; a router is trained through route (moe_route
+with its gradient) or through weights formed from the choice, w =
+logits.gather(1, ids.long()).softmax(-1) (the same values).  Gathers, SwiGLU
+without dropout and the sum over slots are torch operations.
 """
 from __future__ import annotations
 
@@ -126,6 +127,53 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, dev_
     return _GroupedLinear.apply(x, w, offsets, dev_status)
 
 
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, how, choice):
+        ids, w = moe.moe_route(logits, k, **how, **choice)
+        ctx.save_for_backward(logits, ids)
+        ctx.how = how
+        ctx.mark_non_differentiable(ids)
+        return ids, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, dw):
+        logits, ids = ctx.saved_tensors
+        return moe.moe_route_bwd(dw.contiguous(), logits, ids, **ctx.how), None, None, None
+
+
+def route(logits: torch.Tensor, k: int, score: int = moe.MOE_SCORE_SOFTMAX, bias=None, groups: int = 1,
+          topk_groups: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0, load=None):
+    """moe_route with the gradient of logits from that of the weights: (ids, w).
+    To capture the backward pass, as for grouped_linear."""
+    (logits,), kept = _guarded(logits)
+    return _Route.apply(logits, k, dict(score=score, renorm=renorm, scale=scale),
+                        dict(bias=bias, groups=groups, topk_groups=topk_groups, group_top=group_top, load=load))
+
+
+class _SwigluDropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gu, p, rng):
+        rng = None if rng is None else rng.clone()                   # a program may move it on before the backward pass
+        ctx.save_for_backward(gu, rng)
+        ctx.p = p
+        return moe.moe_swiglu_dropout(gu, p, rng)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        gu, rng = ctx.saved_tensors
+        return moe.moe_swiglu_dropout_bwd(dh.contiguous(), gu, ctx.p, rng), None, None
+
+
+def swiglu_dropout(gu: torch.Tensor, p: float = 0.0, rng: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_swiglu_dropout with the gradient of gu.  To capture the backward pass,
+    as for grouped_linear."""
+    (gu,), kept = _guarded(gu)
+    return _SwigluDropout.apply(gu, p, rng)
+
+
 def _swiglu(h: torch.Tensor) -> torch.Tensor:
     g, u = h.float().chunk(2, dim=-1)
     return torch.nn.functional.silu(g) * u
@@ -141,14 +189,18 @@ def _combine(rows: torch.Tensor, groups: Groups, weights: torch.Tensor) -> torch
 
 
 def expert_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
-                 w2: torch.Tensor, dev_status=None) -> torch.Tensor:
+                 w2: torch.Tensor, dev_status=None, dropout: float = 0.0, rng: torch.Tensor | None = None) -> torch.Tensor:
     """y [M, d] (fp32): sum_j w_j W2_e (SiLU(Wg_e x) * Wu_e x), differentiable in
     x [M, d], topk_w [M, k], w13 [E, 2I, d] and w2 [E, d, I] (one of bf16 and
     fp16; h is rounded to it).  dev_status int32 [2]: invalid routes are counted
-    in the first, a device error of either pass is left in the second."""
+    in the first, a device error of either pass is left in the second.  dropout:
+    the chance that an element of h is dropped, by rng int64 [2] ({seed, offset}
+    on the GPU, as moe_swiglu_dropout takes it) and its route's place among the
+    rows in expert order."""
     groups = group_routes(topk_ids, w13.shape[0], dev_status)
     (rows, weights, w13, w2), kept = _guarded(x[groups.token], _weights(topk_w, groups), w13, w2)
-    h = _swiglu(_GroupedLinear.apply(rows, w13, groups.offsets, dev_status)).to(x.dtype)
+    h = _GroupedLinear.apply(rows, w13, groups.offsets, dev_status)
+    h = _SwigluDropout.apply(h, dropout, rng) if dropout else _swiglu(h).to(x.dtype)
     return _combine(_GroupedLinear.apply(h, w2, groups.offsets, dev_status), groups, weights)
 
 
