@@ -577,8 +577,8 @@ moe_status_t moe_swiglu_dropout_bwd(const void *dh, const void *gu, int32_t dt, 
  * are added in FP32; y is rounded once.  The same call gives the same bits.
  * Every further 32 rows of an expert read its weights again (from the L2 where
  * they fit): for many rows use moe_ffn_grouped or 16-bit weights.
- * R = 0 is a no-op.  Limits: E <= 1024, R, N, K and E (R / 8 + 1) <= 2^31 -
- * 1024 (MOE_ERR_UNSUPPORTED); x, y and w's tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */
+ * R = 0 is a no-op.  Limits: E <= 1024, R, N and E (R / 8 + 1) <= 2^31 - 1024,
+ * K <= 2^24 (MOE_ERR_UNSUPPORTED); x, y and w's tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */
 moe_status_t moe_grouped_mm_awq(const void *x, int32_t dt, const moe_weights_t *w, const int32_t *offsets, int32_t R,
                                 void *y, int32_t ydt, int32_t *dev_status, void *stream);
 

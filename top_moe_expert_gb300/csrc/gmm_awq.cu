@@ -14,8 +14,10 @@
 // a row's four takes 16 bytes of codes, k = 32 t .. 32 t + 31, and of each word of
 // 8 the pairs (0, 4), (1, 5), (2, 6), (3, 7), which one AND and OR turn into two
 // numbers 1024 + q (fp16) or 128 + q (bf16).
+#include <atomic>
 #include <type_traits>
 
+#include "attr.h"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "ragged.cuh"
@@ -23,7 +25,7 @@
 namespace moe {
 namespace gmm_awq {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32, kRowsW = 16;
+constexpr int kMaxK = 1 << 24, kDepth = 3;
 
 struct Args {
     const void *x;
@@ -34,14 +36,15 @@ struct Args {
     void *y;
     int32_t *dev_status;
     int R, E, N, K;
+    bool y32;
 };
 
 __device__ __forceinline__ int clamp_off(const Args &a, int e) { return min(max(a.off[e], 0), a.R); }
 
 // The slot-th run of at most `most` rows of one expert, found by one warp: expert
-// (-1: there is none), first row, rows.
+// (-1: there is none), first row, rows; and how many such runs there are.
 struct Run {
-    int e, r0, n;
+    int e, r0, n, runs;
 };
 
 __device__ __forceinline__ Run find_run(const Args &a, int slot, int most, int lane)
@@ -57,7 +60,7 @@ __device__ __forceinline__ Run find_run(const Args &a, int slot, int most, int l
         if (lane >= o)
             run += v;
     }
-    Run f{-1, 0, 0};
+    Run f{-1, 0, 0, __shfl_sync(0xffffffffu, run, 31)};
     const unsigned past = __ballot_sync(0xffffffffu, run > slot);
     if (past == 0)
         return f;
@@ -100,54 +103,178 @@ struct Zero;
 
 template <>
 struct Zero<__half> {
-    __half2 low, high;                       // 1024 + z, and -(64 + z) for the codes in the upper nibbles
-    __device__ __forceinline__ explicit Zero(uint32_t z)
+    uint32_t low, high;                      // 1024 + z, and -(64 + z) for the codes in the upper nibbles
+    __device__ __forceinline__ explicit Zero(uint32_t z) : low(0x64006400u | z | z << 16)
     {
-        low = __half2half2(__ushort_as_half(static_cast<uint16_t>(0x6400u | z)));
-        high = __half2half2(__float2half_rn(-64.f - static_cast<float>(z)));
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(high) : "r"(0x63806380u), "r"(low));                    // 960 - 1024 - z
     }
     __device__ __forceinline__ void widen(uint32_t w, uint32_t (&p)[4]) const
     {
-        const __half2 r16 = __half2half2(__ushort_as_half(0x2C00u));           // 1 / 16
 #pragma unroll
         for (int i = 0; i < 2; ++i, w >>= 8) {
             const uint32_t lo = (w & 0x000F000Fu) | 0x64006400u, hi = (w & 0x00F000F0u) | 0x64006400u;
-            const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), low);
-            const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&hi), r16, high);   // 64 + q - 64 - z
-            p[2 * i] = *reinterpret_cast<const uint32_t *>(&a);
-            p[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&b);
+            asm("sub.f16x2 %0, %1, %2;" : "=r"(p[2 * i]) : "r"(lo), "r"(low));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(p[2 * i + 1]) : "r"(hi), "r"(0x2C002C00u), "r"(high));   // / 16 - 64 - z
         }
     }
 };
 
 template <>
 struct Zero<__nv_bfloat16> {
-    __nv_bfloat162 low;                      // 128 + z
-    __device__ __forceinline__ explicit Zero(uint32_t z)
-    {
-        low = __bfloat162bfloat162(__ushort_as_bfloat16(static_cast<uint16_t>(0x4300u | z)));
-    }
+    uint32_t low;                            // -(128 + z)
+    __device__ __forceinline__ explicit Zero(uint32_t z) : low(0xC300C300u | z | z << 16) {}
     __device__ __forceinline__ void widen(uint32_t w, uint32_t (&p)[4]) const
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i, w >>= 4) {
             const uint32_t v = (w & 0x000F000Fu) | 0x43004300u;
-            const __nv_bfloat162 a = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), low);
-            p[i] = *reinterpret_cast<const uint32_t *>(&a);
+            asm("add.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(v), "r"(low));
         }
     }
 };
 
-template <typename T, typename OT, int NT>
-__global__ void __launch_bounds__(kThreads) gmm_awq_kernel(const Args a)
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src)
 {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A stage of a warp's ring: 16 MT rows of w by a group of 128, 64 bytes each; the
+// words that hold the rows' scales; the words of zeros of every 8 rows.
+template <int MT>
+constexpr int kStage = MT * 1024 + 16 * MT * 4 + 16;
+
+// The loads of a warp's part of w: the groups k0 .. k1 - 1 of the rows from n0 on, a
+// stage at a time.  Rows past N are left out: what their places hold reaches only
+// their own sums, which are not stored.
+template <int MT, int D>
+struct Loader {
+    uint32_t ring;
+    const uint8_t *q, *scale;
+    const uint32_t *zero;
+    int64_t eight;                                     // bytes to the rows 8 further
+    int blocks, left, odd, put;
+    __device__ __forceinline__ Loader(const Args &a, uint32_t at, int e, int n0, int k0, int k1, int lane)
+    {
+        const int G = a.K / 128;
+        const int64_t row = static_cast<int64_t>(e) * a.N + n0, first = (row + lane) * G + k0;
+        ring = at;
+        q = reinterpret_cast<const uint8_t *>(a.q) + (row + (lane >> 2)) * (a.K / 2) + (lane & 3) * 16 + k0 * 64;
+        eight = static_cast<int64_t>(a.K) * 4;
+        odd = static_cast<int>(first & 1);             // a scale is half of an aligned word
+        scale = reinterpret_cast<const uint8_t *>(a.scale) + (first - odd) * 2;
+        zero = a.zero + ((row >> 3) + lane) * G + k0;
+        blocks = min((a.N - n0) / 8, 2 * MT);
+        left = k1 - k0;
+        put = 0;
+    }
+    __device__ __forceinline__ void next(int lane)
+    {
+        if (left > 0) {
+            const uint32_t at = ring + put * kStage<MT>;
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m)
+                if (m < blocks)
+                    cp16(at + m * 512 + lane * 16, q + m * eight);
+            if (lane < 8 * blocks)
+                cp4(at + MT * 1024 + lane * 4, scale);
+            if (lane < blocks)
+                cp4(at + MT * 1024 + MT * 64 + lane * 4, zero);
+            q += 64;
+            odd ^= 1;
+            scale += odd ? 0 : 4;
+            ++zero;
+            --left;
+            put = put + 1 == D ? 0 : put + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+};
+
+// One warp's sums of 16 MT rows of w by 8 NT rows of x over its groups.
+template <typename T, int MT, int NT, int D>
+__device__ __forceinline__ void dot(const Args &a, const Run &f, Loader<MT, D> &load, const uint8_t *ring, int k0, int k1, int lane,
+                                    float (&acc)[MT][NT][4])
+{
+    const int g = lane >> 2, t = lane & 3, odd = a.K / 128 & g & 1;
+    const uint4 *x[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)                       // a lane without a row reads the last one: its column is not used
+        x[j] = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) +
+                                               static_cast<int64_t>(f.r0 + min(8 * j + g, f.n - 1)) * a.K + 32 * t) + 16 * k0;
+    int get = 0;
+    for (int k = k0; k < k1; ++k) {
+        uint4 xv[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j, x[j - 1] += 16)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                xv[j][i] = x[j][i];
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");
+        __syncwarp();
+        load.next(lane);
+        const uint8_t *st = ring + get * kStage<MT>;
+        get = get + 1 == D ? 0 : get + 1;
+        const uint8_t *meta = st + MT * 1024;
+        const int shift = ((odd ^ k) & 1) << 4;         // the scale's half of its word: rows of odd K / 128 alternate
+        uint4 w[2 * MT];
+        float s[2 * MT];
+        uint32_t z[2 * MT];
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) {
+            w[m] = *reinterpret_cast<const uint4 *>(st + m * 512 + lane * 16);
+            s[m] = __half2float(__ushort_as_half(static_cast<uint16_t>(*reinterpret_cast<const uint32_t *>(meta + (8 * m + g) * 4) >> shift)));
+            z[m] = *reinterpret_cast<const uint32_t *>(meta + MT * 64 + m * 4) >> (4 * g) & 15u;
+        }
+        float sum[MT][NT][4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[2 * MT][4];
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m)
+                Zero<T>(z[m]).widen(i == 0 ? w[m].x : i == 1 ? w[m].y : i == 2 ? w[m].z : w[m].w, p[m]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint4 v = xv[j][i];
+                const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);
+                const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    mma<T>(sum[m][j], p[2 * m][0], p[2 * m + 1][0], p[2 * m][1], p[2 * m + 1][1], b0, b1);
+                    mma<T>(sum[m][j], p[2 * m][2], p[2 * m + 1][2], p[2 * m][3], p[2 * m + 1][3], b2, b3);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[m][j][c] = fmaf(sum[m][j][c], s[2 * m + (c >> 1)], acc[m][j][c]);
+    }
+}
+
+// W warps divide K; a CTA takes 16 MT rows of w and a run of up to 8 NT rows of x.
+template <typename T, int W, int MT, int NT>
+__global__ void __launch_bounds__(32 * W, 16 / W) gmm_awq_kernel(const Args a)
+{
+    constexpr int kThreads = 32 * W, kRowsW = 16 * MT, D = kDepth;
     __shared__ Run s_run;
-    __shared__ float part[kWarps][8 * NT][kRowsW + 1];
+    __shared__ float part[W][8 * NT][kRowsW + 1];
+    extern __shared__ __align__(16) uint8_t rings[];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const uint8_t *ring = rings + warp * D * kStage<MT>;
     const int n0 = blockIdx.x * kRowsW, G = a.K / 128;
-    for (int slot = blockIdx.y;; slot += gridDim.y) {
+    const int k0 = G * warp / W, k1 = G * (warp + 1) / W;
+    const int first = clamp_off(a, 0), last = clamp_off(a, a.E), outside = first + a.R - last;
+    for (int slot = blockIdx.y, runs = slot + 1; slot < runs; slot += gridDim.y) {
         if (warp == 0) {
             const Run f = find_run(a, slot, 8 * NT, lane);
             if (lane == 0)
@@ -155,91 +282,88 @@ __global__ void __launch_bounds__(kThreads) gmm_awq_kernel(const Args a)
         }
         __syncthreads();
         const Run f = s_run;
+        runs = f.runs;                                                   // the grid has as many where offsets are in order
         if (f.e < 0)
             break;
-        const bool second = n0 + 8 < a.N;                       // N is a multiple of 8: the tile's lower half may be past it
-        const int64_t row0 = static_cast<int64_t>(f.e) * a.N + n0 + g, row1 = second ? row0 + 8 : row0;
-        const uint4 *q0 = reinterpret_cast<const uint4 *>(a.q + row0 * (a.K / 8)) + t;
-        const uint4 *q1 = reinterpret_cast<const uint4 *>(a.q + row1 * (a.K / 8)) + t;
-        const __half *s0 = a.scale + row0 * G, *s1 = a.scale + row1 * G;
-        const uint32_t *z0 = a.zero + (row0 >> 3) * G, *z1 = a.zero + (row1 >> 3) * G;
-        const int nt = (f.n + 7) / 8;
-        const T *x = static_cast<const T *>(a.x) + static_cast<int64_t>(f.r0 + g) * a.K + 32 * t;
-        float acc[NT][4] = {};
-        const int k0 = static_cast<int>(static_cast<int64_t>(G) * warp / kWarps);
-        const int k1 = static_cast<int>(static_cast<int64_t>(G) * (warp + 1) / kWarps);
-#pragma unroll 2
-        for (int k = k0; k < k1; ++k) {
-            const uint4 w0 = fp4::ld_once_u4(q0 + 4 * k), w1 = fp4::ld_once_u4(q1 + 4 * k);
-            const float f0 = __half2float(s0[k]), f1 = __half2float(s1[k]);
-            const Zero<T> c0(z0[k] >> (4 * g) & 15u), c1(z1[k] >> (4 * g) & 15u);
-            float sum[NT][4] = {};
-            const uint32_t v0[4] = {w0.x, w0.y, w0.z, w0.w}, v1[4] = {w1.x, w1.y, w1.z, w1.w};
+        Loader<MT, D> load(a, static_cast<uint32_t>(__cvta_generic_to_shared(ring)), f.e, n0, k0, k1, lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t p0[4], p1[4];
-                c0.widen(v0[i], p0);
-                c1.widen(v1[i], p1);
+        for (int i = 0; i < D - 1; ++i)
+            load.next(lane);
+        float (*mine)[kRowsW + 1] = part[warp];
+        if (NT == 1 || f.n <= 8) {
+            float acc[MT][1][4] = {};
+            dot<T, MT, 1, D>(a, f, load, ring, k0, k1, lane, acc);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if (j < nt) {
-                        uint4 xv = make_uint4(0, 0, 0, 0);
-                        if (8 * j + g < f.n)
-                            xv = *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(8 * j) * a.K + 128 * k + 8 * i);
-                        mma<T>(sum[j], p0[0], p1[0], p0[1], p1[1], __byte_perm(xv.x, xv.z, 0x5410), __byte_perm(xv.x, xv.z, 0x7632));
-                        mma<T>(sum[j], p0[2], p1[2], p0[3], p1[3], __byte_perm(xv.y, xv.w, 0x5410), __byte_perm(xv.y, xv.w, 0x7632));
-                    }
-                }
-            }
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                acc[j][0] = fmaf(sum[j][0], f0, acc[j][0]);
-                acc[j][1] = fmaf(sum[j][1], f0, acc[j][1]);
-                acc[j][2] = fmaf(sum[j][2], f1, acc[j][2]);
-                acc[j][3] = fmaf(sum[j][3], f1, acc[j][3]);
-            }
-        }
+                for (int c = 0; c < 4; ++c)
+                    mine[2 * t + (c & 1)][16 * m + g + 8 * (c >> 1)] = acc[m][0][c];
+        } else {
+            float acc[MT][NT][4] = {};
+            dot<T, MT, NT, D>(a, f, load, ring, k0, k1, lane, acc);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            part[warp][8 * j + 2 * t][g] = acc[j][0];
-            part[warp][8 * j + 2 * t + 1][g] = acc[j][1];
-            part[warp][8 * j + 2 * t][g + 8] = acc[j][2];
-            part[warp][8 * j + 2 * t + 1][g + 8] = acc[j][3];
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        mine[8 * j + 2 * t + (c & 1)][16 * m + g + 8 * (c >> 1)] = acc[m][j][c];
         }
         __syncthreads();
         for (int i = threadIdx.x; i < kRowsW * f.n; i += kThreads) {
             const int n = i & (kRowsW - 1), r = i / kRowsW;
             float sum = part[0][r][n];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w)
+            for (int w = 1; w < W; ++w)
                 sum += part[w][r][n];
-            if (n0 + n < a.N)
-                static_cast<OT *>(a.y)[static_cast<int64_t>(f.r0 + r) * a.N + n0 + n] = fp4::from_float<OT>(sum);
+            if (n0 + n < a.N) {
+                const int64_t o = static_cast<int64_t>(f.r0 + r) * a.N + n0 + n;
+                if (a.y32)
+                    static_cast<float *>(a.y)[o] = sum;
+                else
+                    static_cast<T *>(a.y)[o] = fp4::from_float<T>(sum);
+            }
         }
         __syncthreads();
     }
     // rows outside every group, divided among the CTAs of a column of tiles
-    const int first = clamp_off(a, 0), last = clamp_off(a, a.E), outside = first + a.R - last;
     for (int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < static_cast<int64_t>(outside) * kRowsW;
          i += static_cast<int64_t>(gridDim.y) * kThreads) {
         const int n = n0 + static_cast<int>(i & (kRowsW - 1)), j = static_cast<int>(i / kRowsW), r = j < first ? j : last + j - first;
-        if (n < a.N)
-            static_cast<OT *>(a.y)[static_cast<int64_t>(r) * a.N + n] = fp4::from_float<OT>(0.f);
+        if (n < a.N) {
+            if (a.y32)
+                static_cast<float *>(a.y)[static_cast<int64_t>(r) * a.N + n] = 0.f;
+            else
+                static_cast<T *>(a.y)[static_cast<int64_t>(r) * a.N + n] = fp4::from_float<T>(0.f);
+        }
     }
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int e = threadIdx.x; e < a.E; e += kThreads)
             ragged::report_bad(a.off, a.R, e, a.dev_status);
 }
 
-template <typename T, typename OT>
+template <typename T, int W, int MT, int NT>
 static moe_status_t launch(const Args &a, cudaStream_t s)
 {
-    const int most = a.R <= 8 ? 8 : 32;
-    const int64_t live = a.E < a.R ? a.E : a.R, runs = (a.R + live * (most - 1)) / most;
-    const dim3 grid(static_cast<unsigned>((a.N + kRowsW - 1) / kRowsW), static_cast<unsigned>(runs < 65535 ? runs : 65535));
-    const cudaError_t e = most == 8 ? launch_pdl(gmm_awq_kernel<T, OT, 1>, grid, dim3(kThreads), 0, s, a)
-                                    : launch_pdl(gmm_awq_kernel<T, OT, 4>, grid, dim3(kThreads), 0, s, a);
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    constexpr int bytes = W * kDepth * kStage<MT>;
+    if (!smem_attr_once(done, reinterpret_cast<const void *>(gmm_awq_kernel<T, W, MT, NT>), bytes))
+        return MOE_ERR_CUDA;
+    const int64_t live = a.E < a.R ? a.E : a.R, most = 8 * NT, runs = (a.R + live * (most - 1)) / most;
+    const dim3 grid(static_cast<unsigned>((a.N + 16 * MT - 1) / (16 * MT)), static_cast<unsigned>(runs < 65535 ? runs : 65535));
+    return launch_pdl(gmm_awq_kernel<T, W, MT, NT>, grid, dim3(32 * W), bytes, s, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename T>
+static moe_status_t run(const Args &a, cudaStream_t s)
+{
+    const int64_t live = a.E < a.R ? a.E : a.R;
+    const bool wide = live * ((a.N + 31) / 32) >= 2 * device_sm_count();
+    if (a.K >= 4096)
+        return a.R <= 8 ? (wide ? launch<T, 4, 2, 1>(a, s) : launch<T, 4, 1, 1>(a, s))
+                        : (wide ? launch<T, 4, 2, 2>(a, s) : launch<T, 4, 1, 2>(a, s));
+    return a.R <= 8 ? (wide ? launch<T, 2, 2, 1>(a, s) : launch<T, 2, 1, 1>(a, s))
+                    : (wide ? launch<T, 2, 2, 2>(a, s) : launch<T, 2, 1, 2>(a, s));
 }
 
 }  // namespace gmm_awq
@@ -256,7 +380,7 @@ MOE_API moe_status_t moe_grouped_mm_awq(const void *x, int32_t dt, const moe_wei
         return MOE_ERR_UNSUPPORTED;
     if (w->N % 8 != 0 || w->K % 128 != 0)
         return MOE_ERR_INVALID_ARG;
-    if (w->E > ragged::kMaxExperts || R > ragged::kMaxSide || w->N > ragged::kMaxSide || w->K > ragged::kMaxSide ||
+    if (w->E > ragged::kMaxExperts || R > ragged::kMaxSide || w->N > ragged::kMaxSide || w->K > gmm_awq::kMaxK ||
         !ragged::list_fits(w->E, R, 1, 8))
         return MOE_ERR_UNSUPPORTED;
     if (R == 0)
@@ -265,9 +389,7 @@ MOE_API moe_status_t moe_grouped_mm_awq(const void *x, int32_t dt, const moe_wei
         !aligned(w->q, 16) || !aligned(w->scale, 16) || !aligned(w->zero, 16) || !aligned(dev_status, 4))
         return MOE_ERR_INVALID_ARG;
     const gmm_awq::Args a{x, static_cast<const uint32_t *>(w->q), static_cast<const __half *>(w->scale),
-                          static_cast<const uint32_t *>(w->zero), offsets, y, dev_status, R, w->E, w->N, w->K};
+                          static_cast<const uint32_t *>(w->zero), offsets, y, dev_status, R, w->E, w->N, w->K, ydt == MOE_FP32};
     cudaStream_t s = as_stream(stream);
-    if (dt == MOE_BF16)
-        return ydt == MOE_FP32 ? gmm_awq::launch<__nv_bfloat16, float>(a, s) : gmm_awq::launch<__nv_bfloat16, __nv_bfloat16>(a, s);
-    return ydt == MOE_FP32 ? gmm_awq::launch<__half, float>(a, s) : gmm_awq::launch<__half, __half>(a, s);
+    return dt == MOE_BF16 ? gmm_awq::run<__nv_bfloat16>(a, s) : gmm_awq::run<__half>(a, s);
 }
