@@ -17,6 +17,11 @@
 // A lane holds consecutive experts of one group, and a group takes a power of two
 // of neighbouring lanes, so that the lowest lane that holds a maximum also holds
 // the lowest index.
+#include <cfloat>
+#include <climits>
+#include <type_traits>
+
+#include "attr.h"
 #include "common.cuh"
 #include "fp4.cuh"
 #include "gmm_common.cuh"
@@ -26,16 +31,16 @@
 namespace moe {
 namespace route {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 16, kBwdWarps = 4;
 constexpr int kMaxExperts = ragged::kMaxExperts;
-constexpr int kMaxK = 32, kMaxGroups = 32, kMaxPer = 64;
+constexpr int kMaxK = 32, kMaxGroups = 32, kMaxPer = 64, kMaxFound = 64;
 
 struct Args {
     const void *logits;
     const float *bias;
     int M, E, k, groups, topk_groups, group_top, sigmoid, renorm;
     float scale;
-    int of_group, lanes, per;            // experts of a group, lanes of a group, experts of a lane (at most)
+    int of_group, lanes, shift, per;     // experts of a group, lanes of a group (2^shift), experts of a lane (at most)
     int32_t *ids;
     float *w;
     int32_t *load;
@@ -44,12 +49,14 @@ struct Args {
 template <typename T>
 __device__ __forceinline__ float value(T v) { return static_cast<float>(v); }
 
+// NaN and +inf are out of the choice, as -inf is.
+__device__ __forceinline__ float clean(float v) { return v < INFINITY ? v : -INFINITY; }
+
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // The two best of two pairs (a1 >= a2, b1 >= b2).
@@ -66,92 +73,17 @@ struct Place {
     int group, base, count;
     __device__ __forceinline__ Place(const Args &a, int lane)
     {
-        group = lane / a.lanes;
-        const int first = (lane - group * a.lanes) * a.per;
+        group = lane >> a.shift;
+        const int first = (lane & (a.lanes - 1)) * a.per;
         base = group * a.of_group + first;
         count = group < a.groups ? min(max(a.of_group - first, 0), a.per) : 0;
     }
 };
 
-// Whether the lane's group is among the best: its value against every other's,
-// the lower group first among equal ones.  Values of 0 experts are -inf.
-template <typename F>
-__device__ __forceinline__ bool in_best(const Args &a, int group, F v)
-{
-    int better = 0;
-    for (int g = 0; g < a.groups; ++g) {
-        const F o = __shfl_sync(0xffffffffu, v, g * a.lanes);
-        better += o > v || (o == v && g < group);
-    }
-    return group < a.groups && better < a.topk_groups;
-}
-
-// The choice of one token in binary64: lane j < k receives slot j's expert, or -1.
-template <typename T>
-__device__ __noinline__ int choose_exact(const Args &a, const T *l, int lane)
-{
-    const Place at(a, lane);
-    double v[kMaxPer];                  // what the choice goes by
-    double m = -INFINITY, z = 1.0;
-    if (!a.sigmoid) {
-        for (int i = 0; i < at.count; ++i)
-            m = fmax(m, static_cast<double>(value(l[at.base + i])));
-        for (int o = 16; o > 0; o >>= 1)
-            m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-        z = 0.0;
-        if (m > -INFINITY)
-            for (int i = 0; i < at.count; ++i)
-                z += exp(static_cast<double>(value(l[at.base + i])) - m);
-        for (int o = 16; o > 0; o >>= 1)
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-    }
-    double b1 = -INFINITY, b2 = -INFINITY;
-    for (int i = 0; i < at.count; ++i) {
-        const double x = value(l[at.base + i]);
-        double s = -INFINITY;
-        if (x > -INFINITY)
-            s = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / z;
-        v[i] = a.bias ? s + static_cast<double>(a.bias[at.base + i]) : x;
-        best_two(b1, b2, a.bias || a.group_top == 2 ? (a.bias ? v[i] : s) : x, -static_cast<double>(INFINITY));
-    }
-    bool live = at.group < a.groups;
-    if (a.groups > 1) {
-        for (int o = 1; o < a.lanes; o <<= 1) {
-            const double o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
-            best_two(b1, b2, o1, o2);
-        }
-        live = in_best(a, at.group, a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1);
-    }
-    uint64_t taken = live ? 0ull : ~0ull;
-    int slot = -1;
-    for (int j = 0; j < a.k; ++j) {
-        double bv = -INFINITY;
-        int bi = -1;
-        for (int i = 0; i < at.count; ++i)
-            if (!(taken >> i & 1) && v[i] > bv) {
-                bv = v[i];
-                bi = i;
-            }
-        double top = bv;
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const unsigned have = __ballot_sync(0xffffffffu, bi >= 0 && bv == top);
-        if (!have)
-            break;
-        const int wl = __ffs(have) - 1;
-        const int e = __shfl_sync(0xffffffffu, at.base + bi, wl);
-        if (lane == wl)
-            taken |= 1ull << bi;
-        if (lane == j)
-            slot = e;
-    }
-    return slot;
-}
-
 // The sigmoid of a logit from exp(-|l|), which does not overflow.
 __device__ __forceinline__ float sigmoid(float l)
 {
-    const float t = expf(-fabsf(l)), r = 1.0f / (1.0f + t);
+    const float t = expf(-fabsf(l)), r = __fdividef(1.0f, 1.0f + t);
     return l >= 0.f ? r : t * r;
 }
 
@@ -168,189 +100,536 @@ __device__ __forceinline__ float weight(bool sigmoid_score, bool renorm, float s
     const float top = warp_max(live ? l : -INFINITY);
     const float s = !live ? 0.f : sigmoid_score && top > -60.f ? sigmoid(l) : expf(l - top);
     const float sum = warp_sum(s);
-    return live ? s / sum * scale : 0.f;
+    return live ? __fdividef(s, sum) * scale : 0.f;         // sum is at least e^-60 / 2
 }
 
-template <typename T, int PER, bool SORT>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const Args a)
+// A token's candidates, one to a lane or two; then in their order.
+struct Slots {
+    uint64_t found[kMaxFound];                         // key64, or order64 of the exact value
+    uint64_t sorted[kMaxK + 1];
+    int expert[kMaxFound];
+};
+
+// A value and its expert as one number: larger values first, then lower experts.
+__device__ __forceinline__ uint64_t key64(float v, int e)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (t >= a.M)
-        return;
-    const T *l = static_cast<const T *>(a.logits) + static_cast<int64_t>(t) * a.E;
-    const Place at(a, lane);
-    float v[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        v[i] = i < at.count ? value(l[at.base + i]) : -INFINITY;
-    bool bad = false;                          // NaN or +inf: out of the choice, and the token's weights are NaN
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (!(v[i] < INFINITY)) {
-            bad = true;
-            v[i] = -INFINITY;
+    return static_cast<uint64_t>(topk_key(v)) << 32 | ~static_cast<uint32_t>(e);
+}
+// Comparisons of binary64 take a warp some 60 cycles, those of whole numbers 4.
+__device__ __forceinline__ uint64_t order64(double v)
+{
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return u ^ (u >> 63 ? ~0ull : 0x8000000000000000ull);
+}
+__device__ __forceinline__ double value64(uint64_t k)
+{
+    return __longlong_as_double(static_cast<long long>(k ^ (k >> 63 ? 0x8000000000000000ull : ~0ull)));
+}
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
+__device__ __forceinline__ int expert_of(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
+__device__ __forceinline__ float value_of(uint64_t k) { return topk_unkey(static_cast<uint32_t>(k >> 32)); }
+
+// The errors that the values of the choice may have in binary32.
+//   sigmoid  2^-21: exp to (2 + 1.7 |l|) ulp moves it by at most 0.7 2^-23, the sum
+//            and the reciprocal by 1.5 2^-23
+//   softmax  (20 + PER / 2) 2^-23 of the largest score 1 / z: its own 3, the sum's
+//            terms' 2 + 1.7 |x| ulp, |x| weighed by the scores at most ln E, and its
+//            additions'
+// Two values that are closer than twice that and their additions' rounding may be
+// in the other order.
+__device__ __forceinline__ float slack_of(const Args &a, float rz)
+{
+    return a.sigmoid ? 0x1p-20f : (40 + a.per) * 0x1p-23f * rz;
+}
+
+// exp(-x) / (1 + exp(-x)) as far as that error; 0 below -88.
+__device__ __forceinline__ float fast_sigmoid(float l)
+{
+    float t, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(l * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return r;
+}
+
+// The same in binary64 for one token, by one warp: what it may choose is found in
+// binary32 as the kernel does, with those errors to spare, and the values of these
+// candidates alone are formed in binary64, one to a lane (a warp's instruction takes
+// some 60 cycles).  Lane j < k receives slot j's expert, or -1.
+template <typename T>
+struct Exact {
+    const Args &a;
+    const T *l;
+    Slots &slots;
+    const Place at;
+    const int lane;
+    double m, z;                                       // of a softmax
+    float slack;
+
+    __device__ __forceinline__ Exact(const Args &args, const T *row, Slots &s, int my_lane)
+        : a(args), l(row), slots(s), at(args, my_lane), lane(my_lane), m(0.0), z(1.0)
+    {
+        if (!a.sigmoid) {
+            float top = -INFINITY;
+            for (int i = 0; i < at.count; ++i)
+                top = fmaxf(top, logit(at.base + i));
+            m = warp_max(top);
+            z = 0.0;
+            if (m > -INFINITY)
+                for (int i = 0; i < at.count; ++i)
+                    z += exp(static_cast<double>(logit(at.base + i)) - m);
+            for (int o = 16; o > 0; o >>= 1)
+                z += __shfl_xor_sync(0xffffffffu, z, o);
         }
-    // row maximum and sum
-    const bool two = a.groups > 1 && a.group_top == 2 && !a.bias;      // group values from scores, choice by logits
-    float m = -INFINITY, z = 1.f;
-    if (!a.sigmoid && (a.bias || two || !a.renorm)) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            m = fmaxf(m, v[i]);
-        m = warp_max(m);
-        z = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            z += v[i] > -INFINITY ? __expf(v[i] - m) : 0.f;
-        z = warp_sum(z);
+        slack = slack_of(a, static_cast<float>(1.0 / z));
     }
-    const float rz = 1.f / z;
-    // Largest error of a score: sigmoids 2^-21 (exp to 2 ulp where it is near 1,
-    // the quotient); of a softmax (20 + PER / 2) 2^-23 of the largest score, the
-    // sum's own error (its terms' 2 + 1.7 |x| ulp, |x| weighed by the scores at
-    // most ln E; the additions') included.  Two values closer than twice that
-    // and their additions' rounding may be in the other order.
-    const float slack = a.sigmoid ? 0x1p-20f : (40 + PER) * 0x1p-23f * rz;
-    float c[PER];
-    float b1 = -INFINITY, b2 = -INFINITY;
-    if (a.bias || two) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            float s;
-            if (a.sigmoid) {
-                const float e = __expf(-fabsf(v[i])), r = __fdividef(1.f, 1.f + e);
-                s = v[i] >= 0.f ? r : e * r;
-            } else {
-                s = __expf(v[i] - m) * rz;
-            }
-            if (!(v[i] > -INFINITY))
-                s = -INFINITY;
-            if (a.bias) {
-                float b = i < at.count ? a.bias[at.base + i] : 0.f;
-                if (!(b < INFINITY)) {
-                    bad = true;
-                    b = -INFINITY;
-                }
-                s += b;
-                c[i] = s;
-            } else {
-                c[i] = v[i];
-            }
-            best_two(b1, b2, s, -INFINITY);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            c[i] = v[i];
-            best_two(b1, b2, v[i], -INFINITY);
-        }
+    __device__ __forceinline__ float logit(int e) const { return clean(value(l[e])); }
+    __device__ __forceinline__ float bias(int e) const { return clean(a.bias[e]); }
+    __device__ __forceinline__ float near_score(int e) const
+    {
+        const float x = logit(e);
+        return !(x > -INFINITY) ? -INFINITY
+               : a.sigmoid      ? fast_sigmoid(x)
+                                : __expf(x - static_cast<float>(m)) * static_cast<float>(1.0 / z);
     }
-    bad = __any_sync(0xffffffffu, bad);
-    bool close = false;
-    bool live = at.group < a.groups;
-    if (a.groups > 1) {
+    // What a group's value is made of, and what experts are chosen by.
+    __device__ __forceinline__ float near(int e, bool of_group) const
+    {
+        if (a.bias)
+            return near_score(e) + bias(e);
+        return of_group && a.group_top == 2 ? near_score(e) : logit(e);
+    }
+    __device__ __forceinline__ double exact(int e, bool of_group) const
+    {
+        const double x = logit(e);
+        if (!a.bias && !(of_group && a.group_top == 2))
+            return x;
+        const double s = a.sigmoid ? sigmoid64(static_cast<float>(x)) : exp(x - m) / z;
+        return a.bias ? s + static_cast<double>(bias(e)) : s;
+    }
+    // All experts of the lane with a value of at least its bound as candidates;
+    // their number, which may be above what there is room for.
+    __device__ __forceinline__ int collect(bool live, float bound, bool of_group)
+    {
+        int found = 0;
+        for (int i = 0; i < a.per; ++i) {
+            const float v = live && i < at.count ? near(at.base + i, of_group) : -INFINITY;
+            const bool is = v > -INFINITY && v >= bound;
+            const unsigned lanes = __ballot_sync(0xffffffffu, is);
+            const int to = found + __popc(lanes & ((1u << lane) - 1u));
+            if (is && to < kMaxFound)
+                slots.expert[to] = at.base + i;
+            found += __popc(lanes);
+        }
+        __syncwarp();
+        for (int i = lane; i < min(found, kMaxFound); i += 32)
+            slots.found[i] = order64(exact(slots.expert[i], of_group));
+        __syncwarp();
+        return found;
+    }
+    // A bound with the values' errors to spare.
+    __device__ __forceinline__ float below(float v) const { return v - (slack + 0x1p-21f * fabsf(v)); }
+
+    __device__ __forceinline__ unsigned groups()         // a bit for each group that is in
+    {
+        if (a.groups == 1)
+            return 1u;
+        float b1 = -INFINITY, b2 = -INFINITY;
+        for (int i = 0; i < at.count; ++i)
+            best_two(b1, b2, near(at.base + i, true), -INFINITY);
         for (int o = 1; o < a.lanes; o <<= 1) {
             const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
             best_two(b1, b2, o1, o2);
         }
-        const float g = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-        live = in_best(a, at.group, g);
-        if (a.bias || two) {
-            const float in = -warp_max(live ? -g : -INFINITY), out = warp_max(live ? -INFINITY : g);
-            const float size = warp_max((b1 > -INFINITY ? fabsf(b1) : 0.f) + (b2 > -INFINITY ? fabsf(b2) : 0.f));
-            close = in - out <= 2.f * slack + 0x1p-22f * size;
+        const int found = collect(at.group < a.groups, below(a.group_top == 2 ? b2 : b1), true);
+        // lane g: group g's value, from the candidates or from all of its experts
+        uint64_t e1 = 0, e2 = 0;
+        if (lane < a.groups) {
+            if (found <= kMaxFound) {
+                const int lo = lane * a.of_group, hi = lo + a.of_group;
+                for (int i = 0; i < found; ++i)
+                    if (slots.expert[i] >= lo && slots.expert[i] < hi)
+                        best_two(e1, e2, slots.found[i], static_cast<uint64_t>(0));
+            } else {
+                for (int e = lane * a.of_group; e < (lane + 1) * a.of_group; ++e)
+                    if (near(e, true) > -INFINITY)
+                        best_two(e1, e2, order64(exact(e, true)), static_cast<uint64_t>(0));
+            }
         }
+        const uint64_t v = a.group_top == 2 && e2 ? order64(value64(e1) + value64(e2)) : e1;
+        int better = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const uint64_t o = __shfl_sync(0xffffffffu, v, g);
+            better += o > v || (o == v && g < lane);
+        }
+        return __ballot_sync(0xffffffffu, lane < a.groups && better < a.topk_groups);
     }
-    // selection: keys of the experts that are in, the rest 0
-    uint32_t key[PER];
+    __device__ __forceinline__ int choose()
+    {
+        const unsigned in = groups();                    // by all lanes, also those without a group
+        const bool live = at.group < a.groups && (in >> at.group & 1u);
+        float top = -INFINITY, last = -INFINITY;
+        for (int i = 0; live && i < at.count; ++i)
+            top = fmaxf(top, near(at.base + i, false));
+        for (int j = 0; j <= a.k; ++j) {
+            last = warp_max(top);
+            if (last == -INFINITY)
+                break;
+            top = top == last ? -INFINITY : top;
+        }
+        const int found = collect(live, a.bias && last > -INFINITY ? below(last) : last, false);
+        if (found <= kMaxFound) {
+            for (int i = lane; i < found; i += 32) {
+                int rank = 0;
+                for (int j = 0; j < found; ++j)
+                    rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && slots.expert[j] < slots.expert[i]);
+                if (rank < a.k)
+                    slots.sorted[rank] = slots.expert[i];
+            }
+            __syncwarp();
+            return lane < a.k && lane < found ? static_cast<int>(slots.sorted[lane]) : -1;
+        }
+        // that many equal values: one slot after the other, over all experts
+        uint64_t taken = live ? 0ull : ~0ull;
+        int slot = -1;
+        for (int j = 0; j < a.k; ++j) {
+            uint64_t best = 0;
+            int at_best = -1;
+            for (int i = 0; i < at.count; ++i)
+                if (!(taken >> i & 1) && near(at.base + i, false) > -INFINITY) {
+                    const uint64_t v = order64(exact(at.base + i, false));
+                    if (v > best) {
+                        best = v;
+                        at_best = i;
+                    }
+                }
+            uint64_t first = best;
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint64_t n = __shfl_xor_sync(0xffffffffu, first, o);
+                first = n > first ? n : first;
+            }
+            const unsigned have = __ballot_sync(0xffffffffu, at_best >= 0 && best == first);
+            if (!have)
+                break;
+            const int wl = __ffs(have) - 1;
+            const int e = __shfl_sync(0xffffffffu, at.base + at_best, wl);
+            if (lane == wl)
+                taken |= 1ull << at_best;
+            if (lane == j)
+                slot = e;
+        }
+        return slot;
+    }
+};
+
+// A token's ids and weights, and its part of the load.
+__device__ __forceinline__ void put(const Args &a, uint32_t t, int slot, float w, bool bad, int lane, int *load)
+{
+    if (lane < a.k) {
+        a.ids[static_cast<int64_t>(t) * a.k + lane] = slot;
+        a.w[static_cast<int64_t>(t) * a.k + lane] = bad ? __uint_as_float(0x7FC00000u) : w;
+        if (a.load && slot >= 0)
+            atomicAdd(load + slot, 1);
+    }
+}
+
+// All of a token by the exact choice.
+template <typename T>
+__device__ __noinline__ void route_exact(const Args &a, uint32_t t, Slots &slots, int *load, int lane)
+{
+    const T *l = static_cast<const T *>(a.logits) + static_cast<int64_t>(t) * a.E;
+    bool bad = false;
+    for (int e = lane; e < a.E; e += 32)
+        bad |= !(value(l[e]) < INFINITY) || (a.bias && !(a.bias[e] < INFINITY));
+    bad = __any_sync(0xffffffffu, bad);
+    Exact<T> exact(a, l, slots, lane);
+    const int slot = exact.choose();
+    const float my_l = slot >= 0 ? value(l[slot]) : 0.f;
+    put(a, t, slot, weight(a.sigmoid, a.renorm, a.scale, my_l, slot >= 0, static_cast<float>(exact.m), static_cast<float>(exact.z)), bad,
+        lane, load);
+    __syncwarp();
+}
+
+// Consecutive elements of a row: 16 bytes at a time where FULL says that every
+// lane has PER of them, on their natural alignment.
+template <typename T, int PER, bool FULL>
+__device__ __forceinline__ void load_row(const T *p, int count, float (&v)[PER])
+{
+    constexpr int kWords = PER * static_cast<int>(sizeof(T)) / 4;
+    if constexpr (FULL && kWords >= 1) {
+        uint32_t w[kWords];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        key[i] = live && c[i] > -INFINITY ? topk_key(c[i]) : 0u;
-    int idx[PER];
-    uint64_t taken = 0;
-    if constexpr (SORT) {
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (kWords % 4 == 0) {
+                if (i % 4 == 0) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(p) + i);
+                    w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+                }
+            } else if constexpr (kWords == 2) {
+                if (i == 0) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                    w[0] = x.x, w[1] = x.y;
+                }
+            } else {
+                w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = __uint_as_float(w[i]);
+            } else {
+                float lo, hi;
+                if constexpr (std::is_same<T, __half>::value)
+                    f16x2_to_float(w[i / 2], lo, hi);
+                else
+                    bf16x2_to_float(w[i / 2], lo, hi);
+                v[i] = i % 2 ? hi : lo;
+            }
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            idx[i] = i;
-#pragma unroll
-        for (int i = 1; i < PER; ++i)
-#pragma unroll
-            for (int j = i; j > 0; --j) {
-                const bool sw = key[j] > key[j - 1];
-                const uint32_t ka = key[j - 1], kb = key[j];
-                const int ia = idx[j - 1], ib = idx[j];
-                key[j - 1] = sw ? kb : ka;
-                key[j] = sw ? ka : kb;
-                idx[j - 1] = sw ? ib : ia;
-                idx[j] = sw ? ia : ib;
-            }
+            v[i] = i < count ? value(p[i]) : -INFINITY;
     }
-    int slot = -1, next = -1;
-    float mine = -INFINITY, after = -INFINITY;
+}
+
+// Warps go over the tokens.  Of a token, each lane finds its best value; the
+// (k + 1)-th best of those bounds what can be chosen, usually some ten values,
+// which the lanes then take one each and rank.  Tokens that binary32 cannot decide
+// are marked, and done at the end, so that their code is out of this loop.
+constexpr int kLater = INT_MIN;
+
+template <typename T, int PER, bool FULL>
+__global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(const Args a)
+{
+    __shared__ Slots all[kWarps];
+    __shared__ int load[kMaxExperts];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int lane = threadIdx.x & 31;
+    Slots &slots = all[threadIdx.x >> 5];
+    if (a.load) {
+        for (int e = threadIdx.x; e < a.E; e += kWarps * 32)
+            load[e] = 0;
+        __syncthreads();
+    }
+    const Place at(a, lane);
+    const bool two = a.groups > 1 && a.group_top == 2 && !a.bias;      // group values from scores, choice by logits
     const int rounds = a.bias ? a.k + 1 : a.k;
-    for (int j = 0; j < rounds; ++j) {
-        uint32_t head = 0;
-        int hi = 0;
-        if constexpr (SORT) {
-            head = key[0];
-            hi = idx[0];
+    constexpr bool kKeep = PER <= 16;                                   // the biases stay in registers
+    float b[PER];
+    if (kKeep && a.bias)
+        load_row<float, PER, FULL>(a.bias + at.base, at.count, b);
+    const uint32_t step = gridDim.x * kWarps, begin = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    bool later = false;
+
+    for (uint32_t t = begin; t < static_cast<uint32_t>(a.M); t += step) {
+        const T *l = static_cast<const T *>(a.logits) + static_cast<int64_t>(t) * a.E;
+        float v[PER], c[PER];
+        load_row<T, PER, FULL>(l + at.base, at.count, v);
+        bool bad = false, finite = FULL;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            finite = finite && fabsf(v[i]) < INFINITY;
+        if (!__all_sync(0xffffffffu, finite)) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (!(v[i] < INFINITY)) {              // the token's weights will be NaN
+                    bad = true;
+                    v[i] = -INFINITY;
+                }
+        }
+        // row maximum and sum
+        float m = -INFINITY, z = 1.f;
+        if (!a.sigmoid && (a.bias || two || !a.renorm)) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                m = fmaxf(m, v[i]);
+            m = warp_max(m);
+            z = 0.f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                z += v[i] > -INFINITY ? __expf(v[i] - m) : 0.f;
+            z = warp_sum(z);
+        }
+        const float rz = 1.f / z, slack = slack_of(a, rz);
+        float b1 = -INFINITY, b2 = -INFINITY;          // the lane's best, of what group values are made of
+        if (a.bias || two) {
+            if (!kKeep && a.bias)
+                load_row<float, PER, FULL>(a.bias + at.base, at.count, b);
+            bool plain = finite;
+            if (a.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    c[i] = fast_sigmoid(v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    c[i] = __expf(v[i] - m) * rz;
+            }
+            if (a.bias) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    c[i] += b[i];
+                    plain = plain && fabsf(c[i]) < INFINITY;
+                }
+            }
+            if (!__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    if (a.bias && i < at.count && !(b[i] < INFINITY))
+                        bad = true;
+                    if (!(v[i] > -INFINITY) || !(fabsf(c[i]) < INFINITY))
+                        c[i] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                b2 = fmaxf(b2, fminf(b1, c[i]));
+                b1 = fmaxf(b1, c[i]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (!(taken >> i & 1) && key[i] > head) {
-                    head = key[i];
-                    hi = i;
-                }
+                b1 = fmaxf(b1, v[i]);
         }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, head);
-        if (top == 0)
-            break;
-        const int wl = __ffs(__ballot_sync(0xffffffffu, head == top)) - 1;
-        const int e = __shfl_sync(0xffffffffu, at.base + hi, wl);
-        if (lane == wl) {
-            if constexpr (SORT) {
+        float top = b1;                                // of what experts are chosen by
+        if (!a.bias) {
+            top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i + 1 < PER; ++i) {
-                    key[i] = key[i + 1];
-                    idx[i] = idx[i + 1];
-                }
-                key[PER - 1] = 0u;
-            } else {
-                taken |= 1ull << hi;
+            for (int i = 0; i < PER; ++i) {
+                c[i] = v[i];
+                top = fmaxf(top, v[i]);
             }
         }
-        if (lane == j) {
-            slot = e;
-            mine = topk_unkey(top);
+        bool close = false;                            // in this lane's view; what follows from it is decided together
+        bool live = at.group < a.groups;
+        if (a.groups > 1) {
+            for (int o = 1; o < a.lanes; o <<= 1) {
+                const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
+                best_two(b1, b2, o1, o2);
+            }
+            const float value = live && a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : live ? b1 : -INFINITY;
+            float g = value, in = -INFINITY;
+            live = false;
+            for (int j = 0; j < a.topk_groups; ++j) {  // the best of the groups that are left
+                in = warp_max(g);
+                const bool is = g == in;
+                live = live || is;
+                g = is ? -INFINITY : g;
+            }
+            if (__popc(__ballot_sync(0xffffffffu, live)) != a.topk_groups << a.shift) {
+                // equal groups came in together, or there were none left: one by one, the first of equal ones first
+                g = value;
+                live = false;
+                for (int j = 0; j < a.topk_groups; ++j) {
+                    in = warp_max(g);
+                    const int first = __ffs(__ballot_sync(0xffffffffu, g == in)) - 1;
+                    if (in > -INFINITY && (lane ^ first) >> a.shift == 0) {
+                        live = true;
+                        g = -INFINITY;
+                    }
+                }
+            }
+            if (a.bias || two) {
+                const float out = warp_max(g), size = (b1 > -INFINITY ? fabsf(b1) : 0.f) + (b2 > -INFINITY ? fabsf(b2) : 0.f);
+                close = in - out <= 2.f * slack + 0x1p-22f * warp_max(size);
+            }
         }
-        if (lane == j - 1) {
-            next = e;
-            after = topk_unkey(top);
+        // a bound of what can be chosen: the last of the best values of as many lanes as are needed
+        float bound = -INFINITY;
+        if (!live)
+            top = -INFINITY;
+#pragma unroll 3
+        for (int j = 0; j < rounds; ++j) {             // (fewer lanes than that: -inf, no bound)
+            bound = warp_max(top);
+            top = top == bound ? -INFINITY : top;
         }
+        if (a.bias)                                    // and what may be as good
+            bound -= slack + 0x1p-22f * fabsf(bound);
+        bound = live ? fmaxf(bound, -FLT_MAX) : INFINITY;
+        int found = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const unsigned lanes = __ballot_sync(0xffffffffu, c[i] >= bound);
+            if (lanes) {
+                const int to = found + __popc(lanes & ((1u << lane) - 1u));
+                if (c[i] >= bound && to < kMaxFound)
+                    slots.found[to] = key64(c[i], at.base + i);
+                found += __popc(lanes);
+            }
+        }
+        __syncwarp();
+        int slot = -1;
+        bool near = false;                             // the order may not be the exact values'
+        if (found <= kMaxFound) {
+            // their order: by value, and by expert among equal ones
+            for (int i = lane; i < found; i += 32) {
+                const uint64_t own = slots.found[i];
+                int rank = 0, j = 0;
+                for (; j + 4 <= found; j += 4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        rank += slots.found[j + u] > own;
+                for (; j < found; ++j)
+                    rank += slots.found[j] > own;
+                if (rank <= a.k)
+                    slots.sorted[rank] = own;
+            }
+            __syncwarp();
+            if (lane < min(a.k, found)) {
+                const uint64_t own = slots.sorted[lane];
+                slot = expert_of(own);
+                if (a.bias && lane + 1 < found) {
+                    const uint64_t after = slots.sorted[lane + 1];
+                    const float x = value_of(own), y = value_of(after);
+                    // equal inputs have equal values, and are in order
+                    if (x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y)))
+                        near = value(l[slot]) != value(l[expert_of(after)]) || a.bias[slot] != a.bias[expert_of(after)];
+                }
+            }
+        }
+        near = __any_sync(0xffffffffu, near);
+        if (found > kMaxFound || __any_sync(0xffffffffu, close) || (near && !a.sigmoid)) {
+            later = true;
+            if (lane == 0)
+                a.ids[static_cast<int64_t>(t) * a.k] = kLater;
+        } else {
+            if (near) {
+                // the candidates' values in binary64, one to a lane
+                for (int i = lane; i < found; i += 32) {
+                    const int e = expert_of(slots.found[i]);
+                    slots.expert[i] = e;
+                    slots.found[i] = order64(sigmoid64(value(l[e])) + static_cast<double>(a.bias[e]));
+                }
+                __syncwarp();
+                for (int i = lane; i < found; i += 32) {
+                    int rank = 0;
+                    for (int j = 0; j < found; ++j)
+                        rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && slots.expert[j] < slots.expert[i]);
+                    if (rank < a.k)
+                        slots.sorted[rank] = slots.expert[i];
+                }
+                __syncwarp();
+                if (lane < min(a.k, found))
+                    slot = static_cast<int>(slots.sorted[lane]);
+            }
+            const float my_l = slot >= 0 ? value(l[slot]) : 0.f;
+            put(a, t, slot, weight(a.sigmoid, a.renorm, a.scale, my_l, slot >= 0, m, z), __any_sync(0xffffffffu, bad), lane, load);
+        }
+        __syncwarp();                                  // the slots are the next token's
     }
-    if (lane >= a.k)
-        slot = next = -1;
-    float my_l = slot >= 0 ? value(l[slot]) : 0.f;
-    if (a.bias && next >= 0) {
-        // equal inputs have equal values, and are in order
-        const bool same = my_l == value(l[next]) && a.bias[slot] == a.bias[next];
-        close |= !same && mine - after <= slack + 0x1p-23f * fmaxf(fabsf(mine), fabsf(after));
-    }
-    if (__any_sync(0xffffffffu, close) && !bad) {
-        slot = choose_exact<T>(a, l, lane);
-        my_l = slot >= 0 ? value(l[slot]) : 0.f;
-    }
-    float w = weight(a.sigmoid, a.renorm, a.scale, my_l, slot >= 0, m, z);
-    if (bad)
-        w = __uint_as_float(0x7FC00000u);
-    if (lane < a.k) {
-        a.ids[static_cast<int64_t>(t) * a.k + lane] = slot;
-        a.w[static_cast<int64_t>(t) * a.k + lane] = w;
-        if (a.load && slot >= 0)
-            atomicAdd(a.load + slot, 1);
+    if (later)
+        for (uint32_t t = begin; t < static_cast<uint32_t>(a.M); t += step) {
+            if (a.ids[static_cast<int64_t>(t) * a.k] == kLater)
+                route_exact<T>(a, t, slots, load, lane);
+            __syncwarp();
+        }
+    if (a.load) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += kWarps * 32)
+            if (load[e])
+                atomicAdd(a.load + e, load[e]);
     }
 }
 
@@ -371,14 +650,14 @@ struct BwdArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const BwdArgs a)
+__global__ void __launch_bounds__(kBwdWarps * 32) route_bwd_kernel(const BwdArgs a)
 {
     extern __shared__ float rows[];                    // a row of E for each warp
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31;
     float *row = rows + (threadIdx.x >> 5) * a.E;
-    const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int t = blockIdx.x * kBwdWarps + (threadIdx.x >> 5);
     if (t >= a.M)
         return;
     const T *l = static_cast<const T *>(a.logits) + static_cast<int64_t>(t) * a.E;
@@ -449,16 +728,28 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const BwdArgs a)
 template <typename T>
 static cudaError_t launch(Args &a, cudaStream_t s)
 {
-    int lanes = 32;
-    for (int g = 1; g < a.groups; g <<= 1)
+    int lanes = 32, shift = 5;
+    for (int g = 1; g < a.groups; g <<= 1, --shift)
         lanes >>= 1;
     a.lanes = lanes;
+    a.shift = shift;
     a.of_group = a.E / a.groups;
     a.per = (a.of_group + lanes - 1) / lanes;
-    const dim3 grid((a.M + kWarps - 1) / kWarps), block(kWarps * 32);
-    auto k = a.per <= 2   ? route_kernel<T, 2, true>
-             : a.per <= 4 ? route_kernel<T, 4, true>
-             : a.per <= 8 ? route_kernel<T, 8, true>
+    // every lane has all of its experts, and they begin on the alignment of its loads
+    auto full = [&](int per) {
+        const size_t unit = sizeof(T) * per < 16 ? sizeof(T) * per : 16;
+        return a.per == per && a.of_group == per * lanes && a.groups * lanes == 32 && aligned(a.logits, unit) &&
+               aligned(a.bias, per * 4 < 16 ? per * 4 : 16);
+    };
+    const int64_t wanted = (static_cast<int64_t>(a.M) + kWarps - 1) / kWarps, most = device_sm_count() * (a.per <= 8 ? 2 : 1);
+    const dim3 grid(static_cast<unsigned>(wanted < most ? wanted : most)), block(kWarps * 32);
+    auto k = full(2)       ? route_kernel<T, 2, true>
+             : full(4)     ? route_kernel<T, 4, true>
+             : full(8)     ? route_kernel<T, 8, true>
+             : full(16)    ? route_kernel<T, 16, true>
+             : a.per <= 2  ? route_kernel<T, 2, false>
+             : a.per <= 4  ? route_kernel<T, 4, false>
+             : a.per <= 8  ? route_kernel<T, 8, false>
              : a.per <= 16 ? route_kernel<T, 16, false>
              : a.per <= 32 ? route_kernel<T, 32, false>
                            : route_kernel<T, kMaxPer, false>;
@@ -492,7 +783,7 @@ MOE_API moe_status_t moe_route(const void *logits, int32_t ldt, const float *bia
         !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(load, 4))
         return MOE_ERR_INVALID_ARG;
     route::Args a{logits, bias, M, E, k, groups, topk_groups, group_top, score == MOE_SCORE_SIGMOID, renorm, scale,
-                  0, 0, 0, topk_ids, topk_w, load};
+                  0, 0, 0, 0, topk_ids, topk_w, load};
     cudaStream_t s = as_stream(stream);
     const cudaError_t e = ldt == MOE_BF16   ? route::launch<__nv_bfloat16>(a, s)
                           : ldt == MOE_FP16 ? route::launch<__half>(a, s)
@@ -516,8 +807,8 @@ MOE_API moe_status_t moe_route_bwd(const float *dw, const void *logits, int32_t 
         !aligned(dlogits, size))
         return MOE_ERR_INVALID_ARG;
     const route::BwdArgs a{dw, logits, topk_ids, M, E, k, score == MOE_SCORE_SIGMOID, renorm, scale, dlogits};
-    const dim3 grid((M + route::kWarps - 1) / route::kWarps), block(route::kWarps * 32);
-    const size_t smem = sizeof(float) * route::kWarps * E;                  // at most 16 KB
+    const dim3 grid((M + route::kBwdWarps - 1) / route::kBwdWarps), block(route::kBwdWarps * 32);
+    const size_t smem = sizeof(float) * route::kBwdWarps * E;                  // at most 16 KB
     cudaStream_t s = as_stream(stream);
     const cudaError_t e = ldt == MOE_BF16   ? launch_pdl(route::route_bwd_kernel<__nv_bfloat16>, grid, block, smem, s, a)
                           : ldt == MOE_FP16 ? launch_pdl(route::route_bwd_kernel<__half>, grid, block, smem, s, a)
