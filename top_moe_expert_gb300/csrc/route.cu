@@ -126,6 +126,13 @@ __device__ __forceinline__ double value64(uint64_t k)
     return __longlong_as_double(static_cast<long long>(k ^ (k >> 63 ? 0x8000000000000000ull : ~0ull)));
 }
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
+// A score in binary64.  Not inlined: what runs for a few tokens only should be
+// little code, which every SM fetches anew.
+__device__ __noinline__ double score64(double l, bool sigmoid_score, double m, double z)
+{
+    const double t = exp(sigmoid_score ? -l : l - m);
+    return (sigmoid_score ? 1.0 : t) / (sigmoid_score ? 1.0 + t : z);
+}
 __device__ __forceinline__ int expert_of(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 __device__ __forceinline__ float value_of(uint64_t k) { return topk_unkey(static_cast<uint32_t>(k >> 32)); }
 
@@ -163,20 +170,24 @@ struct Exact {
     const Place at;
     const int lane;
     double m, z;                                       // of a softmax
-    float slack;
+    float slack, kept_x = NAN, kept_b = 0.f;
+    uint64_t kept = 0;
 
     __device__ __forceinline__ Exact(const Args &args, const T *row, Slots &s, int my_lane)
         : a(args), l(row), slots(s), at(args, my_lane), lane(my_lane), m(0.0), z(1.0)
     {
         if (!a.sigmoid) {
             float top = -INFINITY;
+#pragma unroll 1
             for (int i = 0; i < at.count; ++i)
                 top = fmaxf(top, logit(at.base + i));
             m = warp_max(top);
             z = 0.0;
             if (m > -INFINITY)
+#pragma unroll 1
                 for (int i = 0; i < at.count; ++i)
-                    z += exp(static_cast<double>(logit(at.base + i)) - m);
+                    z += score64(logit(at.base + i), false, m, 1.0);
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1)
                 z += __shfl_xor_sync(0xffffffffu, z, o);
         }
@@ -198,19 +209,26 @@ struct Exact {
             return near_score(e) + bias(e);
         return of_group && a.group_top == 2 ? near_score(e) : logit(e);
     }
-    __device__ __forceinline__ double exact(int e, bool of_group) const
+    // The same exactly, as its order.  The last one is kept: of many equal experts
+    // (a router that starts at zero) one is formed.
+    __device__ __forceinline__ uint64_t exact(int e, bool of_group)
     {
-        const double x = logit(e);
+        const float x = logit(e), b = a.bias ? bias(e) : 0.f;
         if (!a.bias && !(of_group && a.group_top == 2))
-            return x;
-        const double s = a.sigmoid ? sigmoid64(static_cast<float>(x)) : exp(x - m) / z;
-        return a.bias ? s + static_cast<double>(bias(e)) : s;
+            return order64(x);
+        if (x != kept_x || b != kept_b) {
+            kept_x = x;
+            kept_b = b;
+            kept = order64(score64(x, a.sigmoid, m, z) + static_cast<double>(b));
+        }
+        return kept;
     }
     // All experts of the lane with a value of at least its bound as candidates;
     // their number, which may be above what there is room for.
     __device__ __forceinline__ int collect(bool live, float bound, bool of_group)
     {
         int found = 0;
+#pragma unroll 1
         for (int i = 0; i < a.per; ++i) {
             const float v = live && i < at.count ? near(at.base + i, of_group) : -INFINITY;
             const bool is = v > -INFINITY && v >= bound;
@@ -221,8 +239,9 @@ struct Exact {
             found += __popc(lanes);
         }
         __syncwarp();
+#pragma unroll 1
         for (int i = lane; i < min(found, kMaxFound); i += 32)
-            slots.found[i] = order64(exact(slots.expert[i], of_group));
+            slots.found[i] = exact(slots.expert[i], of_group);
         __syncwarp();
         return found;
     }
@@ -234,8 +253,10 @@ struct Exact {
         if (a.groups == 1)
             return 1u;
         float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 1
         for (int i = 0; i < at.count; ++i)
             best_two(b1, b2, near(at.base + i, true), -INFINITY);
+#pragma unroll 1
         for (int o = 1; o < a.lanes; o <<= 1) {
             const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
             best_two(b1, b2, o1, o2);
@@ -246,17 +267,20 @@ struct Exact {
         if (lane < a.groups) {
             if (found <= kMaxFound) {
                 const int lo = lane * a.of_group, hi = lo + a.of_group;
+#pragma unroll 1
                 for (int i = 0; i < found; ++i)
                     if (slots.expert[i] >= lo && slots.expert[i] < hi)
                         best_two(e1, e2, slots.found[i], static_cast<uint64_t>(0));
             } else {
+#pragma unroll 1
                 for (int e = lane * a.of_group; e < (lane + 1) * a.of_group; ++e)
                     if (near(e, true) > -INFINITY)
-                        best_two(e1, e2, order64(exact(e, true)), static_cast<uint64_t>(0));
+                        best_two(e1, e2, exact(e, true), static_cast<uint64_t>(0));
             }
         }
         const uint64_t v = a.group_top == 2 && e2 ? order64(value64(e1) + value64(e2)) : e1;
         int better = 0;
+#pragma unroll 1
         for (int g = 0; g < a.groups; ++g) {
             const uint64_t o = __shfl_sync(0xffffffffu, v, g);
             better += o > v || (o == v && g < lane);
@@ -268,18 +292,23 @@ struct Exact {
         const unsigned in = groups();                    // by all lanes, also those without a group
         const bool live = at.group < a.groups && (in >> at.group & 1u);
         float top = -INFINITY, last = -INFINITY;
+#pragma unroll 1
         for (int i = 0; live && i < at.count; ++i)
             top = fmaxf(top, near(at.base + i, false));
-        for (int j = 0; j <= a.k; ++j) {
+#pragma unroll 1
+        for (int lanes = 0; lanes <= a.k;) {
             last = warp_max(top);
             if (last == -INFINITY)
                 break;
+            lanes += __popc(__ballot_sync(0xffffffffu, top == last));
             top = top == last ? -INFINITY : top;
         }
         const int found = collect(live, a.bias && last > -INFINITY ? below(last) : last, false);
         if (found <= kMaxFound) {
+#pragma unroll 1
             for (int i = lane; i < found; i += 32) {
                 int rank = 0;
+#pragma unroll 1
                 for (int j = 0; j < found; ++j)
                     rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && slots.expert[j] < slots.expert[i]);
                 if (rank < a.k)
@@ -291,18 +320,21 @@ struct Exact {
         // that many equal values: one slot after the other, over all experts
         uint64_t taken = live ? 0ull : ~0ull;
         int slot = -1;
+#pragma unroll 1
         for (int j = 0; j < a.k; ++j) {
             uint64_t best = 0;
             int at_best = -1;
+#pragma unroll 1
             for (int i = 0; i < at.count; ++i)
                 if (!(taken >> i & 1) && near(at.base + i, false) > -INFINITY) {
-                    const uint64_t v = order64(exact(at.base + i, false));
+                    const uint64_t v = exact(at.base + i, false);
                     if (v > best) {
                         best = v;
                         at_best = i;
                     }
                 }
             uint64_t first = best;
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) {
                 const uint64_t n = __shfl_xor_sync(0xffffffffu, first, o);
                 first = n > first ? n : first;
