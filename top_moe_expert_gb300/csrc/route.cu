@@ -110,10 +110,11 @@ struct Slots {
     int expert[kMaxFound];
 };
 
-// A value and its expert as one number: larger values first, then lower experts.
-__device__ __forceinline__ uint64_t key64(float v, int e)
+// A value and its place among the candidates as one number: larger values first,
+// then lower places.
+__device__ __forceinline__ uint64_t key64(float v, int place)
 {
-    return static_cast<uint64_t>(topk_key(v)) << 32 | ~static_cast<uint32_t>(e);
+    return static_cast<uint64_t>(topk_key(v)) << 32 | ~static_cast<uint32_t>(place);
 }
 // Comparisons of binary64 take a warp some 60 cycles, those of whole numbers 4.
 __device__ __forceinline__ uint64_t order64(double v)
@@ -133,7 +134,7 @@ __device__ __noinline__ double score64(double l, bool sigmoid_score, double m, d
     const double t = exp(sigmoid_score ? -l : l - m);
     return (sigmoid_score ? 1.0 : t) / (sigmoid_score ? 1.0 + t : z);
 }
-__device__ __forceinline__ int expert_of(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
+__device__ __forceinline__ int index_of(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 __device__ __forceinline__ float value_of(uint64_t k) { return topk_unkey(static_cast<uint32_t>(k >> 32)); }
 
 // The errors that the values of the choice may have in binary32.
@@ -381,6 +382,14 @@ __device__ __noinline__ void route_exact(const Args &a, uint32_t t, Slots &slots
     __syncwarp();
 }
 
+// A bit for each of a lane's experts.
+template <int PER>
+using Mask = std::conditional_t<(PER > 32), uint64_t, uint32_t>;
+__device__ __forceinline__ int popc(uint32_t m) { return __popc(m); }
+__device__ __forceinline__ int popc(uint64_t m) { return __popcll(m); }
+__device__ __forceinline__ int first_of(uint32_t m) { return __ffs(m) - 1; }
+__device__ __forceinline__ int first_of(uint64_t m) { return __ffsll(m) - 1; }
+
 // Consecutive elements of a row: 16 bytes at a time where FULL says that every
 // lane has PER of them, on their natural alignment.
 template <typename T, int PER, bool FULL>
@@ -580,44 +589,61 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
         if (a.bias)                                    // and what may be as good
             bound -= slack + 0x1p-22f * fabsf(bound);
         bound = live ? fmaxf(bound, -FLT_MAX) : INFINITY;
-        int found = 0;
+        // what is not below it, by expert: the lanes' counts give each its place
+        Mask<PER> which = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const unsigned lanes = __ballot_sync(0xffffffffu, c[i] >= bound);
-            if (lanes) {
-                const int to = found + __popc(lanes & ((1u << lane) - 1u));
-                if (c[i] >= bound && to < kMaxFound)
-                    slots.found[to] = key64(c[i], at.base + i);
-                found += __popc(lanes);
-            }
+        for (int i = 0; i < PER; ++i)
+            which |= c[i] >= bound ? static_cast<Mask<PER>>(1) << i : 0;
+        int to = popc(which);
+        const int own = to;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, to, o);
+            to += lane >= o ? n : 0;
         }
-        __syncwarp();
-        int slot = -1;
+        const int found = __shfl_sync(0xffffffffu, to, 31);
         bool near = false;                             // the order may not be the exact values'
+        int slot = -1;
+        float my_l = 0.f;
         if (found <= kMaxFound) {
-            // their order: by value, and by expert among equal ones
+            for (to -= own; which; which &= which - 1)
+                slots.expert[to++] = at.base + first_of(which);
+            __syncwarp();
+            // each lane takes one, or two, and finds its rank; equal ones are in order already
             for (int i = lane; i < found; i += 32) {
-                const uint64_t own = slots.found[i];
+                const int e = slots.expert[i];
+                const float x = value(l[e]);
+                float y = x;
+                if (a.bias)
+                    y = (a.sigmoid ? fast_sigmoid(x) : __expf(x - m) * rz) + a.bias[e];
+                slots.found[i] = key64(y, i);
+            }
+            __syncwarp();
+            for (int i = lane; i < found; i += 32) {
+                const uint64_t mine = slots.found[i];
                 int rank = 0, j = 0;
                 for (; j + 4 <= found; j += 4)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        rank += slots.found[j + u] > own;
+                        rank += slots.found[j + u] > mine;
                 for (; j < found; ++j)
-                    rank += slots.found[j] > own;
+                    rank += slots.found[j] > mine;
                 if (rank <= a.k)
-                    slots.sorted[rank] = own;
+                    slots.sorted[rank] = mine;
             }
             __syncwarp();
             if (lane < min(a.k, found)) {
-                const uint64_t own = slots.sorted[lane];
-                slot = expert_of(own);
+                const uint64_t mine = slots.sorted[lane];
+                slot = slots.expert[index_of(mine)];
+                my_l = value(l[slot]);
                 if (a.bias && lane + 1 < found) {
                     const uint64_t after = slots.sorted[lane + 1];
-                    const float x = value_of(own), y = value_of(after);
+                    const float x = value_of(mine), y = value_of(after);
                     // equal inputs have equal values, and are in order
-                    if (x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y)))
-                        near = value(l[slot]) != value(l[expert_of(after)]) || a.bias[slot] != a.bias[expert_of(after)];
+                    if (x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y))) {
+                        const int e = slots.expert[index_of(after)];
+                        near = my_l != value(l[e]) || a.bias[slot] != a.bias[e];
+                    }
                 }
             }
         }
@@ -630,23 +656,23 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
             if (near) {
                 // the candidates' values in binary64, one to a lane
                 for (int i = lane; i < found; i += 32) {
-                    const int e = expert_of(slots.found[i]);
-                    slots.expert[i] = e;
+                    const int e = slots.expert[i];
                     slots.found[i] = order64(sigmoid64(value(l[e])) + static_cast<double>(a.bias[e]));
                 }
                 __syncwarp();
                 for (int i = lane; i < found; i += 32) {
                     int rank = 0;
                     for (int j = 0; j < found; ++j)
-                        rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && slots.expert[j] < slots.expert[i]);
+                        rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && j < i);
                     if (rank < a.k)
                         slots.sorted[rank] = slots.expert[i];
                 }
                 __syncwarp();
-                if (lane < min(a.k, found))
+                if (lane < min(a.k, found)) {
                     slot = static_cast<int>(slots.sorted[lane]);
+                    my_l = value(l[slot]);
+                }
             }
-            const float my_l = slot >= 0 ? value(l[slot]) : 0.f;
             put(a, t, slot, weight(a.sigmoid, a.renorm, a.scale, my_l, slot >= 0, m, z), __any_sync(0xffffffffu, bad), lane, load);
         }
         __syncwarp();                                  // the slots are the next token's
