@@ -171,8 +171,9 @@ struct Exact {
     const Place at;
     const int lane;
     double m, z;                                       // of a softmax
-    float slack, kept_x = NAN, kept_b = 0.f;
+    float slack, rz, kept_x = NAN, kept_b = 0.f;
     uint64_t kept = 0;
+    float own[kMaxPer];                                // the lane's experts' values in binary32
 
     __device__ __forceinline__ Exact(const Args &args, const T *row, Slots &s, int my_lane)
         : a(args), l(row), slots(s), at(args, my_lane), lane(my_lane), m(0.0), z(1.0)
@@ -192,7 +193,8 @@ struct Exact {
             for (int o = 16; o > 0; o >>= 1)
                 z += __shfl_xor_sync(0xffffffffu, z, o);
         }
-        slack = slack_of(a, static_cast<float>(1.0 / z));
+        rz = 1.0f / static_cast<float>(z);
+        slack = slack_of(a, rz);
     }
     __device__ __forceinline__ float logit(int e) const { return clean(value(l[e])); }
     __device__ __forceinline__ float bias(int e) const { return clean(a.bias[e]); }
@@ -201,7 +203,7 @@ struct Exact {
         const float x = logit(e);
         return !(x > -INFINITY) ? -INFINITY
                : a.sigmoid      ? fast_sigmoid(x)
-                                : __expf(x - static_cast<float>(m)) * static_cast<float>(1.0 / z);
+                                : __expf(x - static_cast<float>(m)) * rz;
     }
     // What a group's value is made of, and what experts are chosen by.
     __device__ __forceinline__ float near(int e, bool of_group) const
@@ -224,6 +226,12 @@ struct Exact {
         }
         return kept;
     }
+    __device__ __forceinline__ void form(bool of_group)
+    {
+#pragma unroll 4
+        for (int i = 0; i < at.count; ++i)
+            own[i] = near(at.base + i, of_group);
+    }
     // All experts of the lane with a value of at least its bound as candidates;
     // their number, which may be above what there is room for.
     __device__ __forceinline__ int collect(bool live, float bound, bool of_group)
@@ -231,7 +239,7 @@ struct Exact {
         int found = 0;
 #pragma unroll 1
         for (int i = 0; i < a.per; ++i) {
-            const float v = live && i < at.count ? near(at.base + i, of_group) : -INFINITY;
+            const float v = live && i < at.count ? own[i] : -INFINITY;
             const bool is = v > -INFINITY && v >= bound;
             const unsigned lanes = __ballot_sync(0xffffffffu, is);
             const int to = found + __popc(lanes & ((1u << lane) - 1u));
@@ -253,10 +261,11 @@ struct Exact {
     {
         if (a.groups == 1)
             return 1u;
+        form(true);
         float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll 1
         for (int i = 0; i < at.count; ++i)
-            best_two(b1, b2, near(at.base + i, true), -INFINITY);
+            best_two(b1, b2, own[i], -INFINITY);
 #pragma unroll 1
         for (int o = 1; o < a.lanes; o <<= 1) {
             const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
@@ -292,10 +301,12 @@ struct Exact {
     {
         const unsigned in = groups();                    // by all lanes, also those without a group
         const bool live = at.group < a.groups && (in >> at.group & 1u);
+        if (a.groups == 1 || !a.bias)
+            form(false);
         float top = -INFINITY, last = -INFINITY;
 #pragma unroll 1
         for (int i = 0; live && i < at.count; ++i)
-            top = fmaxf(top, near(at.base + i, false));
+            top = fmaxf(top, own[i]);
 #pragma unroll 1
         for (int lanes = 0; lanes <= a.k;) {
             last = warp_max(top);
@@ -308,12 +319,14 @@ struct Exact {
         if (found <= kMaxFound) {
 #pragma unroll 1
             for (int i = lane; i < found; i += 32) {
+                const uint64_t v = slots.found[i];
+                const int e = slots.expert[i];
                 int rank = 0;
-#pragma unroll 1
+#pragma unroll 4
                 for (int j = 0; j < found; ++j)
-                    rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && slots.expert[j] < slots.expert[i]);
+                    rank += slots.found[j] > v || (slots.found[j] == v && slots.expert[j] < e);
                 if (rank < a.k)
-                    slots.sorted[rank] = slots.expert[i];
+                    slots.sorted[rank] = e;
             }
             __syncwarp();
             return lane < a.k && lane < found ? static_cast<int>(slots.sorted[lane]) : -1;
@@ -327,7 +340,7 @@ struct Exact {
             int at_best = -1;
 #pragma unroll 1
             for (int i = 0; i < at.count; ++i)
-                if (!(taken >> i & 1) && near(at.base + i, false) > -INFINITY) {
+                if (!(taken >> i & 1) && own[i] > -INFINITY) {
                     const uint64_t v = exact(at.base + i, false);
                     if (v > best) {
                         best = v;
