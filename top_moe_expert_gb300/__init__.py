@@ -802,17 +802,24 @@ def moe_grouped_mm_awq(x: torch.Tensor, w: Weights, offsets: torch.Tensor, out_d
     product).  out_dtype: x's type (default) or float32."""
     if not isinstance(w, Weights) or w.fmt != MOE_W_AWQ4:
         raise ValueError("w must be AWQ4 Weights")
-    _arg(x, "x", _DT16, 2)
-    gpu, dev, dt = x.get_device(), x.device, x.dtype
-    _arg(offsets, "offsets", _IDS, 1, dev)
+    try:
+        gpu, dt = x.get_device(), x.dtype
+        ok = (gpu >= 0 and dt in _DT16 and x.is_contiguous() and x.dim() == 2 and offsets.dtype is torch.int32
+              and offsets.get_device() == gpu and offsets.is_contiguous() and offsets.dim() == 1)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _arg(x, "x", _DT16, 2)
+        _arg(offsets, "offsets", _IDS, 1, x.device)
+    dev, dt, c = x.device, x.dtype, w.c_struct()
     w.on("w", dev)
-    (R, k), E = x.shape, _experts(offsets)
-    if w.E != E or w.K != k:
-        raise ValueError(f"w is [{w.E}, {w.N}, {w.K}]; offsets are for {E} experts and x has K = {k}")
-    if (R | E | w.N | k) >> 31:
-        _too_long(R, E, w.N, k)
-    y = _result(y, "y", (R, w.N), out_dtype or dt, (dt, torch.float32), dev, stream)
-    _launch(gpu, "moe_grouped_mm_awq", x.data_ptr(), _DT[dt], w.c_struct(), offsets.data_ptr(), R, y.data_ptr(),
+    (R, k), E, N = x.shape, _experts(offsets), c.N
+    if c.E != E or c.K != k:
+        raise ValueError(f"w is [{c.E}, {N}, {c.K}]; offsets are for {E} experts and x has K = {k}")
+    if (R | E | N | k) >> 31:
+        _too_long(R, E, N, k)
+    y = _result(y, "y", (R, N), out_dtype or dt, (dt, torch.float32), dev, stream)
+    _launch(gpu, "moe_grouped_mm_awq", x.data_ptr(), _DT[dt], c, offsets.data_ptr(), R, y.data_ptr(),
             _DT[y.dtype], _status(dev_status, dev), _on(stream, gpu, dev))
     return y
 
@@ -839,8 +846,31 @@ def moe_route(logits: torch.Tensor, k: int, score: int = MOE_SCORE_SOFTMAX, bias
     topk_groups best of `groups` groups, each worth its group_top (1 or 2) best
     values; weights scale * score, over their sum with renorm.  load int32 [E] is
     increased by each expert's slots.  ragged.route has the gradient."""
+    try:
+        gpu, (M, E) = logits.get_device(), logits.shape
+        ok = (gpu >= 0 and logits.dtype in _DT and logits.is_contiguous() and score in _SCORES and 0 < k <= E
+              and 0.0 < scale < math.inf and 0 < topk_groups <= groups <= E and E % groups == 0
+              and k <= topk_groups * (E // groups) and 0 < group_top < 3 and (M * k) >> 31 == 0
+              and (bias is None or bias.dtype is torch.float32 and bias.get_device() == gpu and bias.is_contiguous()
+                   and bias.dim() == 1 and bias.shape[0] == E)
+              and (load is None or load.dtype is torch.int32 and load.get_device() == gpu and load.is_contiguous()
+                   and load.dim() == 1 and load.shape[0] == E))
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        _need_route(logits, k, score, bias, groups, topk_groups, group_top, scale, load)
+    dev = logits.device
+    ids = _result(topk_ids, "topk_ids", (M, k), torch.int32, _IDS, dev, stream)
+    w = _result(topk_w, "topk_w", (M, k), torch.float32, _F32, dev, stream)
+    _launch(gpu, "moe_route", logits.data_ptr(), _DT[logits.dtype], _ptr(bias), M, E, k, score, groups, topk_groups,
+            group_top, 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(), _ptr(load), _on(stream, gpu, dev))
+    return ids, w
+
+
+def _need_route(logits, k, score, bias, groups, topk_groups, group_top, scale, load) -> None:
+    """What moe_route asks of its arguments, with the reason why not."""
     M, E = _arg(logits, "logits", _DT, 2)
-    gpu, dev = logits.get_device(), logits.device
+    dev = logits.device
     _route_how(k, E, score, scale)
     if not 1 <= groups <= E or E % groups or not 1 <= topk_groups <= groups or group_top not in (1, 2):
         raise ValueError(f"groups = {groups}, topk_groups = {topk_groups}, group_top = {group_top} do not fit E = {E}")
@@ -850,27 +880,31 @@ def moe_route(logits: torch.Tensor, k: int, score: int = MOE_SCORE_SOFTMAX, bias
         _too_long(M, k)
     _opt(bias, "bias", dtypes=_F32, shape=(E,), device=dev)
     _opt(load, "load", dtypes=_IDS, shape=(E,), device=dev)
-    ids = _result(topk_ids, "topk_ids", (M, k), torch.int32, _IDS, dev, stream)
-    w = _result(topk_w, "topk_w", (M, k), torch.float32, _F32, dev, stream)
-    _launch(gpu, "moe_route", logits.data_ptr(), _DT[logits.dtype], _ptr(bias), M, E, k, score, groups, topk_groups,
-            group_top, 1 if renorm else 0, scale, ids.data_ptr(), w.data_ptr(), _ptr(load), _on(stream, gpu, dev))
-    return ids, w
 
 
 def moe_route_bwd(dw: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, score: int = MOE_SCORE_SOFTMAX,
                   renorm: bool = True, scale: float = 1.0, dlogits=None, stream=None):
     """dlogits [M, E], of logits' type: the gradient of moe_route's logits from
     that of its weights, dw float32 [M, k], at the ids it gave."""
-    M, E = _arg(logits, "logits", _DT, 2)
-    gpu, dev = logits.get_device(), logits.device
-    m, k = _arg(topk_ids, "topk_ids", _IDS, 2, dev)
-    if m != M:
-        raise ValueError(f"topk_ids is for {m} tokens, logits for {M}")
-    _route_how(k, E, score, scale)
-    if _arg(dw, "dw", _F32, 2, dev) != (M, k):
-        raise ValueError(f"dw has shape {tuple(dw.shape)}; expected {(M, k)}")
-    if (M * k) >> 31:
-        _too_long(M, k)
+    try:
+        gpu, (M, E), (m, k) = logits.get_device(), logits.shape, topk_ids.shape
+        ok = (gpu >= 0 and logits.dtype in _DT and logits.is_contiguous() and topk_ids.dtype is torch.int32
+              and topk_ids.get_device() == gpu and topk_ids.is_contiguous() and dw.dtype is torch.float32
+              and dw.get_device() == gpu and dw.is_contiguous() and dw.shape == topk_ids.shape and m == M
+              and score in _SCORES and 0 < k <= E and 0.0 < scale < math.inf and (M * k) >> 31 == 0)
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:                                                        # the same, with the reason why not
+        M, E = _arg(logits, "logits", _DT, 2)
+        m, k = _arg(topk_ids, "topk_ids", _IDS, 2, logits.device)
+        if m != M:
+            raise ValueError(f"topk_ids is for {m} tokens, logits for {M}")
+        _route_how(k, E, score, scale)
+        if _arg(dw, "dw", _F32, 2, logits.device) != (M, k):
+            raise ValueError(f"dw has shape {tuple(dw.shape)}; expected {(M, k)}")
+        if (M * k) >> 31:
+            _too_long(M, k)
+    dev = logits.device
     dl = _result(dlogits, "dlogits", (M, E), logits.dtype, (logits.dtype,), dev, stream)
     _launch(gpu, "moe_route_bwd", dw.data_ptr(), logits.data_ptr(), _DT[logits.dtype], topk_ids.data_ptr(), M, E, k,
             score, 1 if renorm else 0, scale, dl.data_ptr(), _on(stream, gpu, dev))
@@ -878,7 +912,17 @@ def moe_route_bwd(dw: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor
 
 
 def _swiglu_args(gu, p, rng):
-    R, cols = _arg(gu, "gu", _DT, 2)
+    """Check gu, p and rng; returns R, I and the GPU's index."""
+    try:
+        gpu, (R, cols) = gu.get_device(), gu.shape
+        if (gpu >= 0 and gu.dtype in _DT and gu.is_contiguous() and cols > 0 and cols % 2 == 0 and (R | cols // 2) >> 31 == 0
+                and 0.0 <= p < 1.0 - 2.0 ** -17
+                and (p < 2.0 ** -17 if rng is None else rng.dtype is torch.int64 and rng.get_device() == gpu
+                     and rng.is_contiguous() and rng.dim() == 1 and rng.shape[0] == 2)):
+            return R, cols // 2, gpu
+    except (AttributeError, TypeError, ValueError):
+        pass
+    R, cols = _arg(gu, "gu", _DT, 2)                                  # the same, with the reason why not
     if cols < 2 or cols % 2:
         raise ValueError(f"gu must be [R, 2 I], not {tuple(gu.shape)}")
     if (R | cols // 2) >> 31:
@@ -889,14 +933,15 @@ def _swiglu_args(gu, p, rng):
         _need(rng, "rng", (torch.int64,), (2,), device=gu.device)
     elif p >= 2.0 ** -17:
         raise ValueError("dropout needs rng, int64 [2]: seed and offset")
-    return R, cols // 2, gu.get_device(), gu.device
+    return R, cols // 2, gu.get_device()
 
 
 def moe_swiglu_dropout(gu: torch.Tensor, p: float = 0.0, rng=None, h=None, stream=None):
     """h [R, I] of gu [R, 2 I] = [g | u] (fp32, bf16 or fp16): silu(g) u, dropped
     with chance p (in steps of 2^-16) and divided by what is kept of 1.  rng int64
     [2] on the GPU: {seed, offset}; each call of a step takes its own offset."""
-    R, I, gpu, dev = _swiglu_args(gu, p, rng)
+    R, I, gpu = _swiglu_args(gu, p, rng)
+    dev = gu.device
     h = _result(h, "h", (R, I), gu.dtype, (gu.dtype,), dev, stream)
     _launch(gpu, "moe_swiglu_dropout", gu.data_ptr(), _DT[gu.dtype], R, I, p, _ptr(rng), h.data_ptr(),
             _on(stream, gpu, dev))
@@ -906,7 +951,8 @@ def moe_swiglu_dropout(gu: torch.Tensor, p: float = 0.0, rng=None, h=None, strea
 def moe_swiglu_dropout_bwd(dh: torch.Tensor, gu: torch.Tensor, p: float = 0.0, rng=None, dgu=None, stream=None):
     """dgu [R, 2 I], the gradient of moe_swiglu_dropout's gu from dh [R, I], with
     the p and rng of that call.  dgu may be gu."""
-    R, I, gpu, dev = _swiglu_args(gu, p, rng)
+    R, I, gpu = _swiglu_args(gu, p, rng)
+    dev = gu.device
     if _arg(dh, "dh", (gu.dtype,), 2, dev) != (R, I):
         raise ValueError(f"dh has shape {tuple(dh.shape)}; expected {(R, I)}")
     dgu = _result(dgu, "dgu", (R, 2 * I), gu.dtype, (gu.dtype,), dev, stream)
