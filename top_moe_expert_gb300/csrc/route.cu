@@ -447,6 +447,30 @@ __device__ __forceinline__ void load_row(const T *p, int count, float (&v)[PER])
     }
 }
 
+template <typename T, int PER>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[PER])
+{
+    constexpr int kWords = PER * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 4)
+            w[i] = __float_as_uint(v[i]);
+        else
+            w[i] = gmm::pack2<T>(v[2 * i], v[2 * i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) {
+        uint32_t *to = reinterpret_cast<uint32_t *>(p) + i;
+        if constexpr (kWords % 4 == 0)
+            *reinterpret_cast<uint4 *>(to) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        else if constexpr (kWords == 2)
+            *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+        else
+            *to = w[0];
+    }
+}
+
 // Warps go over the tokens.  Of a token, each lane finds its best value; the
 // (k + 1)-th best of those bounds what can be chosen, usually some ten values,
 // which the lanes then take one each and rank.  Tokens that binary32 cannot decide
@@ -720,16 +744,26 @@ struct BwdArgs {
     void *dl;
 };
 
-template <typename T>
+// Where a row of the gradient holds expert e: the pieces of four of a lane's PER
+// experts lie apart, so that the lanes' pieces are neighbours.
+template <int PER>
+__device__ __forceinline__ int place_of(int e)
+{
+    return PER < 4 ? e : e % PER / 4 * 128 + e / PER * 4 + e % 4;
+}
+
+// PER: experts of a lane, neighbouring ones that it loads and stores as vectors; 0:
+// any number, every 32nd one.
+template <typename T, int PER>
 __global__ void __launch_bounds__(kBwdWarps * 32) route_bwd_kernel(const BwdArgs a)
 {
-    extern __shared__ float rows[];                    // a row of E for each warp
+    extern __shared__ __align__(16) float rows[];      // a row of E for each warp
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31;
     float *row = rows + (threadIdx.x >> 5) * a.E;
-    const int t = blockIdx.x * kBwdWarps + (threadIdx.x >> 5);
-    if (t >= a.M)
+    const uint32_t t = blockIdx.x * kBwdWarps + (threadIdx.x >> 5);
+    if (t >= static_cast<uint32_t>(a.M))
         return;
     const T *l = static_cast<const T *>(a.logits) + static_cast<int64_t>(t) * a.E;
     T *dl = static_cast<T *>(a.dl) + static_cast<int64_t>(t) * a.E;
@@ -749,19 +783,45 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_bwd_kernel(const BwdArgs
     }
     float m = -INFINITY, z = 0.f;
     bool bad = false;
-    for (int i = lane; i < a.E; i += 32) {
-        const float x = value(l[i]);
-        bad |= !(x < INFINITY);
-        m = fmaxf(m, x);
-        row[i] = 0.f;
+    constexpr int kOwn = PER ? PER : 1;
+    float v[kOwn];                                     // logits, then exp(logit - m)
+    if constexpr (PER > 0) {
+        load_row<T, kOwn, true>(l + lane * PER, PER, v);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            bad |= !(v[i] < INFINITY);
+            if (PER < 4)
+                row[lane * PER + i] = 0.f;
+            else if (i % 4 == 0)
+                reinterpret_cast<float4 *>(row)[i * 8 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (dense) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                m = fmaxf(m, v[i]);
+            m = warp_max(m);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                v[i] = v[i] > -INFINITY ? expf(v[i] - m) : 0.f;
+                z += v[i];
+            }
+            z = warp_sum(z);
+        }
+    } else {
+        for (int i = lane; i < a.E; i += 32) {
+            const float x = value(l[i]);
+            bad |= !(x < INFINITY);
+            m = fmaxf(m, x);
+            row[i] = 0.f;
+        }
+        if (dense) {
+            m = warp_max(m);
+            for (int i = lane; i < a.E; i += 32)
+                z += m > -INFINITY ? expf(value(l[i]) - m) : 0.f;
+            z = warp_sum(z);
+        }
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (dense) {
-        m = warp_max(m);
-        for (int i = lane; i < a.E; i += 32)
-            z += m > -INFINITY ? expf(value(l[i]) - m) : 0.f;
-        z = warp_sum(z);
-    }
     const float w = weight(a.sigmoid, a.renorm, a.scale, lj, e >= 0, m, z);
     float g = e >= 0 ? w * dw : 0.f;
     const float sum = warp_sum(g);
@@ -784,15 +844,36 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_bwd_kernel(const BwdArgs
     }
     __syncwarp();
     if (e >= 0)
-        row[e] = g;
+        row[PER ? place_of<kOwn>(e) : e] = g;
     __syncwarp();
-    for (int i = lane; i < a.E; i += 32) {
-        float d = row[i];
-        if (dense) {
-            const float x = value(l[i]);
-            d -= x > -INFINITY ? expf(x - m) / z * sum : 0.f;
+    const float f = sum / z;
+    if constexpr (PER > 0) {
+        float d[kOwn];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (PER < 4) {
+                d[i] = row[lane * PER + i];
+            } else if (i % 4 == 0) {
+                const float4 q = reinterpret_cast<const float4 *>(row)[i * 8 + lane];
+                d[i] = q.x, d[(i + 1) % kOwn] = q.y, d[(i + 2) % kOwn] = q.z, d[(i + 3) % kOwn] = q.w;
+            }
         }
-        dl[i] = fp4::from_float<T>(bad ? __uint_as_float(0x7FC00000u) : d);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (dense)
+                d[i] -= v[i] * f;
+            d[i] = bad ? __uint_as_float(0x7FC00000u) : d[i];
+        }
+        store_row<T, kOwn>(dl + lane * PER, d);
+    } else {
+        for (int i = lane; i < a.E; i += 32) {
+            float d = row[i];
+            if (dense) {
+                const float x = value(l[i]);
+                d -= x > -INFINITY ? expf(x - m) * f : 0.f;
+            }
+            dl[i] = fp4::from_float<T>(bad ? __uint_as_float(0x7FC00000u) : d);
+        }
     }
 }
 
@@ -825,6 +906,21 @@ static cudaError_t launch(Args &a, cudaStream_t s)
              : a.per <= 32 ? route_kernel<T, 32, false>
                            : route_kernel<T, kMaxPer, false>;
     return launch_pdl(k, grid, block, 0, s, a);
+}
+
+template <typename T>
+static cudaError_t launch_bwd(const BwdArgs &a, dim3 grid, dim3 block, size_t smem, cudaStream_t s)
+{
+    auto full = [&](int per) {
+        const size_t unit = sizeof(T) * per < 16 ? sizeof(T) * per : 16;
+        return a.E == 32 * per && aligned(a.logits, unit) && aligned(a.dl, unit);
+    };
+    auto k = full(2)    ? route_bwd_kernel<T, 2>
+             : full(4)  ? route_bwd_kernel<T, 4>
+             : full(8)  ? route_bwd_kernel<T, 8>
+             : full(16) ? route_bwd_kernel<T, 16>
+                        : route_bwd_kernel<T, 0>;
+    return launch_pdl(k, grid, block, smem, s, a);
 }
 
 static bool how(int32_t E, int32_t k, int32_t score, int32_t renorm, float scale)
@@ -881,8 +977,8 @@ MOE_API moe_status_t moe_route_bwd(const float *dw, const void *logits, int32_t 
     const dim3 grid((M + route::kBwdWarps - 1) / route::kBwdWarps), block(route::kBwdWarps * 32);
     const size_t smem = sizeof(float) * route::kBwdWarps * E;                  // at most 16 KB
     cudaStream_t s = as_stream(stream);
-    const cudaError_t e = ldt == MOE_BF16   ? launch_pdl(route::route_bwd_kernel<__nv_bfloat16>, grid, block, smem, s, a)
-                          : ldt == MOE_FP16 ? launch_pdl(route::route_bwd_kernel<__half>, grid, block, smem, s, a)
-                                            : launch_pdl(route::route_bwd_kernel<float>, grid, block, smem, s, a);
+    const cudaError_t e = ldt == MOE_BF16   ? route::launch_bwd<__nv_bfloat16>(a, grid, block, smem, s)
+                          : ldt == MOE_FP16 ? route::launch_bwd<__half>(a, grid, block, smem, s)
+                                            : route::launch_bwd<float>(a, grid, block, smem, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
