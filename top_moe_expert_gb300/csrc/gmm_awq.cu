@@ -2,18 +2,31 @@
 // y[r][n] = sum_k x[r][k] (q[e][n][k] - zero) scale for the rows r of expert e.
 //
 // The work is reading the weights of the experts that have rows once, 0.52 bytes
-// each, and widening them.  A CTA takes 16 rows of an expert's weights and up to
-// 8 NT of its rows of x, and its warps divide K.  The codes less their zero, whole
-// numbers up to 15, are exact in x's own type, and so are the products: the
-// tensor cores (m16n8k16, the weights as the left operand) add a group of 128 in
-// FP32, and the group's scale comes to the sum.  Against multiplications on the
-// CUDA cores that saves the conversion to FP32 and, for more than one row, widens
+// each, and widening them.  A CTA takes 16 or 32 rows of an expert's weights and up to
+// 8 or 16 of its rows of x; its two or four warps divide K (by K alone, so that a
+// row's result does not depend on the other rows), each with a ring of its own that
+// cp.async fills two groups ahead, and add their sums in order at the end.  The codes
+// less their zero, whole numbers up to 15, are exact in x's own type, and so are the
+// products: the tensor cores (m16n8k16, the weights as the left operand) add a group
+// of 128 in FP32, and the group's scale comes to the sum.  Against multiplications on
+// the CUDA cores that saves the conversion to FP32 and, for more than one row, widens
 // each weight once for all rows.
 //
 // The order of k inside a group is free as long as both operands agree: lane t of
 // a row's four takes 16 bytes of codes, k = 32 t .. 32 t + 31, and of each word of
 // 8 the pairs (0, 4), (1, 5), (2, 6), (3, 7), which one AND and OR turn into two
 // numbers 1024 + q (fp16) or 128 + q (bf16).
+//
+// Bound by the widening: some 145 instructions for 16 rows by a group, half of them
+// shifts and masks of the pipe that runs at half rate, which is two thirds busy.  One
+// row by 65536 x 8192 takes 76 us (3.7 TB/s), one row of each of 128 experts of 1536 x
+// 2048 63 us (3.4 TB/s), 512 rows, Zipf over them, 57.5 us.  What did not help there:
+// deeper rings or weights straight into registers, a group ahead or not; x a group
+// ahead; one CTA per SM that walks all its tiles with x staged in shared memory (102
+// us); the zero taken off the sums instead of the codes would save a fifth of the
+// instructions, but the sums of 128 + q lose four bits.  Few rows are bound by one
+// warp's chain of instructions: 8 rows of 8 of 128 experts 8.0 us, one row by 4096 x
+// 7168 8.0 us.
 #include <atomic>
 #include <type_traits>
 
@@ -261,7 +274,7 @@ __device__ __forceinline__ void dot(const Args &a, const Run &f, Loader<MT, D> &
 
 // W warps divide K; a CTA takes 16 MT rows of w and a run of up to 8 NT rows of x.
 template <typename T, int W, int MT, int NT>
-__global__ void __launch_bounds__(32 * W, 16 / W) gmm_awq_kernel(const Args a)
+__global__ void __launch_bounds__(32 * W, (W == 2 && MT * NT == 1 ? 24 : 16) / W) gmm_awq_kernel(const Args a)
 {
     constexpr int kThreads = 32 * W, kRowsW = 16 * MT, D = kDepth;
     __shared__ Run s_run;
@@ -358,7 +371,14 @@ template <typename T>
 static moe_status_t run(const Args &a, cudaStream_t s)
 {
     const int64_t live = a.E < a.R ? a.E : a.R;
-    const bool wide = live * ((a.N + 31) / 32) >= 2 * device_sm_count();
+    // 32 rows of w per CTA halve the work on x, where that leaves eight CTAs for every
+    // SM: 512 rows over 128 experts 57.5 us, 74.5 with 16 rows; for 8 rows of 8 experts
+    // (2.5 CTAs per SM) 8.7 us with 32 rows, 8.0 with 16
+    const bool wide = live * ((a.N + 31) / 32) >= 8 * device_sm_count();
+    // Groups per warp: at K = 2048 two warps take 57.5 us for those 512 rows and four
+    // 62; one row by 4096 x 7168 takes 8.0 us with four and 11.7 with two.  Runs of up
+    // to 16 rows of x widen the weights once where an expert has that many, and cost
+    // registers where R could not fill one of 8.
     if (a.K >= 4096)
         return a.R <= 8 ? (wide ? launch<T, 4, 2, 1>(a, s) : launch<T, 4, 1, 1>(a, s))
                         : (wide ? launch<T, 4, 2, 2>(a, s) : launch<T, 4, 1, 2>(a, s));
