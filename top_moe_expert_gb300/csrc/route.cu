@@ -587,8 +587,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
                 const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
                 best_two(b1, b2, o1, o2);
             }
-            const float value = live && a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : live ? b1 : -INFINITY;
-            float g = value, in = -INFINITY;
+            const float whole = live && a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : live ? b1 : -INFINITY;
+            float g = whole, in = -INFINITY;
             live = false;
             for (int j = 0; j < a.topk_groups; ++j) {  // the best of the groups that are left
                 in = warp_max(g);
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
             }
             if (__popc(__ballot_sync(0xffffffffu, live)) != a.topk_groups << a.shift) {
                 // equal groups came in together, or there were none left: one by one, the first of equal ones first
-                g = value;
+                g = whole;
                 live = false;
                 for (int j = 0; j < a.topk_groups; ++j) {
                     in = warp_max(g);
@@ -611,7 +611,38 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
             }
             if (a.bias || two) {
                 const float out = warp_max(g), size = (b1 > -INFINITY ? fabsf(b1) : 0.f) + (b2 > -INFINITY ? fabsf(b2) : 0.f);
-                close = in - out <= 2.f * slack + 0x1p-22f * warp_max(size);
+                const float apart = 2.f * slack + 0x1p-22f * warp_max(size);
+                close = in - out <= apart;
+                if (close && a.sigmoid) {
+                    // the groups that are in or out by less than their errors, by their values in binary64
+                    const bool open = live ? whole - out <= apart : in - whole <= apart;
+                    const int left = __popc(__ballot_sync(0xffffffffu, live && open)) >> a.shift;
+                    float least = a.group_top == 2 ? b2 : b1;
+                    least = fmaxf(least - apart, -FLT_MAX);
+                    Mask<PER> which = 0;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        which |= open && (two ? fast_sigmoid(v[i]) : c[i]) >= least && v[i] > -INFINITY ? static_cast<Mask<PER>>(1) << i : 0;
+                    uint64_t e1 = 0, e2 = 0;
+                    for (; which; which &= which - 1) {
+                        const int e = at.base + first_of(which);
+                        const double x = sigmoid64(value(l[e])) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0);
+                        best_two(e1, e2, order64(x), static_cast<uint64_t>(0));
+                    }
+                    __syncwarp();
+                    for (int o = 1; o < a.lanes; o <<= 1) {
+                        const uint64_t o1 = __shfl_xor_sync(0xffffffffu, e1, o), o2 = __shfl_xor_sync(0xffffffffu, e2, o);
+                        best_two(e1, e2, o1, o2);
+                    }
+                    const uint64_t exact = a.group_top == 2 && e2 ? order64(value64(e1) + value64(e2)) : e1;
+                    int better = 0;
+                    for (int i = 0; i < a.groups; ++i) {
+                        const uint64_t o = __shfl_sync(0xffffffffu, exact, i << a.shift);
+                        better += o > exact || (o == exact && i < at.group);
+                    }
+                    live = open ? better < left : live;
+                    close = false;
+                }
             }
         }
         // a bound of what can be chosen: the last of the best values of as many lanes as are needed
