@@ -60,10 +60,15 @@ __device__ __forceinline__ float warp_max(float v)
 }
 
 // The two best of two pairs (a1 >= a2, b1 >= b2).
-template <typename F>
-__device__ __forceinline__ void best_two(F &a1, F &a2, F b1, F b2)
+__device__ __forceinline__ void best_two(float &a1, float &a2, float b1, float b2)
 {
-    const F lo = a1 < b1 ? a1 : b1, hi = a1 < b1 ? b1 : a1, s = a2 < b2 ? b2 : a2;
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+}
+
+__device__ __forceinline__ void best_two(uint64_t &a1, uint64_t &a2, uint64_t b1, uint64_t b2)
+{
+    const uint64_t lo = a1 < b1 ? a1 : b1, hi = a1 < b1 ? b1 : a1, s = a2 < b2 ? b2 : a2;
     a1 = hi;
     a2 = lo < s ? s : lo;
 }
