@@ -54,7 +54,7 @@ def _logits(M, E, dt, g, std=1.0):
 @pytest.mark.parametrize("E,k,groups,topk_groups", [
     (1, 1, 1, 1), (2, 2, 1, 1), (7, 3, 1, 1), (8, 8, 8, 8), (32, 32, 1, 1), (64, 6, 1, 1), (100, 12, 1, 1), (128, 8, 1, 1),
     (160, 6, 8, 3), (256, 8, 8, 4), (256, 1, 1, 1), (320, 9, 5, 2), (384, 8, 2, 1), (512, 10, 16, 16), (512, 32, 1, 1),
-    (1000, 8, 5, 2), (1003, 8, 17, 9), (1024, 32, 32, 20), (1024, 4, 1, 1), (31, 31, 31, 31)])
+    (1000, 8, 5, 2), (1003, 8, 17, 9), (1024, 12, 8, 1), (512, 12, 16, 4), (512, 20, 4, 1), (1024, 32, 32, 20), (1024, 4, 1, 1), (31, 31, 31, 31)])
 def test_choice_and_weights(dt, E, k, groups, topk_groups):
     g = torch.Generator().manual_seed(E * 100 + k)
     for i, (score, with_bias, top, renorm) in enumerate([(SOFT, 0, 1, True), (SOFT, 0, 2, False), (SIG, 1, 2, True),
@@ -162,6 +162,52 @@ def test_many_tokens():
     s = torch.sigmoid(l.double()) + 0.125
     ids, _ = moe.moe_route(l, 8, score=SIG, bias=torch.full((128,), 0.125, device="cuda"))
     assert torch.equal(ids.long(), torch.sort(s, dim=1, descending=True, stable=True)[1][:, :8])
+
+
+@pytest.mark.parametrize("E,k,groups,topk_groups,top", [(64, 6, 1, 1, 1), (64, 16, 4, 3, 2), (128, 8, 1, 1, 1), (128, 4, 8, 2, 1),
+                                                        (256, 8, 8, 4, 2), (256, 16, 16, 5, 2), (256, 1, 1, 1, 1), (256, 8, 2, 1, 1)])
+def test_many_rows_agree_with_few(E, k, groups, topk_groups, top):
+    """Calls of many tokens, which two of them share a warp's steps in, give each row what a call of few gives it: random
+    logits, equal ones, nearly equal ones, masks that leave a part or nothing, NaN; an odd number of rows."""
+    g = torch.Generator().manual_seed(E + k + groups)
+    for dt in (F32, BF):
+        few = _logits(150, E, dt, g)
+        few[20:30] = (few[20:30] * 2).round() / 2
+        few[30:40] = 0.625 + (torch.randint(-3, 4, (10, E), generator=g) * 2.0 ** -24)
+        few[40] = -INF
+        few[41:50, E // 3:] = -INF
+        few[50:60, ::2] = -INF
+        few[60, 1:] = -INF
+        few[61, 3], few[62, 5] = float("nan"), INF
+        few[63] = torch.finfo(dt).min
+        few[64:70] = 1e-40 * torch.randint(-3, 4, (6, E), generator=g).float()
+        few[70:80] = few[70:80] * 30
+        few = few.to(dt)
+        order = torch.cat([torch.arange(150), torch.randint(0, 150, (9001,), generator=g)])
+        many = few[order].cuda()
+        b = 0.05 * torch.randn(E, generator=g)
+        off = b.clone()
+        off[5:9] = -INF
+        for kw in (dict(score=SIG, bias=b, scale=2.5), dict(score=SIG, bias=torch.zeros(E)), dict(score=SOFT, bias=off, renorm=False),
+                   dict(score=SOFT, renorm=False), dict(score=SIG), dict()):
+            kw = {n: _dev(v) if n == "bias" else v for n, v in kw.items()}
+            kw.update(groups=groups, topk_groups=topk_groups, group_top=top)
+            i1, w1 = moe.moe_route(few.cuda(), k, **kw)
+            i2, w2 = moe.moe_route(many, k, **kw)
+            assert torch.equal(i2, i1[order.cuda()])
+            w1 = w1[order.cuda()]
+            assert torch.equal(w1.isnan(), w2.isnan())
+            span = 110.0
+            assert ((w1 - w2).abs().nan_to_num() <= 2 * (40 + E / 16 + span / 2) * 2.0 ** -23 * w1.abs().nan_to_num() + 1e-36).all()
+
+
+def test_subnormal_logits():
+    """Maxima of subnormal logits, of either sign, are found."""
+    l = torch.tensor([[1e-40, 3e-40, 2e-40, -1e-40], [-1e-40, -3e-40, -2e-40, -4e-40]]).repeat(1, 8)
+    for dt in (F32, BF):
+        x = l.to(dt)
+        for kw in (dict(), dict(groups=4, topk_groups=2), dict(groups=4, topk_groups=2, group_top=2, score=SIG)):
+            assert torch.equal(moe.moe_route(x.cuda(), 3, **kw)[0].cpu().long(), ref.route(x, 3, **kw)[0])
 
 
 def test_load_is_added():

@@ -503,10 +503,10 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
     float b[PER];
     if (kKeep && a.bias)
         load_row<float, PER, FULL>(a.bias + at.base, at.count, b);
-    const uint32_t step = gridDim.x * kWarps, begin = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t M = a.M, step = gridDim.x * kWarps, begin = blockIdx.x * kWarps + (threadIdx.x >> 5);
     bool later = false;
 
-    for (uint32_t t = begin; t < static_cast<uint32_t>(a.M); t += step) {
+    for (uint32_t t = begin; t < M; t += step) {
         const T *l = static_cast<const T *>(a.logits) + static_cast<int64_t>(t) * a.E;
         float v[PER], c[PER];
         load_row<T, PER, FULL>(l + at.base, at.count, v);
@@ -576,12 +576,14 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
             for (int i = 0; i < PER; ++i)
                 b1 = fmaxf(b1, v[i]);
         }
-        float top = b1;                                // of what experts are chosen by
+        float top = b1, second = b2;                   // the lane's best, of what experts are chosen by
         if (!a.bias) {
-            top = -INFINITY;
+            top = second = -INFINITY;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 c[i] = v[i];
+                if (a.groups > 1)                      // all lanes are in otherwise, mostly more than are needed
+                    second = fmaxf(second, fminf(top, v[i]));
                 top = fmaxf(top, v[i]);
             }
         }
@@ -607,8 +609,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
                 live = false;
                 for (int j = 0; j < a.topk_groups; ++j) {
                     in = warp_max(g);
-                    const int first = __ffs(__ballot_sync(0xffffffffu, g == in)) - 1;
-                    if (in > -INFINITY && (lane ^ first) >> a.shift == 0) {
+                    const int best = __ffs(__ballot_sync(0xffffffffu, g == in)) - 1;
+                    if (in > -INFINITY && (lane ^ best) >> a.shift == 0) {
                         live = true;
                         g = -INFINITY;
                     }
@@ -650,14 +652,32 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
                 }
             }
         }
-        // a bound of what can be chosen: the last of the best values of as many lanes as are needed
+        // a bound of what can be chosen: as many of the lanes' two best as are needed are not below it
         float bound = -INFINITY;
         if (!live)
-            top = -INFINITY;
+            top = second = -INFINITY;
 #pragma unroll 3
-        for (int j = 0; j < rounds; ++j) {             // (fewer lanes than that: -inf, no bound)
+        for (int j = 0; j < rounds; ++j) {             // (fewer than that: -inf, no bound)
             bound = warp_max(top);
-            top = top == bound ? -INFINITY : top;
+            const bool is = top == bound;
+            top = is ? second : top;
+            second = is ? -INFINITY : second;
+        }
+        if (bound == -INFINITY && __popc(__ballot_sync(0xffffffffu, live)) * a.per > kMaxFound) {
+            // few lanes, of one or two groups, with many experts each: their values in turn
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                top = live ? fmaxf(top, c[i]) : top;
+            for (int j = 0; j < rounds; ++j) {
+                bound = warp_max(top);
+                if (top == bound) {
+                    top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        top = c[i] < bound ? fmaxf(top, c[i]) : top;
+                }
+            }
         }
         if (a.bias)                                    // and what may be as good
             bound -= slack + 0x1p-22f * fabsf(bound);
@@ -678,80 +698,81 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
         bool near = false;                             // the order may not be the exact values'
         int slot = -1;
         float my_l = 0.f;
-        if (found <= kMaxFound) {
+        const int n = found <= kMaxFound ? found : 0;  // more: all that equal values
+        if (n)
             for (to -= own; which; which &= which - 1)
                 slots.expert[to++] = at.base + first_of(which);
-            __syncwarp();
-            // each lane takes one, or two, and finds its rank; equal ones are in order already
-            for (int i = lane; i < found; i += 32) {
-                const int e = slots.expert[i];
-                const float x = value(l[e]);
-                float y = x;
-                if (a.bias)
-                    y = (a.sigmoid ? fast_sigmoid(x) : __expf(x - m) * rz) + a.bias[e];
-                slots.found[i] = key64(y, i);
-            }
-            __syncwarp();
-            for (int i = lane; i < found; i += 32) {
-                const uint64_t mine = slots.found[i];
-                int rank = 0, j = 0;
-                for (; j + 4 <= found; j += 4)
+        __syncwarp();
+        // each lane takes one after the other, and finds its rank; equal ones are in order already
+        for (int i = lane; i < n; i += 32) {
+            const int e = slots.expert[i];
+            const float x = value(l[e]);
+            float y = x;
+            if (a.bias)
+                y = (a.sigmoid ? fast_sigmoid(x) : __expf(x - m) * rz) + a.bias[e];
+            slots.found[i] = key64(y, i);
+        }
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) {
+            const uint64_t own = slots.found[i];
+            int rank = 0, j = 0;
+            for (; j + 4 <= n; j += 4)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        rank += slots.found[j + u] > mine;
-                for (; j < found; ++j)
-                    rank += slots.found[j] > mine;
-                if (rank <= a.k)
-                    slots.sorted[rank] = mine;
+                for (int u = 0; u < 4; ++u)
+                    rank += slots.found[j + u] > own;
+            for (; j < n; ++j)
+                rank += slots.found[j] > own;
+            if (rank <= a.k)
+                slots.sorted[rank] = own;
+        }
+        __syncwarp();
+        if (lane < min(a.k, n)) {
+            const uint64_t own = slots.sorted[lane];
+            slot = slots.expert[index_of(own)];
+            my_l = value(l[slot]);
+            if (a.bias && lane + 1 < n) {
+                const uint64_t after = slots.sorted[lane + 1];
+                const float x = value_of(own), y = value_of(after);
+                // equal inputs have equal values, and are in order
+                if (x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y))) {
+                    const int e = slots.expert[index_of(after)];
+                    near = my_l != value(l[e]) || a.bias[slot] != a.bias[e];
+                }
+            }
+        }
+        bool undecided = found > kMaxFound || close;
+        if (__any_sync(0xffffffffu, near)) {
+            undecided = undecided || !a.sigmoid;
+            // the candidates' values in binary64, one to a lane
+            const int again = a.sigmoid ? n : 0;
+            for (int i = lane; i < again; i += 32) {
+                const int e = slots.expert[i];
+                slots.found[i] = order64(sigmoid64(value(l[e])) + static_cast<double>(a.bias[e]));
             }
             __syncwarp();
-            if (lane < min(a.k, found)) {
-                const uint64_t mine = slots.sorted[lane];
-                slot = slots.expert[index_of(mine)];
+            for (int i = lane; i < again; i += 32) {
+                int rank = 0;
+                for (int j = 0; j < again; ++j)
+                    rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && j < i);
+                if (rank < a.k)
+                    slots.sorted[rank] = slots.expert[i];
+            }
+            __syncwarp();
+            if (lane < min(a.k, again)) {
+                slot = static_cast<int>(slots.sorted[lane]);
                 my_l = value(l[slot]);
-                if (a.bias && lane + 1 < found) {
-                    const uint64_t after = slots.sorted[lane + 1];
-                    const float x = value_of(mine), y = value_of(after);
-                    // equal inputs have equal values, and are in order
-                    if (x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y))) {
-                        const int e = slots.expert[index_of(after)];
-                        near = my_l != value(l[e]) || a.bias[slot] != a.bias[e];
-                    }
-                }
             }
         }
-        near = __any_sync(0xffffffffu, near);
-        if (found > kMaxFound || __any_sync(0xffffffffu, close) || (near && !a.sigmoid)) {
-            later = true;
-            if (lane == 0)
-                a.ids[static_cast<int64_t>(t) * a.k] = kLater;
-        } else {
-            if (near) {
-                // the candidates' values in binary64, one to a lane
-                for (int i = lane; i < found; i += 32) {
-                    const int e = slots.expert[i];
-                    slots.found[i] = order64(sigmoid64(value(l[e])) + static_cast<double>(a.bias[e]));
-                }
-                __syncwarp();
-                for (int i = lane; i < found; i += 32) {
-                    int rank = 0;
-                    for (int j = 0; j < found; ++j)
-                        rank += slots.found[j] > slots.found[i] || (slots.found[j] == slots.found[i] && j < i);
-                    if (rank < a.k)
-                        slots.sorted[rank] = slots.expert[i];
-                }
-                __syncwarp();
-                if (lane < min(a.k, found)) {
-                    slot = static_cast<int>(slots.sorted[lane]);
-                    my_l = value(l[slot]);
-                }
-            }
-            put(a, t, slot, weight(a.sigmoid, a.renorm, a.scale, my_l, slot >= 0, m, z), __any_sync(0xffffffffu, bad), lane, load);
-        }
+        const float w = weight(a.sigmoid, a.renorm, a.scale, my_l, slot >= 0, m, z);
+        if (!undecided)
+            put(a, t, slot, w, __any_sync(0xffffffffu, bad), lane, load);
+        else if (lane == 0)
+            a.ids[static_cast<int64_t>(t) * a.k] = kLater;
+        later = later || undecided;
         __syncwarp();                                  // the slots are the next token's
     }
     if (later)
-        for (uint32_t t = begin; t < static_cast<uint32_t>(a.M); t += step) {
+        for (uint32_t t = begin; t < M; t += step) {
             if (a.ids[static_cast<int64_t>(t) * a.k] == kLater)
                 route_exact<T>(a, t, slots, load, lane);
             __syncwarp();
