@@ -11,12 +11,22 @@
 //
 // What is compared are the values in binary64.  A warp takes a token and forms
 // them in binary32; where two that decide something are nearer than their errors
-// can be (a share of about 1e-3 of the tokens at logits of spread 1), it forms
-// that token's anew in binary64.  Logits without a bias are compared as they are.
+// can be (a share of about 1e-3 of the tokens at logits of spread 1), those and
+// their rivals alone are formed anew in binary64, whose instructions take a warp some
+// 60 cycles each.  Logits without a bias are compared as they are.
 //
 // A lane holds consecutive experts of one group, and a group takes a power of two
 // of neighbouring lanes, so that the lowest lane that holds a maximum also holds
 // the lowest index.
+//
+// Bound by instruction issue (0.73 per cycle and scheduler), some 650 of a warp for a
+// token of 256 experts: 50 for the loads, 110 for the scores, 140 for the groups, 90
+// for the bound, 90 to collect what is above it, 160 to rank it, 100 for the weights.
+// 65536 tokens, 8 of 256 in 4 of 8 groups, bf16 with a bias: 55.1 us, where the bytes
+// take 5.6; 4096 tokens, 8 of 128, FP32: 4.8 us.  Before: k rounds of a maximum over
+// sorted lanes 100 us; candidates placed by a ballot for each of a lane's experts 74;
+// all of an undecided token in binary64 at the end 69.  Two tokens in the halves of a
+// warp, whose maxima take shuffles, gained nothing (52 us against 48 without groups).
 #include <cfloat>
 #include <climits>
 #include <type_traits>
