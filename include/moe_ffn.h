@@ -575,7 +575,7 @@ moe_status_t moe_swiglu_dropout_bwd(const void *dh, const void *gu, int32_t dt, 
  * Codes less their zero and their products with x are exact, each group of 128
  * is one FP32 sum of the tensor cores, times its scale in FP32, and the groups
  * are added in FP32; y is rounded once.  The same call gives the same bits.
- * Every further 32 rows of an expert read its weights again (from the L2 where
+ * Every further 16 rows of an expert read its weights again (from the L2 where
  * they fit): for many rows use moe_ffn_grouped or 16-bit weights.
  * R = 0 is a no-op.  Limits: E <= 1024, R, N and E (R / 8 + 1) <= 2^31 - 1024,
  * K <= 2^24 (MOE_ERR_UNSUPPORTED); x, y and w's tensors 16-byte aligned (MOE_ERR_INVALID_ARG). */

@@ -286,10 +286,11 @@ __global__ void __launch_bounds__(32 * W, (W == 2 && MT * NT == 1 ? 24 : 16) / W
     const uint8_t *ring = rings + warp * D * kStage<MT>;
     const int n0 = blockIdx.x * kRowsW, G = a.K / 128;
     const int k0 = G * warp / W, k1 = G * (warp + 1) / W;
-    const int first = clamp_off(a, 0), last = clamp_off(a, a.E), outside = first + a.R - last;
-    for (int slot = blockIdx.y, runs = slot + 1; slot < runs; slot += gridDim.y) {
+    const int first = clamp_off(a, 0), last = clamp_off(a, a.E);
+    const int64_t outside = static_cast<int64_t>(first) + a.R - last;
+    for (int64_t slot = blockIdx.y, runs = slot + 1; slot < runs; slot += gridDim.y) {
         if (warp == 0) {
-            const Run f = find_run(a, slot, 8 * NT, lane);
+            const Run f = find_run(a, static_cast<int>(slot), 8 * NT, lane);
             if (lane == 0)
                 s_run = f;
         }
@@ -340,14 +341,15 @@ __global__ void __launch_bounds__(32 * W, (W == 2 && MT * NT == 1 ? 24 : 16) / W
         __syncthreads();
     }
     // rows outside every group, divided among the CTAs of a column of tiles
-    for (int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < static_cast<int64_t>(outside) * kRowsW;
+    for (int64_t i = static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x; i < outside * kRowsW;
          i += static_cast<int64_t>(gridDim.y) * kThreads) {
-        const int n = n0 + static_cast<int>(i & (kRowsW - 1)), j = static_cast<int>(i / kRowsW), r = j < first ? j : last + j - first;
+        const int n = n0 + static_cast<int>(i & (kRowsW - 1));
+        const int64_t j = i / kRowsW, r = j < first ? j : last + j - first;
         if (n < a.N) {
             if (a.y32)
-                static_cast<float *>(a.y)[static_cast<int64_t>(r) * a.N + n] = 0.f;
+                static_cast<float *>(a.y)[r * a.N + n] = 0.f;
             else
-                static_cast<T *>(a.y)[static_cast<int64_t>(r) * a.N + n] = fp4::from_float<T>(0.f);
+                static_cast<T *>(a.y)[r * a.N + n] = fp4::from_float<T>(0.f);
         }
     }
     if (blockIdx.x == 0 && blockIdx.y == 0)
