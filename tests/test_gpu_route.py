@@ -251,6 +251,25 @@ def test_gradient(dt, score, renorm, M, E, k):
     assert not dl.cpu()[l == -INF].any()
 
 
+@pytest.mark.parametrize("E", [64, 100, 128, 256, 512])
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_masked_rows(E, score, renorm):
+    """A token without any expert gets zeros, beside others, one expert alone its own gradient."""
+    g = torch.Generator().manual_seed(E)
+    for dt in (F32, BF):
+        l, dw = _logits(7, E, dt, g), torch.randn((7, 4), generator=g)
+        l[1] = l[6] = -INF
+        l[3, 1:] = -INF
+        l[4] = torch.finfo(dt).min
+        ids, _ = moe.moe_route(l.cuda(), 4, score=score, renorm=renorm)
+        dl = moe.moe_route_bwd(dw.cuda(), l.cuda(), ids, score=score, renorm=renorm).cpu()
+        assert not dl[[1, 6]].any() and torch.isfinite(dl).all()
+        want, mag = ref.route_bwd(dw, l, ids.cpu().long(), score, renorm, 1.0)
+        off = (dl.double() - want).abs() - _grad_bound(want, mag, l.double(), E, dt)
+        assert not (off[[0, 2, 3, 4, 5]] > 0).any(), float(off.max())
+
+
 @pytest.mark.parametrize("score", [SOFT, SIG])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_gradient_of_given_ids(score, renorm):
@@ -284,6 +303,18 @@ def test_gradient_against_differences(score, renorm):
         h = 1e-4
         diff = (f(l.double() + h * d) - f(l.double() - h * d)) / (2 * h)
         assert abs(diff - float((leaf.grad.cpu().double() * d).sum())) < 1e-5 + 40 * float(dw.abs().sum()) * h * h
+
+
+def test_two_calls_at_once_share_a_load():
+    """Whole numbers added from two streams at a time."""
+    g = torch.Generator().manual_seed(31)
+    l = _logits(20000, 64, BF, g).cuda()
+    load, side = torch.zeros(64, dtype=torch.int32, device="cuda"), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [moe.moe_route(l, 6, load=load, stream=s) for s in (None, side) * 3]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1]) for o in outs)
+    assert torch.equal(load.long(), 6 * torch.bincount(outs[0][0].flatten().long(), minlength=64))
 
 
 # ---------------------------------------------------------------- streams, graphs, repeatability

@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32) route_bwd_kernel(const BwdArgs
     if (e >= 0)
         row[PER ? place_of<kOwn>(e) : e] = g;
     __syncwarp();
-    const float f = sum / z;
+    const float f = z > 0.f ? sum / z : 0.f;           // z is 0 where no expert is left, else at least 1
     if constexpr (PER > 0) {
         float d[kOwn];
 #pragma unroll
