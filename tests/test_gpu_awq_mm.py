@@ -47,6 +47,21 @@ def test_exact_sums(dt, sizes, N, K):
 
 
 @pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("sizes,N,K", [([3], 8, 131072), ([700, 0, 813], 136, 256), ([1] * 1024, 8, 128), ([0] * 1023 + [17], 40, 128)],
+                         ids=["long", "many rows", "an expert each", "the last expert"])
+def test_extreme_sizes(dt, sizes, N, K):
+    """Exact sums as above: x up to 1 over the long ones."""
+    g = torch.Generator().manual_seed(N + K)
+    E, R, top = len(sizes), sum(sizes) + 1, 1 if K > 10000 else 4
+    w, values = _weights(E, N, K, g, [0.5, 1.0, 2.0])
+    x = torch.randint(-top, top + 1, (R, K), generator=g).to(dt)
+    want, mag = rr.mm(x, values, sizes)
+    assert mag.max() < 2 ** 23
+    y = moe.moe_grouped_mm_awq(x.cuda(), w, rr.offsets_of(sizes).cuda(), out_dtype=F32)
+    assert torch.equal(y.cpu(), want.float())
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
 @pytest.mark.parametrize("sizes,N,K", [([1], 4096, 7168), ([8, 0, 1, 33], 72, 2048), ([5], 256, 16384), ([20, 70], 512, 768),
                                        ([1] * 64, 40, 384)])
 def test_normal_inputs(dt, sizes, N, K):

@@ -44,7 +44,8 @@ def _check(R, I, p, dt, seed=1, offset=0, std=1.0, g=None):
 
 
 @pytest.mark.parametrize("dt", [BF, F16, F32])
-@pytest.mark.parametrize("R,I", [(1, 1), (1, 8), (3, 7), (2, 16), (5, 129), (37, 1001), (64, 768), (300, 24), (1025, 40), (9, 4096)])
+@pytest.mark.parametrize("R,I", [(1, 1), (1, 8), (3, 7), (2, 16), (5, 129), (37, 1001), (64, 768), (300, 24), (1025, 40), (9, 4096), (2, 1 << 20),
+                                 (3, (1 << 18) + 3), (70000, 8), (70001, 3)])
 def test_values_and_gradients(dt, R, I):
     for p in (0.0, 0.1, 0.5, 1e-6, 0.9999):
         _check(R, I, p, dt, seed=R * 1000 + I, offset=3)
