@@ -604,7 +604,9 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
                 const float o1 = __shfl_xor_sync(0xffffffffu, b1, o), o2 = __shfl_xor_sync(0xffffffffu, b2, o);
                 best_two(b1, b2, o1, o2);
             }
-            const float whole = live && a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : live ? b1 : -INFINITY;
+            // half the sum of the two best: it stays finite whatever the biases, and groups without experts alone are at -inf
+            const float part = a.group_top == 2 ? 0.5f : 1.f;
+            const float h1 = part * b1, h2 = a.group_top == 2 && b2 > -INFINITY ? part * b2 : 0.f, whole = h1 + h2;
             float g = whole, in = -INFINITY;
             live = false;
             for (int j = 0; j < a.topk_groups; ++j) {  // the best of the groups that are left
@@ -627,15 +629,15 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
                 }
             }
             if (a.bias || two) {
-                const float out = warp_max(g), size = (b1 > -INFINITY ? fabsf(b1) : 0.f) + (b2 > -INFINITY ? fabsf(b2) : 0.f);
-                const float apart = 2.f * slack + 0x1p-22f * warp_max(size);
+                const float size = h1 > -INFINITY ? fabsf(h1) + fabsf(h2) : 0.f;
+                const float out = warp_max(g), apart = slack + 0x1p-22f * warp_max(size);
                 close = in - out <= apart;
                 if (close && a.sigmoid) {
                     // the groups that are in or out by less than their errors, by their values in binary64
                     const bool open = live ? whole - out <= apart : in - whole <= apart;
                     const int left = __popc(__ballot_sync(0xffffffffu, live && open)) >> a.shift;
                     float least = a.group_top == 2 ? b2 : b1;
-                    least = fmaxf(least - apart, -FLT_MAX);
+                    least = fmaxf(least - 2.f * apart, -FLT_MAX);
                     Mask<PER> which = 0;
 #pragma unroll
                     for (int i = 0; i < PER; ++i)
