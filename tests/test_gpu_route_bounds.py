@@ -52,3 +52,17 @@ def test_biases_of_any_finite_size(score, top, E, k, groups, topk_groups):
         assert torch.equal(ids.cpu().long()[clear], rids[clear]), (i, ids.cpu()[clear][:2], rids[clear][:2])
         off = (w.cpu().double() - rw).abs() - _weight_bound(l.double(), rw, E)
         assert not (off[clear] > 0).any(), (i, float(off[clear].max()))
+
+
+def test_most_rows_there_can_be():
+    """M * k just below 2^31: a row for every count of 32 bits, in both directions.  Sigmoid of 0: w = 1/2, dl = dw / 4."""
+    M = 2 ** 31 - 1
+    l = torch.zeros((M, 1), dtype=torch.bfloat16, device="cuda")
+    load = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ids, w = moe.moe_route(l, 1, score=SIG, renorm=False, load=load)
+    assert load.item() == M and not ids.any() and (w == 0.5).all()
+    del w
+    dw = torch.ones((M, 1), device="cuda")
+    dl = torch.full((M, 1), float("nan"), dtype=torch.bfloat16, device="cuda")
+    moe.moe_route_bwd(dw, l, ids, score=SIG, renorm=False, dlogits=dl)
+    assert (dl == 0.25).all()

@@ -1043,7 +1043,8 @@ MOE_API moe_status_t moe_route_bwd(const float *dw, const void *logits, int32_t 
         !aligned(dlogits, size))
         return MOE_ERR_INVALID_ARG;
     const route::BwdArgs a{dw, logits, topk_ids, M, E, k, score == MOE_SCORE_SIGMOID, renorm, scale, dlogits};
-    const dim3 grid((M + route::kBwdWarps - 1) / route::kBwdWarps), block(route::kBwdWarps * 32);
+    const int64_t ctas = (static_cast<int64_t>(M) + route::kBwdWarps - 1) / route::kBwdWarps;
+    const dim3 grid(static_cast<unsigned>(ctas)), block(route::kBwdWarps * 32);
     const size_t smem = sizeof(float) * route::kBwdWarps * E;                  // at most 16 KB
     cudaStream_t s = as_stream(stream);
     const cudaError_t e = ldt == MOE_BF16   ? route::launch_bwd<__nv_bfloat16>(a, grid, block, smem, s)
