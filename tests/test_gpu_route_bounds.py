@@ -66,3 +66,56 @@ def test_most_rows_there_can_be():
     dl = torch.full((M, 1), float("nan"), dtype=torch.bfloat16, device="cuda")
     moe.moe_route_bwd(dw, l, ids, score=SIG, renorm=False, dlogits=dl)
     assert (dl == 0.25).all()
+
+
+def _hard_rows(E, g):
+    """Rows whose choice binary32 does not settle, beside ordinary ones: equal logits (more candidates than a warp's lanes
+    hold), nearly equal ones, masks, NaN."""
+    l = torch.randn((90, E), generator=g)
+    l[0:20] = 0.0
+    l[20:40] = 0.625 + torch.randint(-3, 4, (20, E), generator=g) * 2.0 ** -24
+    l[40:45] = -float("inf")
+    l[45:50, E // 3:] = -float("inf")
+    l[50:55] = -TOP
+    l[55, 3] = float("nan")
+    l[56:60, 1:] = -float("inf")
+    return l
+
+
+HARD = [dict(), dict(score=SOFT, bias=0.0), dict(score=SIG, bias=0.0), dict(score=SOFT, renorm=False),
+        dict(score=SOFT, bias=0.0, groups=8, topk_groups=3, group_top=2), dict(score=SIG, bias=0.0, groups=8, topk_groups=3, group_top=2),
+        dict(score=SOFT, groups=4, topk_groups=2, group_top=2), dict(score=SIG, groups=4, topk_groups=2, group_top=1)]
+
+
+@pytest.mark.parametrize("E,k", [(128, 8), (160, 6), (384, 8), (1024, 32)])
+@pytest.mark.parametrize("how", HARD, ids=str)
+def test_load_counts_every_slot_once(E, k, how):
+    """Tokens whose choice is settled in a second pass are counted there alone."""
+    g = torch.Generator().manual_seed(E + k)
+    l = _hard_rows(E, g)[torch.randint(0, 90, (6001,), generator=g)].cuda()
+    how = dict(how)
+    if "bias" in how:
+        how["bias"] = (torch.randint(-3, 4, (E,), generator=g) * 2.0 ** -27).cuda()
+    load = torch.full((E,), 5, dtype=torch.int32, device="cuda")
+    ids, _ = moe.moe_route(l, k, load=load, **how)
+    v = ids.long().flatten()
+    assert ((v >= -1) & (v < E)).all()
+    assert torch.equal(load.long(), 5 + torch.bincount(v[v >= 0], minlength=E))
+
+
+@pytest.mark.parametrize("E,k", [(128, 8), (160, 6), (384, 8), (1024, 32)])
+@pytest.mark.parametrize("how", HARD, ids=str)
+def test_a_row_has_the_same_bits_beside_others(E, k, how):
+    g = torch.Generator().manual_seed(E + k + 1)
+    few = _hard_rows(E, g)
+    order = torch.cat([torch.arange(90), torch.randint(0, 90, (9001,), generator=g)]).cuda()
+    how = dict(how)
+    if "bias" in how:
+        how["bias"] = (torch.randint(-3, 4, (E,), generator=g) * 2.0 ** -27).cuda()
+    few = few.cuda()
+    i1, w1 = moe.moe_route(few, k, **how)
+    i2, w2 = moe.moe_route(few[order], k, **how)
+    assert torch.equal(i2, i1[order]) and torch.equal(w2.view(torch.int32), w1[order].view(torch.int32))
+    for r in (0, 25, 42, 47, 55, 57, 70):
+        i, w = moe.moe_route(few[r:r + 1].contiguous(), k, **how)
+        assert torch.equal(i[0], i1[r]) and torch.equal(w[0].view(torch.int32), w1[r].view(torch.int32))
