@@ -119,3 +119,36 @@ def test_a_row_has_the_same_bits_beside_others(E, k, how):
     for r in (0, 25, 42, 47, 55, 57, 70):
         i, w = moe.moe_route(few[r:r + 1].contiguous(), k, **how)
         assert torch.equal(i[0], i1[r]) and torch.equal(w[0].view(torch.int32), w1[r].view(torch.int32))
+
+
+@pytest.mark.parametrize("score", [SOFT, SIG])
+@pytest.mark.parametrize("E,groups,topk_groups", [(2, 1, 1), (6, 1, 1), (32, 1, 1), (40, 1, 1), (60, 4, 3), (64, 8, 5), (256, 16, 3)])
+def test_few_distinct_values(score, E, groups, topk_groups):
+    """Runs of experts with the same logit and bias that reach past the last slot, and others, lower or higher by less than
+    binary32 tells apart, behind them: logits a few units in the last place apart, sigmoids near 1 and scores near 0,
+    biases that take the scores' bits away.  (Differences in binary64: 1e-8 of scores near 1/2; 1e-9 of sigmoids at 17;
+    beside a bias of 10^4 they are those of scores 0.1 apart.)"""
+    g = torch.Generator().manual_seed(E)
+    for base, step, shift in ((0.625, 2.0 ** -24, 0.0), (17.0, 0.25, 0.0), (-22.0, 0.25, 0.0), (0.0, 0.5, 1e4), (0.0, 0.5, -1e4)):
+        if score == SOFT and base == 17.0:
+            continue
+        for kinds in (2, 3):
+            l = base + step * torch.randint(0, kinds, (60, E), generator=g).float()
+            l[::4] = base
+            l[::4, -1] += step                                         # the best one is the last
+            if base == -22.0 and score == SOFT:
+                l[:, 0] = 0.0                                          # the others' scores are near 0
+            b = torch.full((E,), shift)
+            if kinds == 3:
+                b[torch.rand(E, generator=g) < 0.3] += 0.25
+            for k in (1, 2, 3, 8, 16):
+                if k > topk_groups * (E // groups):
+                    continue
+                kw = dict(score=score, groups=groups, topk_groups=topk_groups, group_top=1 + k % 2)
+                ids, w = moe.moe_route(l.cuda(), k, bias=b.cuda(), **kw)
+                rids, rw, gap = ref.route(l, k, bias=b, **kw)
+                clear = gap > 1e-13 * (1 + abs(shift))
+                assert clear.double().mean() > 0.5
+                assert torch.equal(ids.cpu().long()[clear], rids[clear]), (base, shift, k, (ids.cpu() != rids).any(dim=1).nonzero()[:4])
+                off = (w.cpu().double() - rw).abs() - _weight_bound(l.double(), rw, E)
+                assert not (off[clear] > 0).any(), (base, shift, k, float(off[clear].max()))

@@ -410,6 +410,24 @@ __device__ __noinline__ void route_exact(const Args &a, uint32_t t, Slots &slots
     __syncwarp();
 }
 
+// Whether any of the n candidates behind the expert of the last slot is nearer to it
+// than the values' errors, and not by equal inputs, whose order is known.
+template <typename T>
+__device__ __noinline__ bool others_near(const Args &a, const T *l, const Slots &slots, int n, float slack, int lane)
+{
+    const uint64_t last = slots.sorted[a.k - 1];
+    const float x = value_of(last);
+    const int e = slots.expert[index_of(last)];
+    bool near = false;
+    for (int i = lane; i < n; i += 32) {
+        const float y = value_of(slots.found[i]);
+        const int o = slots.expert[i];
+        if (slots.found[i] < last && x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y)))
+            near = near || value(l[e]) != value(l[o]) || a.bias[e] != a.bias[o];
+    }
+    return __any_sync(0xffffffffu, near);
+}
+
 // A bit for each of a lane's experts.
 template <int PER>
 using Mask = std::conditional_t<(PER > 32), uint64_t, uint32_t>;
@@ -745,18 +763,19 @@ __global__ void __launch_bounds__(kWarps * 32, PER <= 8 ? 2 : 1) route_kernel(co
             if (a.bias && lane + 1 < n) {
                 const uint64_t after = slots.sorted[lane + 1];
                 const float x = value_of(own), y = value_of(after);
-                // equal inputs have equal values, and are in order
+                // equal inputs have equal values, and are in order; behind the last slot others may follow them
                 if (x - y <= slack + 0x1p-23f * fmaxf(fabsf(x), fabsf(y))) {
                     const int e = slots.expert[index_of(after)];
-                    near = my_l != value(l[e]) || a.bias[slot] != a.bias[e];
+                    near = my_l != value(l[e]) || a.bias[slot] != a.bias[e] || lane == a.k - 1;
                 }
             }
         }
         bool undecided = found > kMaxFound || close;
         if (__any_sync(0xffffffffu, near)) {
-            undecided = undecided || !a.sigmoid;
+            near = __any_sync(0xffffffffu, near && lane != a.k - 1) || others_near<T>(a, l, slots, n, slack, lane);
+            undecided = undecided || (near && !a.sigmoid);
             // the candidates' values in binary64, one to a lane
-            const int again = a.sigmoid ? n : 0;
+            const int again = near && a.sigmoid ? n : 0;
             for (int i = lane; i < again; i += 32) {
                 const int e = slots.expert[i];
                 slots.found[i] = order64(sigmoid64(value(l[e])) + static_cast<double>(a.bias[e]));
