@@ -152,3 +152,25 @@ def test_few_distinct_values(score, E, groups, topk_groups):
                 assert torch.equal(ids.cpu().long()[clear], rids[clear]), (base, shift, k, (ids.cpu() != rids).any(dim=1).nonzero()[:4])
                 off = (w.cpu().double() - rw).abs() - _weight_bound(l.double(), rw, E)
                 assert not (off[clear] > 0).any(), (base, shift, k, float(off[clear].max()))
+
+
+def test_weights_of_tiny_sigmoids():
+    """Renormalised weights keep their relative accuracy where some of the chosen sigmoids are below FP32's normal range
+    and their sum is tiny too; the gradient's terms likewise.  All experts are chosen.  (4e-37: scores below 2^-126 are off
+    by 2 units of 2^-149, times the scale 2 over a sum of at least e^-18; in the gradient times |dw| and its mean, below 10
+    together.)"""
+    g = torch.Generator().manual_seed(5)
+    top = torch.cat([torch.arange(-64.0, -10.0, 0.5), torch.tensor([0.0, 5.0])])
+    l = top[:, None] - 85.0 * torch.rand((top.numel(), 32), generator=g)
+    l[:, 0] = top
+    ids, w = moe.moe_route(l.cuda(), 32, score=SIG, scale=2.0)
+    rids, rw, _ = ref.route(l, 32, score=SIG, scale=2.0)
+    assert torch.equal(ids.cpu().long(), rids)
+    # the chosen logits span up to 85: exp of such an argument is off by 85 / 2 units, by itself 40 more with the sum
+    off = (w.cpu().double() - rw).abs() - (40 + 32 / 16 + 85 / 2) * 2.0 ** -23 * rw - 4e-37
+    assert not (off > 0).any(), (float(off.max()), (off > 0).nonzero()[:4])
+    dw = torch.randn((top.numel(), 32), generator=g)
+    dl = moe.moe_route_bwd(dw.cuda(), l.cuda(), ids, score=SIG, scale=2.0).cpu().double()
+    want, mag = ref.route_bwd(dw, l, rids, SIG, True, 2.0)
+    off = (dl - want).abs() - (100 + 32 / 8 + 2 * 85) * 2.0 ** -23 * mag - 4e-36
+    assert not (off > 0).any(), float(off.max())

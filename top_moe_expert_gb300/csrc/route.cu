@@ -110,12 +110,13 @@ __device__ __forceinline__ float weight(bool sigmoid_score, bool renorm, float s
         const float s = sigmoid_score ? sigmoid(l) : expf(l - m) / z;
         return live ? s * scale : 0.f;
     }
-    // the chosen scores over their sum.  Sigmoids of logits below -60 are exp(l)
-    // to within 2^-86, and a softmax of the logits does not lose them to zero.
+    // the chosen scores over their sum.  Sigmoids of logits below -18 are exp(l) to
+    // within 2^-25, and a softmax of the logits loses none of them, nor their bits to
+    // the subnormal range, before it is divided.
     const float top = warp_max(live ? l : -INFINITY);
-    const float s = !live ? 0.f : sigmoid_score && top > -60.f ? sigmoid(l) : expf(l - top);
+    const float s = !live ? 0.f : sigmoid_score && top > -18.f ? sigmoid(l) : expf(l - top);
     const float sum = warp_sum(s);
-    return live ? __fdividef(s, sum) * scale : 0.f;         // sum is at least e^-60 / 2
+    return live ? __fdividef(s, sum) * scale : 0.f;         // sum is at least e^-18 / 2
 }
 
 // A token's candidates, one to a lane or two; then in their order.
