@@ -15,18 +15,23 @@
 // The order of k inside a group is free as long as both operands agree: lane t of
 // a row's four takes 16 bytes of codes, k = 32 t .. 32 t + 31, and of each word of
 // 8 the pairs (0, 4), (1, 5), (2, 6), (3, 7), which one AND and OR turn into two
-// numbers 1024 + q (fp16) or 128 + q (bf16).
+// numbers 1024 + q (fp16) or 128 + q (bf16): a whole number in the low bits of a
+// float's fraction (Kim, Henry, Fahim, Hassan Awadalla: "Who says elephants can't run",
+// 2022, widen 4-bit weights to fp16 so).
 //
-// Bound by the widening: some 145 instructions for 16 rows by a group, half of them
-// shifts and masks of the pipe that runs at half rate, which is two thirds busy.  One
-// row by 65536 x 8192 takes 76 us (3.7 TB/s), one row of each of 128 experts of 1536 x
-// 2048 63 us (3.4 TB/s), 512 rows, Zipf over them, 57.5 us.  What did not help there:
-// deeper rings or weights straight into registers, a group ahead or not; x a group
-// ahead; one CTA per SM that walks all its tiles with x staged in shared memory (102
-// us); the zero taken off the sums instead of the codes would save a fifth of the
-// instructions, but the sums of 128 + q lose four bits.  Few rows are bound by one
-// warp's chain of instructions: 8 rows of 8 of 128 experts 8.0 us, one row by 4096 x
-// 7168 8.0 us.
+// Bound in two parts.  The widening: some 145 instructions for 16 rows by a group, half
+// of them shifts and masks of the pipe that runs at half rate, which is 66 % busy.  The
+// rest is latency: with 120 registers a quarter of the warps are resident, 58 % of the
+// issue slots are used, and what warps wait for first are global loads (x, in the loop),
+// then that pipe, then the barriers around each tile.  One row by 65536 x 8192 takes 76
+// us (3.7 TB/s), one row of each of 128 experts of 1536 x 2048 63 us (3.4 TB/s), 512
+// rows, Zipf over them, 57.2 us.  What did not help there: deeper rings or weights
+// straight into registers, a group ahead or not; x a group ahead; one CTA per SM that
+// walks all its tiles with x staged in shared memory (102 us); the zero taken off the
+// sums instead of the codes would save a fifth of the instructions, but the sums of 128 +
+// q lose four bits.  Few rows are bound by one warp's chain of instructions, near half of
+// it waits for global loads: 8 rows of 8 of 128 experts 8.1 us, one row by 4096 x 7168
+// 8.1 us.
 #include <atomic>
 #include <type_traits>
 
@@ -374,13 +379,16 @@ static moe_status_t run(const Args &a, cudaStream_t s)
 {
     const int64_t live = a.E < a.R ? a.E : a.R;
     // 32 rows of w per CTA halve the work on x, where that leaves eight CTAs for every
-    // SM: 512 rows over 128 experts 57.5 us, 74.5 with 16 rows; for 8 rows of 8 experts
-    // (2.5 CTAs per SM) 8.7 us with 32 rows, 8.0 with 16
+    // SM: 512 rows over 128 experts 57.2 us, 74.5 with 16 rows; for 8 rows of 8 experts
+    // (2.5 CTAs per SM) 8.7 us with 32 rows, 8.1 with 16
     const bool wide = live * ((a.N + 31) / 32) >= 8 * device_sm_count();
-    // Groups per warp: at K = 2048 two warps take 57.5 us for those 512 rows and four
-    // 62; one row by 4096 x 7168 takes 8.0 us with four and 11.7 with two.  Runs of up
-    // to 16 rows of x widen the weights once where an expert has that many, and cost
-    // registers where R could not fill one of 8.
+    // Groups per warp: 512 such rows take 33.0, 54.9, 65.5, 98.6 and 163.1 us with two
+    // warps at K = 1024, 2048, 2560, 4096 and 7168, and 41.0, 61.4, 71.3, 102.6 and 164.1
+    // with four; one row by 4096 x K takes 4.0, 5.5, 6.2, 10.1 and 15.9 with two and 3.5,
+    // 4.2, 4.5, 6.6 and 9.5 with four.  (So few tiles with a K just below the border lose:
+    // 9.1 us at K = 3584, 5.7 with four.)  Runs of up to 16 rows of x widen the weights
+    // once where an expert has that many, and cost registers where R could not fill one of
+    // 8.
     if (a.K >= 4096)
         return a.R <= 8 ? (wide ? launch<T, 4, 2, 1>(a, s) : launch<T, 4, 1, 1>(a, s))
                         : (wide ? launch<T, 4, 2, 2>(a, s) : launch<T, 4, 1, 2>(a, s));

@@ -19,14 +19,22 @@
 // of neighbouring lanes, so that the lowest lane that holds a maximum also holds
 // the lowest index.
 //
-// Bound by instruction issue (0.73 per cycle and scheduler), some 650 of a warp for a
-// token of 256 experts: 50 for the loads, 110 for the scores, 140 for the groups, 90
-// for the bound, 90 to collect what is above it, 160 to rank it, 100 for the weights.
-// 65536 tokens, 8 of 256 in 4 of 8 groups, bf16 with a bias: 55.1 us, where the bytes
-// take 5.6; 4096 tokens, 8 of 128, FP32: 4.8 us.  Before: k rounds of a maximum over
+// Bound by instruction issue (0.73 per cycle and scheduler), 746 of a warp for a token
+// of 256 experts (in parts, roughly: 50 for the loads, 110 for the scores, 140 for the
+// groups, 90 for the bound, 90 to collect what is above it, 160 to rank it, 100 for the
+// weights).  65536 tokens, 8 of 256 in 4 of 8 groups, bf16 with a bias: 55.2 us, where the
+// bytes take 5.6; 4096 tokens, 8 of 128, FP32: 4.8 us.  Before: k rounds of a maximum over
 // sorted lanes 100 us; candidates placed by a ballot for each of a lane's experts 74;
 // all of an undecided token in binary64 at the end 69.  Two tokens in the halves of a
 // warp, whose maxima take shuffles, gained nothing (52 us against 48 without groups).
+//
+// The time depends on the data.  What binary32 leaves open costs binary64 values, and a
+// softmax with a bias, or more than 64 candidates, the whole token anew (route_exact).
+// The same 65536 tokens in FP32, all logits equal (a router that starts at zero): 1.51 ms
+// by sigmoids, 1.35 by softmax with a bias, 1.50 without groups or bias.  The groups'
+// margin is one for all: a finite bias of -1e9 or the type's lowest value on one group
+// makes it wider than all scores, and every token's groups are settled in binary64, in
+// 0.85 ms (softmax 1.36); -inf on that group leaves them to binary32, in 61 us (95).
 #include <cfloat>
 #include <climits>
 #include <type_traits>

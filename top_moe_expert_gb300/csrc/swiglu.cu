@@ -158,9 +158,10 @@ __device__ __forceinline__ void store8(T *p, const float (&x)[8])
 }
 
 // Whole units at 16-byte accesses: a thread takes one unit after the other, each
-// `step` further.  Bound by HBM: 38400 x 2048 bf16, p = 0.3, takes 80.3 us forward
-// (5.9 TB/s) and 111.7 us backward (7.0 TB/s; a fifth of the tensors is still in the
-// L2 from call to call).  With 16 CTAs per SM rather than 64 83.3 and 117.3; with a
+// `step` further.  38400 x 2048 bf16, p = 0.3, takes 80.2 us forward (5.9 TB/s) and
+// 111.9 us backward (7.0 TB/s; a part of the tensors is still in the L2 from call to
+// call).  Backward is bound by HBM; forward, with the same generator for three fifths of
+// the bytes, by both: DRAM at 66 % of its nominal rate, 75 % of the issue slots used.  With 16 CTAs per SM rather than 64 83.3 and 117.3; with a
 // division per unit and the generator's keys formed anew 88.4 and 114.8.
 template <typename T, bool DROP, bool BWD>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const Args a)
